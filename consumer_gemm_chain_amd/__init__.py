@@ -3,7 +3,9 @@
 The compute path is the HIP library ``lib/libmlp_chain.so`` (built from
 ``csrc/`` for gfx950) behind the C ABI in ``include/mlp_chain.h``;
 ``mlp_chain`` is its ctypes binding and ``gen`` the seeded input
-generator.  Importing the package does not load the library; the first
+generator.  ``mlp_block`` binds the operators around the chain's products
+(layer norm, linear layer, the whole pre-norm block) declared in
+``include/mlp_block.h``.  Importing the package does not load the library; the first
 binding call does, and fails loudly if it has not been built.
 """
 from .mlp_chain import (  # noqa: F401
@@ -14,3 +16,4 @@ from .mlp_chain import (  # noqa: F401
     mlp_chain_debug_set_spin_limit, mlp_chain_debug_skip_producer, mlp_chain_debug_set_config,
     mlp_chain_debug_read_intermediate, mlp_chain_debug_set_split, mlp_chain_debug_set_trace,
 )
+from .mlp_block import MlpBlock, MlpLinear, MlpNorm  # noqa: F401

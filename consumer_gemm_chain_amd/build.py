@@ -27,6 +27,8 @@ ARCH = "gfx950"
 
 SOURCES = ["chain_api.cpp", "chain_dispatch.cpp", "chain_scratch.hip", "chain_litmus.hip"]
 KERNELS = "chain_kernels.hip"     # compiled once per tile configuration
+# the operators around the chain's products (include/mlp_block.h)
+BLOCK_SOURCES = ["block_api.cpp", "norm_kernels.hip", "linear_kernels.hip"]
 
 
 def num_configs() -> int:
@@ -78,11 +80,12 @@ def build(verbose: bool = False) -> str:
     kern = [(KERNELS, c, False) for c in range(num_configs())]
     chaos = [(KERNELS, c, True) for c in range(num_configs())]
     api = [(src, None, False) for src in SOURCES]
-    jobs = kern + chaos + api
+    block = [(src, None, False) for src in BLOCK_SOURCES]
+    jobs = kern + chaos + api + block
     workers = min(len(jobs), max(1, min(8, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:
         objs = dict(zip(jobs, ex.map(lambda j: _compile(j, verbose), jobs)))
-    _link([objs[j] for j in kern + api], LIB, verbose)
+    _link([objs[j] for j in kern + api + block], LIB, verbose)
     _link([objs[j] for j in chaos + api], CHAOS_LIB, verbose)
     return LIB
 

@@ -56,6 +56,11 @@ uint32_t cdiv(int64_t a, int64_t b) { return (uint32_t)((a + b - 1) / b); }
 
 }  // namespace
 
+int mlpc_set_error(int code, const char* msg) {
+    g_err = msg;
+    return code;
+}
+
 struct mlp_chain {
     int64_t M, H, I;
     int64_t ldt;                // row stride of T: I rounded up to 64 elements

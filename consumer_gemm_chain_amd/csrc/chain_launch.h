@@ -15,6 +15,10 @@ struct CfgInfo {
     int lds;              // LDS bytes of the ring per workgroup
 };
 
+// Record `msg` as the calling thread's last error (mlp_chain_last_error) and
+// return `code`.
+int mlpc_set_error(int code, const char* msg);
+
 int mlpc_num_configs();
 CfgInfo mlpc_config_info(int id);
 

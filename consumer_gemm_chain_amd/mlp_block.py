@@ -1,0 +1,270 @@
+"""Thin Python binding of the C ABI in include/mlp_block.h (ctypes): layer
+norm and the linear layer of a transformer MLP block, forward and backward,
+and the whole pre-norm block composed of them.
+
+As in the chain's binding, only argument marshalling happens here; torch
+supplies device memory and streams, and there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from .mlp_chain import ACTS, DTYPES, MLP_EINVAL, MlpChainError, _check, load_library, mlp_chain_last_error
+
+EXPORTS = ("mlp_norm_create", "mlp_norm_forward", "mlp_norm_backward", "mlp_norm_destroy",
+           "mlp_linear_create", "mlp_linear_forward", "mlp_linear_backward", "mlp_linear_destroy")
+
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = load_library()
+        vp, i64, ci, f = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+        lib.mlp_norm_create.argtypes = [i64, ci, f]
+        lib.mlp_norm_create.restype = vp
+        lib.mlp_norm_forward.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp]
+        lib.mlp_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp]
+        lib.mlp_linear_create.argtypes = [i64, i64, i64, ci, ci]
+        lib.mlp_linear_create.restype = vp
+        lib.mlp_linear_forward.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp]
+        lib.mlp_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp]
+        for name in ("mlp_norm_destroy", "mlp_linear_destroy"):
+            getattr(lib, name).argtypes = [vp]
+        for name in EXPORTS:
+            if not name.endswith("_create"):
+                getattr(lib, name).restype = ci
+        _lib = lib
+    return _lib
+
+
+# ---- the C ABI, name for name (pointers are integers, NULL is None) ------------
+
+def _created(h):
+    if not h:
+        raise MlpChainError(MLP_EINVAL, mlp_chain_last_error())
+    return h
+
+
+def mlp_norm_create(H: int, dtype: int, eps: float) -> int:
+    return _created(_library().mlp_norm_create(int(H), int(dtype), float(eps)))
+
+
+def mlp_norm_forward(h, rows, x, ldx, weight, bias, y, ldy, mean, rstd, hip_stream) -> int:
+    return _check(_library().mlp_norm_forward(h, rows, x, ldx, weight, bias, y, ldy, mean, rstd, hip_stream))
+
+
+def mlp_norm_backward(h, rows, dy, lddy, x, ldx, weight, mean, rstd, dres, lddres, dx, lddx, dweight, dbias,
+                      hip_stream) -> int:
+    return _check(_library().mlp_norm_backward(h, rows, dy, lddy, x, ldx, weight, mean, rstd, dres, lddres, dx, lddx,
+                                               dweight, dbias, hip_stream))
+
+
+def mlp_norm_destroy(h: int | None) -> int:
+    return _check(_library().mlp_norm_destroy(h))
+
+
+def mlp_linear_create(max_rows: int, K: int, N: int, act: int, dtype: int) -> int:
+    return _created(_library().mlp_linear_create(int(max_rows), int(K), int(N), int(act), int(dtype)))
+
+
+def mlp_linear_forward(h, rows, x, ldx, w, ldw, bias, residual, ldres, y, ldy, z, ldz, hip_stream) -> int:
+    return _check(_library().mlp_linear_forward(h, rows, x, ldx, w, ldw, bias, residual, ldres, y, ldy, z, ldz,
+                                                hip_stream))
+
+
+def mlp_linear_backward(h, rows, dy, lddy, x, ldx, w, ldw, z, ldz, dx, lddx, dw, lddw, db, hip_stream) -> int:
+    return _check(_library().mlp_linear_backward(h, rows, dy, lddy, x, ldx, w, ldw, z, ldz, dx, lddx, dw, lddw, db,
+                                                 hip_stream))
+
+
+def mlp_linear_destroy(h: int | None) -> int:
+    return _check(_library().mlp_linear_destroy(h))
+
+
+# ---- convenience wrappers over torch tensors ------------------------------------
+
+def _storage(dtype: str):
+    import torch
+    return torch.float16 if dtype == "f16" else torch.bfloat16
+
+
+class _Layer:
+    """Owns one handle; `_destroy` releases it."""
+    h = None
+
+    def close(self):
+        h, self.h = self.h, None
+        if h:
+            self._destroy(h)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    @staticmethod
+    def _stream(stream):
+        if stream is not None:
+            return int(getattr(stream, "cuda_stream", stream))
+        import torch
+        return torch.cuda.current_stream().cuda_stream
+
+    def _rows(self, name, t, rows, width):
+        """Pointer and row stride of a [rows, width] operand (0, 0: absent)."""
+        if t is None:
+            return None, 0
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 2 or shape[0] != rows or shape[1] != width:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected {(rows, width)}")
+        if not t.is_cuda or t.dtype != self.torch_dtype:
+            raise ValueError(f"{name} must be a {self.dtype} device tensor")
+        if width > 1 and stride[1] != 1:
+            raise ValueError(f"{name} must have contiguous rows, got strides {stride}")
+        if rows <= 1:       # the stride of a single row is never used
+            return t.data_ptr(), width
+        return t.data_ptr(), stride[0]
+
+    def _vector(self, name, t, n, dtype=None):
+        if t is None:
+            return None
+        if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} must be a contiguous vector of {n} elements, got shape {tuple(t.shape)}")
+        if not t.is_cuda or t.dtype != (dtype or self.torch_dtype):
+            raise ValueError(f"{name} must be a {dtype or self.dtype} device tensor")
+        return t.data_ptr()
+
+
+class MlpNorm(_Layer):
+    """Layer norm over rows of H elements.  Outputs are the caller's tensors;
+    work is enqueued on torch's current stream (or `stream`)."""
+
+    def __init__(self, H: int, dtype: str = "f16", eps: float = 1e-5):
+        self.H, self.dtype, self.eps = int(H), dtype, float(eps)
+        self.torch_dtype = _storage(dtype)
+        self.h = mlp_norm_create(H, DTYPES[dtype], eps)
+
+    _destroy = staticmethod(mlp_norm_destroy)
+
+    def forward(self, x, weight, bias, out, mean=None, rstd=None, stream=None):
+        """out = norm(x) weight + bias ([rows, H]); `mean` and `rstd` (float32
+        [rows]) receive the statistics the gradient needs."""
+        import torch
+        rows, f32 = x.shape[0], torch.float32
+        px, ldx = self._rows("x", x, rows, self.H)
+        py, ldy = self._rows("out", out, rows, self.H)
+        mlp_norm_forward(self.h, rows, px, ldx, self._vector("weight", weight, self.H),
+                         self._vector("bias", bias, self.H), py, ldy, self._vector("mean", mean, rows, f32),
+                         self._vector("rstd", rstd, rows, f32), self._stream(stream))
+        return out
+
+    def backward(self, dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, dres=None, stream=None):
+        """The gradients of `forward`; `dres` is added to dx."""
+        import torch
+        rows, f32 = x.shape[0], torch.float32
+        pdy, lddy = self._rows("dy", dy, rows, self.H)
+        px, ldx = self._rows("x", x, rows, self.H)
+        pr, ldr = self._rows("dres", dres, rows, self.H)
+        pdx, lddx = self._rows("dx", dx, rows, self.H)
+        mlp_norm_backward(self.h, rows, pdy, lddy, px, ldx, self._vector("weight", weight, self.H),
+                          self._vector("mean", mean, rows, f32), self._vector("rstd", rstd, rows, f32), pr, ldr, pdx,
+                          lddx, self._vector("dweight", dweight, self.H), self._vector("dbias", dbias, self.H),
+                          self._stream(stream))
+        return dx
+
+
+class MlpLinear(_Layer):
+    """Linear layer K -> N with bias, activation and residual for calls of up
+    to `rows` rows.  W is [K, gN] (g = 2 for swiglu: gate, then up)."""
+
+    def __init__(self, rows: int, K: int, N: int, act: str = "none", dtype: str = "f16"):
+        self.rows, self.K, self.N = int(rows), int(K), int(N)
+        self.act, self.dtype = act, dtype
+        self.gN = self.N * (2 if act == "swiglu" else 1)
+        self.torch_dtype = _storage(dtype)
+        self.h = mlp_linear_create(rows, K, N, ACTS[act], DTYPES[dtype])
+
+    _destroy = staticmethod(mlp_linear_destroy)
+
+    def forward(self, x, w, out, bias=None, residual=None, z=None, stream=None):
+        """out = act(x w + bias) + residual; `z` receives x w + bias."""
+        rows = x.shape[0]
+        px, ldx = self._rows("x", x, rows, self.K)
+        pw, ldw = self._rows("w", w, self.K, self.gN)
+        pr, ldr = self._rows("residual", residual, rows, self.N)
+        py, ldy = self._rows("out", out, rows, self.N)
+        pz, ldz = self._rows("z", z, rows, self.gN)
+        mlp_linear_forward(self.h, rows, px, ldx, pw, ldw, self._vector("bias", bias, self.gN), pr, ldr, py, ldy,
+                           pz, ldz, self._stream(stream))
+        return out
+
+    def backward(self, dy, x, w, dx=None, dw=None, db=None, z=None, stream=None):
+        """The gradients of `forward` that are asked for; activations need the
+        saved `z`.  The residual's gradient is dy itself."""
+        rows = dy.shape[0]
+        pdy, lddy = self._rows("dy", dy, rows, self.N)
+        px, ldx = self._rows("x", x, rows, self.K)
+        pw, ldw = self._rows("w", w, self.K, self.gN)
+        pz, ldz = self._rows("z", z, rows, self.gN)
+        pdx, lddx = self._rows("dx", dx, rows, self.K)
+        pdw, lddw = self._rows("dw", dw, self.K, self.gN)
+        pdb = self._vector("db", db, self.gN)
+        mlp_linear_backward(self.h, rows, pdy, lddy, px, ldx, pw, ldw, pz, ldz, pdx, lddx, pdw, lddw, pdb,
+                            self._stream(stream))
+        return dx, dw, db
+
+
+class MlpBlock:
+    """The pre-norm MLP block y = x + act(norm(x) W1 + b1) W2 + b2 for up to
+    `rows` rows, H wide with I inner columns: one norm and two linear layers,
+    and their gradients.  `params` maps names to tensors: weight, bias [H],
+    w1 [H, gI], b1 [gI], w2 [I, H], b2 [H]."""
+
+    def __init__(self, rows: int, H: int, I: int, act: str = "gelu_tanh", dtype: str = "f16", eps: float = 1e-5):
+        self.H, self.I, self.act, self.dtype = int(H), int(I), act, dtype
+        self.norm = MlpNorm(H, dtype, eps)
+        self.lin1 = MlpLinear(rows, H, I, act, dtype)
+        self.lin2 = MlpLinear(rows, I, H, "none", dtype)
+
+    def close(self):
+        for layer in (self.norm, self.lin1, self.lin2):
+            layer.close()
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def forward(self, x, params, save: bool = False):
+        """Returns y, and with `save` also what `backward` needs."""
+        import torch
+        rows, gI = x.shape[0], self.lin1.gN
+        n, a, y = torch.empty_like(x), x.new_empty(rows, self.I), torch.empty_like(x)
+        mean = rstd = z = None
+        if save:
+            mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
+            z = x.new_empty(rows, gI) if self.act != "none" else None
+        self.norm.forward(x, params["weight"], params["bias"], n, mean, rstd)
+        self.lin1.forward(n, params["w1"], a, bias=params["b1"], z=z)
+        self.lin2.forward(a, params["w2"], y, bias=params["b2"], residual=x)
+        return (y, (x, n, a, z, mean, rstd)) if save else y
+
+    def backward(self, dy, params, saved):
+        """dx and the gradients of every parameter, by name."""
+        import torch
+        x, n, a, z, mean, rstd = saved
+        grads = {k: torch.empty_like(v) for k, v in params.items()}
+        da, dn, dx = torch.empty_like(a), torch.empty_like(n), torch.empty_like(x)
+        self.lin2.backward(dy, a, params["w2"], dx=da, dw=grads["w2"], db=grads["b2"])
+        self.lin1.backward(da, n, params["w1"], dx=dn, dw=grads["w1"], db=grads["b1"], z=z)
+        self.norm.backward(dn, x, params["weight"], mean, rstd, dx, grads["weight"], grads["bias"], dres=dy)
+        return dx, grads

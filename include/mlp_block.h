@@ -1,0 +1,124 @@
+/*
+ * mlp_block.h -- C ABI of the operators around the two products of a
+ * transformer MLP block on MI355X (gfx950): layer norm and the linear layer
+ * (matrix product with bias, activation and residual), forward and backward.
+ * Part of the same library as mlp_chain.h; enums, error codes and
+ * mlp_chain_last_error are that header's.
+ *
+ * With R rows (tokens), all matrices row-major and every 2-d operand with a
+ * row stride of its own, in elements:
+ *
+ *   norm      mean_r = 1/H sum_c x[r,c]
+ *             rstd_r = 1 / sqrt(1/H sum_c (x[r,c] - mean_r)^2 + eps)
+ *             y[r,c] = (x[r,c] - mean_r) rstd_r weight[c] + bias[c]
+ *   its       xhat = (x - mean) rstd,  g = dy weight
+ *   gradient  dx = rstd (g - mean_c(g) - xhat mean_c(g xhat)) + dres
+ *             dweight = sum_r dy xhat,  dbias = sum_r dy
+ *
+ *   linear    h = x W + bias           (z = h, saved on request)
+ *             y = act(h) + residual
+ *             act as in mlp_chain.h; swiglu reads W [K, 2N] and bias [2N]
+ *             with the gate in columns 0..N-1 and up in N..2N-1
+ *   its       dz = dy act'(z)          ([R, gN], g = 2 for swiglu, else 1)
+ *   gradient  dx = dz W^T,  dW = x^T dz,  dbias = sum_r dz
+ *             (the residual's gradient is dy itself)
+ *
+ * Numerics: inputs and outputs are fp16 or bf16, one type per handle; mean
+ * and rstd are fp32.  Sums, statistics and accumulators are fp32 and every
+ * output is rounded once (to nearest even), with one exception: dz is
+ * rounded to the storage type before the two products of the linear
+ * gradient, whose operands the matrix cores take in 16 bits; dbias sums it
+ * unrounded.  Reductions have a fixed order: the same call gives the same
+ * bits.  NaN and infinity pass through as in the formulas.
+ *
+ * Row counts: any R >= 0 per call, up to the handle's limit.  With R = 0
+ * nothing is read and operands of R rows may be NULL; the forward passes
+ * write nothing, the gradients of weights and biases are zero.
+ *
+ * Pointers are DEVICE pointers owned by the caller.  In the linear layer
+ * they are 16-byte aligned, K and N are multiples of 8 and so are the row
+ * strides (16-byte rows).  The norm takes any H >= 1, any row stride >= H
+ * and 2-byte aligned rows; 16-byte aligned rows with H a multiple of 8 run
+ * fastest.  y may be the residual's own buffer and a norm's dx may be dres's
+ * (same row stride); no other outputs may overlap an operand.
+ *
+ * Streams, handles, errors: as in mlp_chain.h.  Every entry point but create
+ * and destroy is asynchronous on `hip_stream`, launches kernels only (it may
+ * be captured into a HIP graph) and depends on nothing from earlier calls.
+ * A handle owns its workspace, so calls on one handle that may use it (every
+ * call of a linear handle, the gradients of a norm) must be ordered on one
+ * stream; separate handles are independent.  destroy waits for the stream of
+ * the handle's last call.
+ */
+#ifndef MLP_BLOCK_H
+#define MLP_BLOCK_H
+
+#include <stdint.h>
+
+#include "mlp_chain.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct mlp_norm* mlp_norm_t;
+typedef struct mlp_linear* mlp_linear_t;
+
+/* Create a layer norm over rows of H elements (1 <= H <= 2^22) with `eps`
+ * (finite, >= 0) on the current HIP device, and allocate the workspace of
+ * its weight gradients.  Returns NULL on error with mlp_chain_last_error()
+ * set. */
+mlp_norm_t mlp_norm_create(int64_t H, int dtype, float eps);
+
+/* y = norm(x) of `rows` rows.  weight and bias have H elements of the
+ * storage type; NULL leaves out the scale or the shift.  mean and rstd
+ * (fp32, `rows` each, 4-byte aligned) are written unless NULL; the gradient
+ * needs both.  Returns MLP_EINVAL for bad pointers, sizes or strides,
+ * MLP_EHIP if a launch fails. */
+int mlp_norm_forward(mlp_norm_t h, int64_t rows, const void* x, int64_t ldx, const void* weight, const void* bias,
+                     void* y, int64_t ldy, float* mean, float* rstd, void* hip_stream);
+
+/* The gradient of mlp_norm_forward: dx from dy, x, weight (NULL: 1) and the
+ * forward's mean and rstd; dres (NULL: none) is added to dx before its one
+ * rounding -- the gradient that reaches x past the norm in a block with a
+ * residual.  dweight and dbias (H elements each) are written unless NULL. */
+int mlp_norm_backward(mlp_norm_t h, int64_t rows, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                      const void* weight, const float* mean, const float* rstd, const void* dres, int64_t lddres,
+                      void* dx, int64_t lddx, void* dweight, void* dbias, void* hip_stream);
+
+/* Release the handle and its workspace.  NULL-safe. */
+int mlp_norm_destroy(mlp_norm_t h);
+
+/* Create a linear layer K -> N for calls of up to max_rows rows, on the
+ * current HIP device.  max_rows >= 1, K and N positive multiples of 8, each
+ * below 2^22; act and dtype from the enums of mlp_chain.h.  The workspace
+ * (split-K partials, counters, dz) is allocated here.  Returns NULL on error
+ * with mlp_chain_last_error() set. */
+mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, int dtype);
+
+/* y = act(x W + bias) + residual for `rows` <= max_rows rows.  x [rows, K],
+ * W [K, gN], bias [gN] or NULL, residual [rows, N] or NULL, y [rows, N];
+ * z [rows, gN], unless NULL, receives h = x W + bias, which the gradient of
+ * an activation needs.  The strides of absent operands are ignored.  Returns
+ * MLP_EINVAL for bad pointers, sizes or strides, MLP_EHIP if a launch
+ * fails. */
+int mlp_linear_forward(mlp_linear_t h, int64_t rows, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                       const void* bias, const void* residual, int64_t ldres, void* y, int64_t ldy, void* z,
+                       int64_t ldz, void* hip_stream);
+
+/* The gradient of mlp_linear_forward: from dy [rows, N] and the saved z
+ * (required unless act is none, then ignored) any of dx [rows, K] (needs w),
+ * dw [K, gN] (needs x) and db [gN]; NULL outputs are not computed, and what
+ * only they need may be NULL too. */
+int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                        const void* w, int64_t ldw, const void* z, int64_t ldz, void* dx, int64_t lddx, void* dw,
+                        int64_t lddw, void* db, void* hip_stream);
+
+/* Release the handle and its workspace.  NULL-safe. */
+int mlp_linear_destroy(mlp_linear_t h);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MLP_BLOCK_H */
