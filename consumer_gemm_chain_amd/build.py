@@ -28,11 +28,12 @@ ARCH = "gfx950"
 SOURCES = ["chain_api.cpp", "chain_dispatch.cpp", "chain_scratch.hip", "chain_litmus.hip"]
 KERNELS = "chain_kernels.hip"     # compiled once per tile configuration
 # the operators around the chain's products (include/mlp_block.h)
-BLOCK_SOURCES = ["block_api.cpp", "norm_kernels.hip", "linear_kernels.hip"]
+BLOCK_SOURCES = ["block_api.cpp", "linear_dispatch.cpp", "norm_kernels.hip", "dz_kernels.hip"]
+LINEAR_KERNELS = "linear_kernels.hip"   # compiled once per configuration of linear_configs.h
 
 
-def num_configs() -> int:
-    text = open(os.path.join(CSRC, "chain_configs.h")).read()
+def num_configs(header: str = "chain_configs.h") -> int:
+    text = open(os.path.join(CSRC, header)).read()
     import re
     return len(re.findall(r"^\s*X\(\d+,", text, flags=re.M))
 
@@ -56,7 +57,8 @@ def _compile(job, verbose: bool) -> str:
     src, cfg, chaos = job
     tag = os.path.basename(src) + ("" if cfg is None else f".cfg{cfg}") + (".chaos" if chaos else "")
     obj = os.path.join(BUILD, tag + ".o")
-    defs = ([] if cfg is None else [f"-DMLPC_CFG={cfg}"]) + (["-DMLPC_CHAOS=1"] if chaos else [])
+    macro = "MLPC_LIN" if src == LINEAR_KERNELS else "MLPC_CFG"
+    defs = ([] if cfg is None else [f"-D{macro}={cfg}"]) + (["-DMLPC_CHAOS=1"] if chaos else [])
     cmd = [hipcc(), "-x", "hip", *FLAGS, *defs, "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -81,6 +83,7 @@ def build(verbose: bool = False) -> str:
     chaos = [(KERNELS, c, True) for c in range(num_configs())]
     api = [(src, None, False) for src in SOURCES]
     block = [(src, None, False) for src in BLOCK_SOURCES]
+    block += [(LINEAR_KERNELS, c, False) for c in range(num_configs("linear_configs.h"))]
     jobs = kern + chaos + api + block
     workers = min(len(jobs), max(1, min(8, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:

@@ -25,10 +25,17 @@ struct mlp_norm {
 struct mlp_linear {
     int64_t max_rows;
     int K, N, gN;
-    int act, dtype, device;
-    void* ws;                   // dz [max_rows, gN] (activations only) | column-sum partials
+    int act, dtype, device, cus;
+    int forced_cfg[3], forced_split[3];     // per pass; -1 / 0: the planner's
+    // workspace (one allocation): zero page | counters | dz [max_rows, gN]
+    // (activations only) | column-sum partials [max parts][gN] | split partials
+    void* ws;
+    void* zero;
+    uint32_t* cnt;
     uint16_t* dz;
-    float* part;                // [max parts][gN]
+    float* colsum;
+    float* part;
+    size_t part_bytes;
     hipStream_t last_stream;
 };
 
@@ -93,12 +100,131 @@ int check_dtype(int dtype) {
     return MLP_OK;
 }
 
+// Argument checks shared by create and plan.
+int check_linear(int64_t rows, int64_t K, int64_t N, int act) {
+    if (rows < 1 || rows > MAX_ROWS || K < 8 || N < 8 || K >= MAX_WIDTH || N >= MAX_WIDTH)
+        return fail(MLP_EINVAL, "sizes must be rows in 1..%lld, K and N in 8..%lld (got rows=%lld K=%lld N=%lld)",
+                    (long long)MAX_ROWS, (long long)(MAX_WIDTH - 8), (long long)rows, (long long)K, (long long)N);
+    if (K % 8 != 0 || N % 8 != 0)
+        return fail(MLP_EINVAL, "K and N must be multiples of 8 (16-byte rows), got K=%lld N=%lld", (long long)K,
+                    (long long)N);
+    if (act < MLP_ACT_NONE || act > MLP_ACT_SWIGLU) return fail(MLP_EINVAL, "unknown activation %d", act);
+    return MLP_OK;
+}
+
 int current_device(int* dev) {
     const hipError_t e = hipGetDevice(dev);
     return e == hipSuccess ? MLP_OK : fail(MLP_EHIP, "no HIP device: %s", hipGetErrorString(e));
 }
 
 int launched(hipError_t e) {
+    return e == hipSuccess ? MLP_OK : fail(MLP_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+}
+
+// ------------------------------------------------------------------ planner
+
+// Workspace a split product may take for its partials, and the parts a
+// reduction may have.
+constexpr size_t MAX_PART_BYTES = (size_t)64 << 20;
+constexpr uint32_t MAX_SPLIT = 32;
+constexpr uint32_t MAX_COUNTERS = (uint32_t)(MAX_PART_BYTES / (2 * 16 * 128 * 4));   // of the smallest tile, split in two
+
+struct Plan {
+    int cfg;
+    uint32_t Mt, Nt, S, ksp;
+    size_t part_bytes;
+};
+
+// The plan of a product of M x N columns (both halves of swiglu's B) over K
+// with configuration cfg and at most `split` parts (no part is empty).
+Plan make_plan(int cfg, int64_t M, int64_t N, int64_t K, uint32_t split) {
+    const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
+    const uint32_t slabs = (uint32_t)(K / mlpc::BK);
+    Plan p;
+    p.cfg = cfg;
+    p.Mt = (uint32_t)((M + c.BM - 1) / c.BM);
+    p.Nt = (uint32_t)((N + c.BN - 1) / c.BN);
+    if (split > slabs) split = slabs;
+    if (split < 1) split = 1;
+    p.ksp = slabs ? (slabs + split - 1) / split : 0;
+    p.S = slabs ? (slabs + p.ksp - 1) / p.ksp : 1;
+    p.part_bytes = p.S > 1 ? (size_t)p.Mt * p.Nt * p.S * c.BM * c.BN * 4 : 0;
+    return p;
+}
+
+bool plan_fits(const Plan& p) { return p.part_bytes <= MAX_PART_BYTES; }
+
+// Estimated microseconds of a plan.
+double plan_cost(const Plan& p, int64_t M, int64_t N, int64_t K, int pass, int cus) {
+    (void)M; (void)N; (void)K; (void)pass;
+    const double slab[5] = {0.6, 0.55, 0.75, 1.1, 1.95};
+    const uint32_t per_cu[5] = {2, 2, 1, 1, 1};
+    const double slots = (double)per_cu[p.cfg] * cus, parts = (double)p.Mt * p.Nt * p.S;
+    const double rounds = (double)(uint64_t)((parts + slots - 1) / slots);
+    return rounds * (2.0 + p.ksp * slab[p.cfg]) + (p.S > 1 ? 4.0 : 0.0);
+}
+
+Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {
+    Plan best{};
+    double cost = 0.0;
+    bool found = false;
+    for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
+        if (!mlpc_linear_has(cfg, pass)) continue;
+        uint32_t last = 0;
+        for (uint32_t split = 1; split <= MAX_SPLIT; ++split) {
+            const Plan p = make_plan(cfg, M, N, K, split);
+            if (p.S == last) continue;
+            last = p.S;
+            if (!plan_fits(p)) break;
+            const double c = plan_cost(p, M, N, K, pass, cus);
+            if (!found || c < cost) {
+                best = p;
+                cost = c;
+                found = true;
+            }
+        }
+    }
+    return best;
+}
+
+// Rows, columns and reduction of a pass.
+void pass_sizes(int pass, int64_t rows, int64_t K, int64_t gN, int64_t* m, int64_t* n, int64_t* k) {
+    *m = pass == mlpc::PASS_DW ? K : rows;
+    *n = pass == mlpc::PASS_DX ? K : gN;
+    *k = pass == mlpc::PASS_FWD ? K : pass == mlpc::PASS_DX ? gN : rows;
+}
+
+// Largest split workspace of any plan for up to max_rows rows.
+size_t max_part_bytes(int64_t max_rows, int64_t K, int64_t gN) {
+    size_t most = 0;
+    for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg)
+        for (int pass = 0; pass < 3; ++pass) {
+            if (!mlpc_linear_has(cfg, pass)) continue;
+            int64_t m, n, k;
+            pass_sizes(pass, max_rows, K, gN, &m, &n, &k);
+            const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
+            const size_t tiles = (size_t)((m + c.BM - 1) / c.BM) * (size_t)((n + c.BN - 1) / c.BN);
+            const size_t slabs = (size_t)(k / mlpc::BK);
+            const size_t b = tiles * (slabs < MAX_SPLIT ? slabs : MAX_SPLIT) * c.BM * c.BN * 4;
+            if (slabs > 1 && b > most) most = b;
+        }
+    return most < MAX_PART_BYTES ? most : MAX_PART_BYTES;
+}
+
+int run_product(mlp_linear* h, int pass, mlpc::GemmArgs& a, hipStream_t s) {
+    const int64_t n = a.up ? (int64_t)a.N + a.up : a.N;
+    const Plan p = h->forced_cfg[pass] < 0 ? choose_plan(a.M, n, a.K, pass, h->cus)
+                                           : make_plan(h->forced_cfg[pass], a.M, n, a.K, (uint32_t)h->forced_split[pass]);
+    if (p.part_bytes > h->part_bytes)
+        return fail(MLP_EINVAL, "the split needs %zu workspace bytes of %zu", p.part_bytes, h->part_bytes);
+    a.Mt = p.Mt;
+    a.Nt = p.Nt;
+    a.S = p.S;
+    a.ksp = p.ksp;
+    a.part = h->part;
+    a.cnt = h->cnt;
+    a.zero = h->zero;
+    const hipError_t e = mlpc_gemm(a, p.cfg, pass, h->dtype, s);
     return e == hipSuccess ? MLP_OK : fail(MLP_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
 }
 
@@ -226,19 +352,7 @@ int mlp_norm_destroy(mlp_norm_t h) {
 }
 
 mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, int dtype) {
-    if (max_rows < 1 || max_rows > MAX_ROWS || K < 8 || N < 8 || K >= MAX_WIDTH || N >= MAX_WIDTH) {
-        fail(MLP_EINVAL, "sizes must be max_rows in 1..%lld, K and N in 8..%lld (got max_rows=%lld K=%lld N=%lld)",
-             (long long)MAX_ROWS, (long long)(MAX_WIDTH - 8), (long long)max_rows, (long long)K, (long long)N);
-        return nullptr;
-    }
-    if (K % 8 != 0 || N % 8 != 0) {
-        fail(MLP_EINVAL, "K and N must be multiples of 8 (16-byte rows), got K=%lld N=%lld", (long long)K, (long long)N);
-        return nullptr;
-    }
-    if (act < MLP_ACT_NONE || act > MLP_ACT_SWIGLU) {
-        fail(MLP_EINVAL, "unknown activation %d", act);
-        return nullptr;
-    }
+    if (check_linear(max_rows, K, N, act) != MLP_OK) return nullptr;
     if (check_dtype(dtype) != MLP_OK) return nullptr;
     int dev = 0;
     if (current_device(&dev) != MLP_OK) return nullptr;
@@ -254,17 +368,44 @@ mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, 
     h->act = act;
     h->dtype = dtype;
     h->device = dev;
-    const size_t dz_b = act == MLP_ACT_NONE ? 0 : align_up((size_t)max_rows * h->gN * 2, 256);
-    const size_t part_b = align_up((size_t)mlpc_dz_max_parts() * h->gN * sizeof(float), 256);
-    const hipError_t e = hipMalloc(&h->ws, dz_b + part_b);
+    for (int i = 0; i < 3; ++i) {
+        h->forced_cfg[i] = -1;
+        h->forced_split[i] = 0;
+    }
+    hipError_t e = hipDeviceGetAttribute(&h->cus, hipDeviceAttributeMultiprocessorCount, dev);
     if (e != hipSuccess) {
-        fail(MLP_ENOMEM, "hipMalloc of %zu workspace bytes failed: %s", dz_b + part_b, hipGetErrorString(e));
+        fail(MLP_EHIP, "hipDeviceGetAttribute failed: %s", hipGetErrorString(e));
+        delete h;
+        return nullptr;
+    }
+    const size_t sync_b = 256 + align_up(MAX_COUNTERS * sizeof(uint32_t), 256);
+    const size_t dz_b = act == MLP_ACT_NONE ? 0 : align_up((size_t)max_rows * h->gN * 2, 256);
+    const size_t col_b = align_up((size_t)mlpc_dz_max_parts() * h->gN * sizeof(float), 256);
+    h->part_bytes = max_part_bytes(max_rows, K, h->gN);
+    const size_t bytes = sync_b + dz_b + col_b + h->part_bytes;
+    e = hipMalloc(&h->ws, bytes);
+    if (e != hipSuccess) {
+        fail(MLP_ENOMEM, "hipMalloc of %zu workspace bytes failed: %s", bytes, hipGetErrorString(e));
         delete h;
         return nullptr;
     }
     char* p = static_cast<char*>(h->ws);
+    h->zero = p;
+    h->cnt = reinterpret_cast<uint32_t*>(p + 256);
+    p += sync_b;
     h->dz = dz_b ? reinterpret_cast<uint16_t*>(p) : nullptr;
-    h->part = reinterpret_cast<float*>(p + dz_b);
+    p += dz_b;
+    h->colsum = reinterpret_cast<float*>(p);
+    p += col_b;
+    h->part = h->part_bytes ? reinterpret_cast<float*>(p) : nullptr;
+    e = hipMemset(h->ws, 0, sync_b);
+    if (e == hipSuccess) e = hipStreamSynchronize(nullptr);
+    if (e != hipSuccess) {
+        fail(MLP_EHIP, "clearing the workspace failed: %s", hipGetErrorString(e));
+        (void)hipFree(h->ws);
+        delete h;
+        return nullptr;
+    }
     return h;
 }
 
@@ -303,7 +444,7 @@ int mlp_linear_forward(mlp_linear_t h, int64_t rows, const void* x, int64_t ldx,
     a.z = static_cast<uint16_t*>(z);
     a.ldr = ldres;
     a.ldz = ldz;
-    return launched(mlpc_gemm(a, mlpc::PASS_FWD, h->dtype, s));
+    return run_product(h, mlpc::PASS_FWD, a, s);
 }
 
 int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t lddy, const void* x, int64_t ldx,
@@ -333,7 +474,7 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
         d.z = static_cast<const uint16_t*>(z);
         d.dz = h->dz;
         d.db = static_cast<uint16_t*>(db);
-        d.part = h->part;
+        d.part = h->colsum;
         d.lddy = lddy;
         d.ldz = ldz;
         d.lddz = h->gN;
@@ -359,7 +500,7 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
         a.M = (int)rows;
         a.N = h->K;
         a.K = h->gN;
-        rc = launched(mlpc_gemm(a, mlpc::PASS_DX, h->dtype, s));
+        rc = run_product(h, mlpc::PASS_DX, a, s);
         if (rc != MLP_OK) return rc;
     }
     if (dw) {
@@ -373,8 +514,34 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
         a.M = h->K;
         a.N = h->gN;
         a.K = (int)rows;
-        return launched(mlpc_gemm(a, mlpc::PASS_DW, h->dtype, s));
+        return run_product(h, mlpc::PASS_DW, a, s);
     }
+    return MLP_OK;
+}
+
+int mlp_linear_plan(int64_t rows, int64_t K, int64_t N, int act, int pass, int cus, int64_t* plan, int n) {
+    if (!plan || n < 3) return fail(MLP_EINVAL, "mlp_linear_plan needs an array of at least 3 slots");
+    if (check_linear(rows, K, N, act) != MLP_OK) return MLP_EINVAL;
+    if (pass < mlpc::PASS_FWD || pass > mlpc::PASS_DW) return fail(MLP_EINVAL, "unknown pass %d", pass);
+    if (cus < 8) return fail(MLP_EINVAL, "cus must be >= 8, got %d", cus);
+    int64_t m, nn, k;
+    pass_sizes(pass, rows, K, act == MLP_ACT_SWIGLU ? 2 * N : N, &m, &nn, &k);
+    const Plan p = choose_plan(m, nn, k, pass, cus);
+    const mlpc::LinearCfgInfo c = mlpc_linear_config(p.cfg);
+    const int64_t v[8] = {p.cfg, p.S, c.BM, c.BN, p.Mt, p.Nt, p.ksp, (int64_t)p.part_bytes};
+    for (int i = 0; i < n && i < 8; ++i) plan[i] = v[i];
+    return MLP_OK;
+}
+
+int mlp_linear_debug_set_plan(mlp_linear_t h, int pass, int config_id, int split) {
+    if (!h) return fail(MLP_EINVAL, "NULL handle");
+    if (pass < mlpc::PASS_FWD || pass > mlpc::PASS_DW) return fail(MLP_EINVAL, "unknown pass %d", pass);
+    if (config_id < -1 || config_id >= mlpc_linear_num_configs() || (config_id >= 0 && !mlpc_linear_has(config_id, pass)))
+        return fail(MLP_EINVAL, "pass %d has no tile configuration %d", pass, config_id);
+    if (split < 0 || split > (int)MAX_SPLIT || (config_id < 0 && split != 0))
+        return fail(MLP_EINVAL, "a configuration's split must be in 0..%u, got %d", MAX_SPLIT, split);
+    h->forced_cfg[pass] = config_id;
+    h->forced_split[pass] = split;
     return MLP_OK;
 }
 

@@ -45,6 +45,15 @@ struct GemmArgs {
     const uint16_t* res;        // nullptr: none
     uint16_t* z;                // nullptr: not saved
     int64_t ldr, ldz;
+    // plan: tiles, parts of each tile's reduction and slabs per part
+    uint32_t Mt, Nt, S, ksp;
+    float* part;                // [Mt * Nt][S][tile accumulators] (S > 1)
+    uint32_t* cnt;              // [Mt * Nt] parts counted in (S > 1), zero between launches
+    const void* zero;           // 16 zero bytes
+};
+
+struct LinearCfgInfo {
+    int BM, BN, NT, lds;
 };
 
 // dz = dy act'(z), and the column sums of dz.
@@ -69,7 +78,12 @@ hipError_t mlpc_norm_backward(const mlpc::NormArgs& a, int dtype, hipStream_t s)
 int mlpc_norm_parts(int64_t rows);
 int mlpc_norm_max_parts();
 
-hipError_t mlpc_gemm(const mlpc::GemmArgs& a, int pass, int dtype, hipStream_t s);
+// Tile configurations (linear_configs.h): their number, sizes, whether a pass
+// has them, and one launch.
+int mlpc_linear_num_configs();
+mlpc::LinearCfgInfo mlpc_linear_config(int cfg);
+bool mlpc_linear_has(int cfg, int pass);
+hipError_t mlpc_gemm(const mlpc::GemmArgs& a, int cfg, int pass, int dtype, hipStream_t s);
 hipError_t mlpc_dz(const mlpc::DzArgs& a, int dtype, hipStream_t s);
 int mlpc_dz_parts(int64_t rows);
 int mlpc_dz_max_parts();

@@ -12,7 +12,10 @@ import ctypes
 from .mlp_chain import ACTS, DTYPES, MLP_EINVAL, MlpChainError, _check, load_library, mlp_chain_last_error
 
 EXPORTS = ("mlp_norm_create", "mlp_norm_forward", "mlp_norm_backward", "mlp_norm_destroy",
-           "mlp_linear_create", "mlp_linear_forward", "mlp_linear_backward", "mlp_linear_destroy")
+           "mlp_linear_create", "mlp_linear_forward", "mlp_linear_backward", "mlp_linear_destroy",
+           "mlp_linear_plan", "mlp_linear_debug_set_plan")
+
+PLAN_FIELDS = ("config", "S", "BM", "BN", "Mt", "Nt", "ksp", "part_bytes")
 
 _lib = None
 
@@ -30,6 +33,8 @@ def _library():
         lib.mlp_linear_create.restype = vp
         lib.mlp_linear_forward.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp]
         lib.mlp_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp]
+        lib.mlp_linear_plan.argtypes = [i64, i64, i64, ci, ci, ci, ctypes.POINTER(i64), ci]
+        lib.mlp_linear_debug_set_plan.argtypes = [vp, ci, ci, ci]
         for name in ("mlp_norm_destroy", "mlp_linear_destroy"):
             getattr(lib, name).argtypes = [vp]
         for name in EXPORTS:
@@ -81,6 +86,17 @@ def mlp_linear_backward(h, rows, dy, lddy, x, ldx, w, ldw, z, ldz, dx, lddx, dw,
 
 def mlp_linear_destroy(h: int | None) -> int:
     return _check(_library().mlp_linear_destroy(h))
+
+
+def mlp_linear_plan(rows: int, K: int, N: int, act: int, op: int, cus: int) -> dict:
+    """The plan of pass `op` (0: x W, 1: dz W^T, 2: x^T dz) on a GPU with `cus` CUs (host only)."""
+    arr = (ctypes.c_int64 * len(PLAN_FIELDS))()
+    _check(_library().mlp_linear_plan(int(rows), int(K), int(N), int(act), int(op), int(cus), arr, len(PLAN_FIELDS)))
+    return dict(zip(PLAN_FIELDS, (int(v) for v in arr)))
+
+
+def mlp_linear_debug_set_plan(h: int, op: int, config_id: int, split: int) -> int:
+    return _check(_library().mlp_linear_debug_set_plan(h, int(op), int(config_id), int(split)))
 
 
 # ---- convenience wrappers over torch tensors ------------------------------------

@@ -117,6 +117,23 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
 /* Release the handle and its workspace.  NULL-safe. */
 int mlp_linear_destroy(mlp_linear_t h);
 
+/* The plan a call of `rows` rows makes on a GPU with `cus` compute units for
+ * pass 0 (x W), 1 (dz W^T) or 2 (x^T dz), computed on the host alone: fills
+ * the first min(n, 8) of
+ *   { config id, parts of the reduction, BM, BN, tile rows, tile columns,
+ *     64-deep slabs per part, workspace bytes of the partials }.
+ * Returns MLP_EINVAL for sizes mlp_linear_create would reject, an unknown
+ * pass, cus < 8, a NULL array or n < 3. */
+int mlp_linear_plan(int64_t rows, int64_t K, int64_t N, int act, int pass, int cus, int64_t* plan, int n);
+
+/* Test and measurement hook: run `pass` of the handle's later calls with tile
+ * configuration `config_id` and its reduction in at most `split` parts (0 or
+ * 1: one); config_id -1 and split 0 restore the planner's choice.  A call
+ * whose partials exceed the handle's workspace is then refused.  Returns
+ * MLP_EINVAL for a NULL handle, a configuration the pass does not have or a
+ * split outside 0..32. */
+int mlp_linear_debug_set_plan(mlp_linear_t h, int pass, int config_id, int split);
+
 #ifdef __cplusplus
 }
 #endif
