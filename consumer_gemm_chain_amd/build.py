@@ -28,7 +28,8 @@ ARCH = "gfx950"
 SOURCES = ["chain_api.cpp", "chain_dispatch.cpp", "chain_scratch.hip", "chain_litmus.hip"]
 KERNELS = "chain_kernels.hip"     # compiled once per tile configuration
 # the operators around the chain's products (include/mlp_block.h)
-BLOCK_SOURCES = ["block_api.cpp", "linear_dispatch.cpp", "norm_kernels.hip", "dz_kernels.hip"]
+BLOCK_SOURCES = ["block_api.cpp", "linear_dispatch.cpp", "linear_reduce.hip", "norm_kernels.hip",
+                 "dz_kernels.hip"]
 LINEAR_KERNELS = "linear_kernels.hip"   # compiled once per configuration of linear_configs.h
 
 

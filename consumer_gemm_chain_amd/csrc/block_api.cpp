@@ -27,11 +27,10 @@ struct mlp_linear {
     int K, N, gN;
     int act, dtype, device, cus;
     int forced_cfg[3], forced_split[3];     // per pass; -1 / 0: the planner's
-    // workspace (one allocation): zero page | counters | dz [max_rows, gN]
-    // (activations only) | column-sum partials [max parts][gN] | split partials
+    // workspace (one allocation): zero page | dz [max_rows, gN] (activations
+    // only) | column-sum partials [max parts][gN] | split partials
     void* ws;
     void* zero;
-    uint32_t* cnt;
     uint16_t* dz;
     float* colsum;
     float* part;
@@ -127,7 +126,6 @@ int launched(hipError_t e) {
 // reduction may have.
 constexpr size_t MAX_PART_BYTES = (size_t)64 << 20;
 constexpr uint32_t MAX_SPLIT = 32;
-constexpr uint32_t MAX_COUNTERS = (uint32_t)(MAX_PART_BYTES / (2 * 16 * 128 * 4));   // of the smallest tile, split in two
 
 struct Plan {
     int cfg;
@@ -148,20 +146,32 @@ Plan make_plan(int cfg, int64_t M, int64_t N, int64_t K, uint32_t split) {
     if (split < 1) split = 1;
     p.ksp = slabs ? (slabs + split - 1) / split : 0;
     p.S = slabs ? (slabs + p.ksp - 1) / p.ksp : 1;
-    p.part_bytes = p.S > 1 ? (size_t)p.Mt * p.Nt * p.S * c.BM * c.BN * 4 : 0;
+    p.part_bytes = p.S > 1 ? (size_t)M * N * p.S * 4 : 0;
     return p;
 }
 
 bool plan_fits(const Plan& p) { return p.part_bytes <= MAX_PART_BYTES; }
 
-// Estimated microseconds of a plan.
-double plan_cost(const Plan& p, int64_t M, int64_t N, int64_t K, int pass, int cus) {
-    (void)M; (void)N; (void)K; (void)pass;
-    const double slab[5] = {0.6, 0.55, 0.75, 1.1, 1.95};
-    const uint32_t per_cu[5] = {2, 2, 1, 1, 1};
-    const double slots = (double)per_cu[p.cfg] * cus, parts = (double)p.Mt * p.Nt * p.S;
-    const double rounds = (double)(uint64_t)((parts + slots - 1) / slots);
-    return rounds * (2.0 + p.ksp * slab[p.cfg]) + (p.S > 1 ? 4.0 : 0.0);
+// Estimated microseconds of a plan, from sweeps of every configuration and
+// split over the package's sizes.  A workgroup takes `slab` microseconds per
+// 64-deep slab with the chip busy (16 x 128 and 64 x 128 tiles: two on a CU
+// take less each than one alone) and `fixed` for its prologue and epilogue.
+// Where operands come from memory, the workgroups running at once share
+// about 5 TB/s.  A split adds a launch and the partials' way out and back.
+double plan_cost(const Plan& p, int64_t M, int64_t N, int cus) {
+    static const double slab[] = {0.37, 0.40, 0.57, 0.93, 1.52}, fixed[] = {2.0, 2.0, 2.5, 3.0, 4.5};
+    const mlpc::LinearCfgInfo c = mlpc_linear_config(p.cfg);
+    const double parts = (double)p.Mt * p.Nt * p.S;
+    const double rounds = ceil(parts / cus), active = parts < cus ? parts : cus;
+    // bytes per slab that are not another running workgroup's too
+    const double bytes = 128.0 * ((double)c.BN / p.Mt + (double)c.BM / p.Nt);
+    double t = slab[p.cfg];
+    if (p.cfg <= 1 && rounds < 2) t *= 1.3;
+    const double mem = bytes * active / 5.0e6;
+    if (mem > t) t = mem;
+    double cost = rounds * (fixed[p.cfg] + p.ksp * t);
+    if (p.S > 1) cost += 4.0 + (double)M * N * 4 * p.S * 2 / 4.0e6;
+    return cost;
 }
 
 Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {
@@ -176,7 +186,7 @@ Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {
             if (p.S == last) continue;
             last = p.S;
             if (!plan_fits(p)) break;
-            const double c = plan_cost(p, M, N, K, pass, cus);
+            const double c = plan_cost(p, M, N, cus);
             if (!found || c < cost) {
                 best = p;
                 cost = c;
@@ -197,17 +207,13 @@ void pass_sizes(int pass, int64_t rows, int64_t K, int64_t gN, int64_t* m, int64
 // Largest split workspace of any plan for up to max_rows rows.
 size_t max_part_bytes(int64_t max_rows, int64_t K, int64_t gN) {
     size_t most = 0;
-    for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg)
-        for (int pass = 0; pass < 3; ++pass) {
-            if (!mlpc_linear_has(cfg, pass)) continue;
-            int64_t m, n, k;
-            pass_sizes(pass, max_rows, K, gN, &m, &n, &k);
-            const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
-            const size_t tiles = (size_t)((m + c.BM - 1) / c.BM) * (size_t)((n + c.BN - 1) / c.BN);
-            const size_t slabs = (size_t)(k / mlpc::BK);
-            const size_t b = tiles * (slabs < MAX_SPLIT ? slabs : MAX_SPLIT) * c.BM * c.BN * 4;
-            if (slabs > 1 && b > most) most = b;
-        }
+    for (int pass = 0; pass < 3; ++pass) {
+        int64_t m, n, k;
+        pass_sizes(pass, max_rows, K, gN, &m, &n, &k);
+        const size_t slabs = (size_t)(k / mlpc::BK);
+        const size_t b = slabs > 1 ? (size_t)m * n * 4 * (slabs < MAX_SPLIT ? slabs : MAX_SPLIT) : 0;
+        if (b > most) most = b;
+    }
     return most < MAX_PART_BYTES ? most : MAX_PART_BYTES;
 }
 
@@ -222,9 +228,9 @@ int run_product(mlp_linear* h, int pass, mlpc::GemmArgs& a, hipStream_t s) {
     a.S = p.S;
     a.ksp = p.ksp;
     a.part = h->part;
-    a.cnt = h->cnt;
     a.zero = h->zero;
-    const hipError_t e = mlpc_gemm(a, p.cfg, pass, h->dtype, s);
+    hipError_t e = mlpc_gemm(a, p.cfg, pass, h->dtype, s);
+    if (e == hipSuccess && p.S > 1) e = mlpc_gemm_reduce(a, h->dtype, s);
     return e == hipSuccess ? MLP_OK : fail(MLP_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
 }
 
@@ -378,11 +384,11 @@ mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, 
         delete h;
         return nullptr;
     }
-    const size_t sync_b = 256 + align_up(MAX_COUNTERS * sizeof(uint32_t), 256);
+    const size_t zero_b = 256;
     const size_t dz_b = act == MLP_ACT_NONE ? 0 : align_up((size_t)max_rows * h->gN * 2, 256);
     const size_t col_b = align_up((size_t)mlpc_dz_max_parts() * h->gN * sizeof(float), 256);
     h->part_bytes = max_part_bytes(max_rows, K, h->gN);
-    const size_t bytes = sync_b + dz_b + col_b + h->part_bytes;
+    const size_t bytes = zero_b + dz_b + col_b + h->part_bytes;
     e = hipMalloc(&h->ws, bytes);
     if (e != hipSuccess) {
         fail(MLP_ENOMEM, "hipMalloc of %zu workspace bytes failed: %s", bytes, hipGetErrorString(e));
@@ -391,14 +397,13 @@ mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, 
     }
     char* p = static_cast<char*>(h->ws);
     h->zero = p;
-    h->cnt = reinterpret_cast<uint32_t*>(p + 256);
-    p += sync_b;
+    p += zero_b;
     h->dz = dz_b ? reinterpret_cast<uint16_t*>(p) : nullptr;
     p += dz_b;
     h->colsum = reinterpret_cast<float*>(p);
     p += col_b;
     h->part = h->part_bytes ? reinterpret_cast<float*>(p) : nullptr;
-    e = hipMemset(h->ws, 0, sync_b);
+    e = hipMemset(h->ws, 0, zero_b);
     if (e == hipSuccess) e = hipStreamSynchronize(nullptr);
     if (e != hipSuccess) {
         fail(MLP_EHIP, "clearing the workspace failed: %s", hipGetErrorString(e));

@@ -47,8 +47,7 @@ struct GemmArgs {
     int64_t ldr, ldz;
     // plan: tiles, parts of each tile's reduction and slabs per part
     uint32_t Mt, Nt, S, ksp;
-    float* part;                // [Mt * Nt][S][tile accumulators] (S > 1)
-    uint32_t* cnt;              // [Mt * Nt] parts counted in (S > 1), zero between launches
+    float* part;                // [S][M][columns] (S > 1)
     const void* zero;           // 16 zero bytes
 };
 
@@ -84,6 +83,8 @@ int mlpc_linear_num_configs();
 mlpc::LinearCfgInfo mlpc_linear_config(int cfg);
 bool mlpc_linear_has(int cfg, int pass);
 hipError_t mlpc_gemm(const mlpc::GemmArgs& a, int cfg, int pass, int dtype, hipStream_t s);
+// Sum the parts of a split product and finish its outputs (linear_reduce.hip).
+hipError_t mlpc_gemm_reduce(const mlpc::GemmArgs& a, int dtype, hipStream_t s);
 hipError_t mlpc_dz(const mlpc::DzArgs& a, int dtype, hipStream_t s);
 int mlpc_dz_parts(int64_t rows);
 int mlpc_dz_max_parts();

@@ -321,6 +321,38 @@ __device__ __forceinline__ void pair8(const f32x4& x, const f32x4& y, float (&v)
     }
 }
 
+// Eight columns n .. n+7 of row r: v + bias (gate; u and bu: up) to z, the
+// activation, the residual, one rounding and the store.
+template <int DT>
+__device__ __forceinline__ void finish8(const GemmArgs& p, int64_t r, int n, float (&v)[8], float (&u)[8],
+                                        const float (&b)[8], const float (&bu)[8], u32x4 res) {
+    const bool gated = p.act == ACT_SWIGLU;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
+    if (gated) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] += bu[i];
+    }
+    if (p.z) {
+        st16(p.z + (size_t)r * p.ldz + n, narrow8<DT>(v));
+        if (gated) st16(p.z + (size_t)r * p.ldz + p.up + n, narrow8<DT>(u));
+    }
+    if (gated) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = silu(v[i]) * u[i];
+    } else if (p.act == ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = gelu_tanh(v[i]);
+    }
+    if (p.res) {
+        float t[8];
+        widen8<DT>(res, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += t[i];
+    }
+    st16(p.d + (size_t)r * p.ldd + n, narrow8<DT>(v));
+}
+
 // bias, activation, residual, rounding and stores of a tile's accumulators.
 template <class C, int DT, int PASS>
 __device__ __forceinline__ void linear_epilogue(const f32x4 (&acc)[C::FM][C::FN], const GemmArgs& p, int m0, int n0) {
@@ -345,23 +377,7 @@ __device__ __forceinline__ void linear_epilogue(const f32x4 (&acc)[C::FM][C::FN]
                 pair8(acc[f][4 * Q], acc[f][4 * Q + 2], vg);
                 pair8(acc[f][4 * Q + 1], acc[f][4 * Q + 3], vu);
                 if (!in || r >= p.M) continue;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    vg[i] += bg[i];
-                    vu[i] += bu[i];
-                }
-                if (p.z) {
-                    st16(p.z + (size_t)r * p.ldz + n, narrow8<DT>(vg));
-                    st16(p.z + (size_t)r * p.ldz + p.up + n, narrow8<DT>(vu));
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) vg[i] = silu(vg[i]) * vu[i];
-                if (p.res) {
-                    widen8<DT>(ld16(p.res + (size_t)r * p.ldr + n), vu);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) vg[i] += vu[i];
-                }
-                st16(p.d + (size_t)r * p.ldd + n, narrow8<DT>(vg));
+                finish8<DT>(p, r, n, vg, vu, bg, bu, p.res ? ld16(p.res + (size_t)r * p.ldr + n) : u32x4{});
             }
         });
         return;
@@ -388,84 +404,34 @@ __device__ __forceinline__ void linear_epilogue(const f32x4 (&acc)[C::FM][C::FN]
             pair8(acc[f][2 * Q], acc[f][2 * Q + 1], v);
             if (!in || r >= p.M) continue;
             if constexpr (PASS == PASS_FWD) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] += b[i];
-                if (p.z) st16(p.z + (size_t)r * p.ldz + n, narrow8<DT>(v));
-                if (p.act == ACT_GELU_TANH) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = gelu_tanh(v[i]);
-                }
-                if (p.res) {
-                    float t[8];
-                    widen8<DT>(res[f], t);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] += t[i];
-                }
+                float none[8] = {};
+                finish8<DT>(p, r, n, v, none, b, none, res[f]);
+            } else {
+                st16(p.d + (size_t)r * p.ldd + n, narrow8<DT>(v));
             }
-            st16(p.d + (size_t)r * p.ldd + n, narrow8<DT>(v));
         }
     });
 }
 
-// Split reduction: every part stores the fp32 accumulators of its rows and
-// counts in at agent scope; the part that counts in last sets the counter
-// back to zero (so the next launch starts from zero) and adds all parts in
-// part order, whichever part it is, so the bits do not depend on the
-// schedule.  No part waits for another.  Returns true in the last part.
-// Slots are ordered by (fragment, wave, row, column group): the valid rows of
-// a short tile are whole 64-byte pieces.
+// A part's fp32 accumulators to its plane of the partials [S][M][gN] (swiglu:
+// gate and up columns where W has them).
 template <class C>
-__device__ __forceinline__ bool linear_reduce(f32x4 (&acc)[C::FM][C::FN], const GemmArgs& p, int m0, uint32_t tile,
-                                              uint32_t s) {
-    __shared__ uint32_t s_last;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int m = m0 + wave / C::WN * C::WTM + (lane & 15);
-    f32x4* base = reinterpret_cast<f32x4*>(p.part) + (size_t)tile * p.S * C::NF * C::NT + wave * 64 + (lane & 15) * 4 + (lane >> 4);
+__device__ __forceinline__ void store_part(const f32x4 (&acc)[C::FM][C::FN], const GemmArgs& p, int m0, int n0,
+                                           uint32_t s) {
+    const int lane = threadIdx.x & 63, wave = uniform_wave();
+    const int g = lane >> 4, m = m0 + wave / C::WN * C::WTM + (lane & 15);
+    const int64_t ld = p.N + p.up;
+    float* part = p.part + (size_t)s * p.M * ld;
 #pragma unroll
-    for (int f = 0; f < C::FM; ++f)
-        if (m + f * 16 < p.M) {
+    for (int f = 0; f < C::FN; ++f) {
+        const int frag = wave % C::WN * C::FN + f;
+        const int n = (p.up ? n0 + (frag >> 1) * 16 : n0 + frag * 16) + g * 4;
+        if (n >= p.N) continue;
 #pragma unroll
-            for (int n = 0; n < C::FN; ++n) base[((size_t)s * C::NF + f * C::FN + n) * C::NT] = acc[f][n];
-        }
-    // every thread's partial happens before thread 0's agent-scope release
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const uint32_t old = __hip_atomic_fetch_add(p.cnt + tile, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        if (old + 1 == p.S) __hip_atomic_store(p.cnt + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = old + 1 == p.S;
+        for (int i = 0; i < C::FM; ++i)
+            if (m + i * 16 < p.M)
+                *reinterpret_cast<f32x4*>(part + (size_t)(m + i * 16) * ld + n + (p.up ? (frag & 1) * p.up : 0)) = acc[i][f];
     }
-    __syncthreads();
-    if (__builtin_amdgcn_readfirstlane(s_last) == 0) return false;
-    constexpr int GR = C::FM < 8 / C::FN ? C::FM : 8 / C::FN;       // fragment rows at a time
-    constexpr int PB = 16 / (GR * C::FN);                           // parts loaded at once
-    static_for<0, C::FM / GR>([&](auto gr) {
-        constexpr int F0 = decltype(gr)::value * GR;
-        f32x4 sum[GR][C::FN] = {};
-        for (uint32_t p0 = 0; p0 < p.S; p0 += PB) {
-            f32x4 v[PB][GR][C::FN] = {};
-#pragma unroll
-            for (int b = 0; b < PB; ++b)
-#pragma unroll
-                for (int r = 0; r < GR; ++r)
-                    if (p0 + b < p.S && m + (F0 + r) * 16 < p.M) {
-#pragma unroll
-                        for (int n = 0; n < C::FN; ++n)
-                            v[b][r][n] = base[((size_t)(p0 + b) * C::NF + (F0 + r) * C::FN + n) * C::NT];
-                    }
-#pragma unroll
-            for (int b = 0; b < PB; ++b)
-#pragma unroll
-                for (int r = 0; r < GR; ++r)
-#pragma unroll
-                    for (int n = 0; n < C::FN; ++n) sum[r][n] = sum[r][n] + v[b][r][n];
-        }
-#pragma unroll
-        for (int r = 0; r < GR; ++r)
-#pragma unroll
-            for (int n = 0; n < C::FN; ++n) acc[F0 + r][n] = sum[r][n];
-    });
-    return true;
 }
 
 // Workgroup b -> part, tile row and tile column.  The dispatcher deals
@@ -498,8 +464,8 @@ __global__ __launch_bounds__(C::NT, C::OCC) void linear_kernel(GemmArgs p) {
         if (s + 1 == p.S && p.K % BK) t.template tail<DT>(acc, slabs, p);
         ring_barrier<0>();      // no DMA in flight when the workgroup ends
     }
-    if (p.S > 1 && !linear_reduce<C>(acc, p, m0, mb * p.Nt + nb, s)) return;
-    linear_epilogue<C, DT, PASS>(acc, p, m0, n0);
+    if (p.S > 1) store_part<C>(acc, p, m0, n0, s);
+    else linear_epilogue<C, DT, PASS>(acc, p, m0, n0);
 }
 
 }  // namespace mlpc
