@@ -16,7 +16,7 @@
 struct mlp_norm {
     int H;
     int dtype;
-    int device;
+    int device, cus;
     float eps;
     float* part;                // [max parts][2][H]
     hipStream_t last_stream;
@@ -269,8 +269,14 @@ mlp_norm_t mlp_norm_create(int64_t H, int dtype, float eps) {
     h->dtype = dtype;
     h->device = dev;
     h->eps = eps;
-    const size_t bytes = (size_t)mlpc_norm_max_parts() * 2 * H * sizeof(float);
-    const hipError_t e = hipMalloc(reinterpret_cast<void**>(&h->part), bytes);
+    hipError_t e = hipDeviceGetAttribute(&h->cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) {
+        fail(MLP_EHIP, "hipDeviceGetAttribute failed: %s", hipGetErrorString(e));
+        delete h;
+        return nullptr;
+    }
+    const size_t bytes = (size_t)mlpc_norm_max_parts(h->H, h->cus) * 2 * H * sizeof(float);
+    e = hipMalloc(reinterpret_cast<void**>(&h->part), bytes);
     if (e != hipSuccess) {
         fail(MLP_ENOMEM, "hipMalloc of %zu workspace bytes failed: %s", bytes, hipGetErrorString(e));
         delete h;
@@ -305,7 +311,7 @@ int mlp_norm_forward(mlp_norm_t h, int64_t rows, const void* x, int64_t ldx, con
     a.ldy = ldy;
     a.H = h->H;
     a.eps = h->eps;
-    return launched(mlpc_norm_forward(a, h->dtype, s));
+    return launched(mlpc_norm_forward(a, h->dtype, h->cus, s));
 }
 
 int mlp_norm_backward(mlp_norm_t h, int64_t rows, const void* dy, int64_t lddy, const void* x, int64_t ldx,
@@ -346,7 +352,7 @@ int mlp_norm_backward(mlp_norm_t h, int64_t rows, const void* dy, int64_t lddy, 
     a.lddres = lddres;
     a.lddx = lddx;
     a.H = h->H;
-    a.parts = mlpc_norm_parts(rows);
+    a.parts = mlpc_norm_parts(rows, h->H, h->cus);
     return launched(mlpc_norm_backward(a, h->dtype, s));
 }
 

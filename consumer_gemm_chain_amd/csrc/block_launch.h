@@ -71,11 +71,12 @@ struct DzArgs {
 
 }  // namespace mlpc
 
-hipError_t mlpc_norm_forward(const mlpc::NormArgs& a, int dtype, hipStream_t s);
+hipError_t mlpc_norm_forward(const mlpc::NormArgs& a, int dtype, int cus, hipStream_t s);
 hipError_t mlpc_norm_backward(const mlpc::NormArgs& a, int dtype, hipStream_t s);
-// Row groups whose column sums the norm's gradient keeps in its workspace.
-int mlpc_norm_parts(int64_t rows);
-int mlpc_norm_max_parts();
+// Row groups whose column sums the norm's gradient keeps in its workspace,
+// for `rows` rows and at most.
+int mlpc_norm_parts(int64_t rows, int H, int cus);
+int mlpc_norm_max_parts(int H, int cus);
 
 // Tile configurations (linear_configs.h): their number, sizes, whether a pass
 // has them, and one launch.

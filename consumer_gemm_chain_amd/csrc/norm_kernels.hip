@@ -1,50 +1,399 @@
 // norm_kernels.hip -- layer norm, forward and backward (include/mlp_block.h
 // has the formulas).
+//
+// Rows of up to 16384 elements are held in registers: a group of threads
+// takes a row, V chunks of 8 elements each, so x (and dy) is read once, the
+// variance comes from centred values and the row is written from registers.
+// Both passes are bound by memory.  Longer rows, and those of fewer
+// than 8, take kernels that read a row once per sweep over it.
+//
+// Rows need only 2-byte alignment: gfx950 loads and stores 16 bytes at any
+// address, so a row stride or width that is no multiple of 8 costs the extra
+// cache lines it touches.  (Values stay packed between the sweeps over the registers, behind
+// an empty asm each time: the compiler would otherwise keep their fp32 copies
+// and halve the waves per CU.)
 #include <hip/hip_runtime.h>
 
 #include "block_launch.h"
 #include "chain_device.hpp"
+#include "linear_device.hpp"
 
 namespace mlpc {
 
-template <int DT>
-__device__ __forceinline__ float widen(uint16_t v) {
-    if constexpr (DT == DT_F16) return (float)__builtin_bit_cast(_Float16, v);
-    else return __builtin_bit_cast(float, (uint32_t)v << 16);
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+// Where chunk c (a multiple of 8, c < H) of a row is moved: at c, or where H
+// is no multiple of 8 (RAGGED) and the row ends inside it, at the row's last
+// 8 elements.  The first c - place of those belong to the chunk before: they
+// add nothing to sums and are not stored.
+template <bool RAGGED>
+__device__ __forceinline__ int place(int c, int H) {
+    if constexpr (RAGGED) return min(c, H - 8);
+    else return c;
 }
 
-constexpr int NORM_NT = 256;
+// (`row` is wave-uniform: a scalar base and a 32-bit lane offset.)
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, int c) {
+    return *reinterpret_cast<const u32x4_any*>(row + (uint32_t)c);
+}
+
+// The last 8 - skip of eight elements.
+template <bool RAGGED>
+__device__ __forceinline__ void store8(uint16_t* row, int c, int skip, u32x4 v) {
+    if (!RAGGED || skip == 0) {
+        *reinterpret_cast<u32x4_any*>(row + (uint32_t)c) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        if (i >= skip) row[(uint32_t)c + i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// v + v rotated by N lanes within each row of 16.
+template <int N>
+__device__ __forceinline__ float add_rotated(float v) {
+    const int r = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + N, 0xf, 0xf, false);
+    return v + __builtin_bit_cast(float, r);
+}
+
+// Sum over the wave, the same bits in every lane: rotations within rows of 16
+// lanes, then swaps between rows (no LDS).
+__device__ __forceinline__ float wave_sum(float v) {
+    v = add_rotated<1>(add_rotated<2>(add_rotated<4>(add_rotated<8>(v))));
+    uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t p0 = p[0], p1 = p[1];
+    v = __builtin_bit_cast(float, p0) + __builtin_bit_cast(float, p1);
+    u = __builtin_bit_cast(uint32_t, v);
+    const auto q = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t q0 = q[0], q1 = q[1];
+    return __builtin_bit_cast(float, q0) + __builtin_bit_cast(float, q1);
+}
+
+// ------------------------------------------------------------------- forward
+
+constexpr int FWD_NT = 256;
+
+// TR (64 or 256) threads per row, V chunks per thread.  A workgroup keeps
+// weight and bias in registers over the rows it takes.
+template <int DT, int TR, int V, bool RAGGED>
+__global__ __launch_bounds__(FWD_NT, V <= 2 ? 8 : V <= 4 ? 5 : 4) void norm_forward_kernel(NormArgs a) {
+    constexpr int RPW = FWD_NT / TR;
+    __shared__ float s[2][FWD_NT / 64];
+    const int t = threadIdx.x % TR, sub = uniform(threadIdx.x / TR);
+    u32x4 w[V], b[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = (i * TR + (int)fresh(t)) * 8;
+        if (c < a.H) {
+            if (a.weight) w[i] = load8(a.weight, place<RAGGED>(c, a.H));
+            if (a.bias) b[i] = load8(a.bias, place<RAGGED>(c, a.H));
+        }
+    }
+    const float inv = 1.0f / a.H;
+    // zeroes what chunk i shares with the chunk before
+    auto mask = [&](int i, float (&f)[8]) {
+        if constexpr (RAGGED) {
+            // (recomputed at each use: kept, the conditions of every chunk take too many registers)
+            const int skip = (i * TR + (int)fresh(t)) * 8 - (a.H - 8);
+#pragma unroll
+            for (int k = 0; k < 7; ++k) f[k] = k < skip ? 0.f : f[k];
+        }
+    };
+    auto row_sum = [&](float v, int k) {
+        v = wave_sum(v);
+        if constexpr (TR == 64) return v;
+        if ((threadIdx.x & 63) == 0) s[k][threadIdx.x >> 6] = v;
+        __syncthreads();
+        return (s[k][0] + s[k][1]) + (s[k][2] + s[k][3]);
+    };
+    // (whole workgroups leave the loop together: the sums meet at barriers)
+    for (int64_t r0 = (int64_t)blockIdx.x * RPW; r0 < a.rows; r0 += (int64_t)gridDim.x * RPW) {
+        const int64_t r = r0 + sub < a.rows ? r0 + sub : a.rows - 1;
+        const uint16_t* x = a.x + r * a.ldx;
+        u32x4 v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * TR + (int)fresh(t)) * 8;
+            v[i] = c < a.H ? load8(x, place<RAGGED>(c, a.H)) : u32x4{0, 0, 0, 0};
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float f[8];
+            widen8<DT>(v[i], f);
+            mask(i, f);
+            sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        }
+        const float mean = row_sum(sum, 0) * inv;
+        float var = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if ((i * TR + (int)fresh(t)) * 8 >= a.H) continue;
+            float f[8];
+            pin(v[i]);
+            widen8<DT>(v[i], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                f[k] -= mean;
+                f[k] *= f[k];
+            }
+            mask(i, f);
+            var += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        }
+        const float rstd = 1.0f / sqrtf(row_sum(var, 1) * inv + a.eps);
+        if (r0 + sub >= a.rows) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * TR + (int)fresh(t)) * 8;
+            if (c >= a.H) continue;
+            float f[8], p[8];
+            pin(v[i]);
+            widen8<DT>(v[i], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = (f[k] - mean) * rstd;
+            if (a.weight) {
+                pin(w[i]);
+                widen8<DT>(w[i], p);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] *= p[k];
+            }
+            if (a.bias) {
+                pin(b[i]);
+                widen8<DT>(b[i], p);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] += p[k];
+            }
+            const int at = place<RAGGED>(c, a.H);
+            store8<RAGGED>(a.y + r * a.ldy, at, c - at, narrow8<DT>(f));
+        }
+        if (t == 0) {
+            if (a.mean) a.mean[r] = mean;
+            if (a.rstd) a.rstd[r] = rstd;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+
+constexpr int BWD_NT = 1024;
+constexpr int MAX_PARTS = 256;      // workgroups that keep column sums: one per CU
+
+// TR threads per row (a power of two of at least a wave), V chunks per
+// thread, BWD_NT / TR rows at a time.  A workgroup walks the rows with its
+// columns' sums in registers and the next rows' loads in flight, and leaves
+// one row of partial sums: 1024 threads and one workgroup per CU keep those
+// partials (8 H bytes each) small against the rows.
+template <int DT, int V, bool RAGGED>
+__global__ __launch_bounds__(BWD_NT) void norm_backward_kernel(NormArgs a, int TR) {
+    __shared__ float s[2][BWD_NT / 64][2];
+    extern __shared__ float cols[];         // [H]: the row groups' column sums (TR < BWD_NT)
+    const uint32_t t = threadIdx.x & (TR - 1);
+    const int sub = uniform(threadIdx.x / TR), rpw = BWD_NT / TR;
+    const int wave = threadIdx.x >> 6, first = sub * (TR / 64), waves = TR / 64;
+    const float inv = 1.0f / a.H;
+    const uint32_t one = DT == DT_F16 ? 0x3c003c00u : 0x3f803f80u;     // 1, 1: no weight
+    u32x4 w[V];
+    float sw[V][8] = {}, sb[V][8] = {};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = (i * TR + (int)fresh(t)) * 8;
+        w[i] = a.weight && c < a.H ? load8(a.weight, place<RAGGED>(c, a.H)) : u32x4{one, one, one, one};
+    }
+    u32x4 x[V], dy[V];
+    float mean = 0.f, rstd = 0.f;
+    // row r's x, dy and statistics; a group past the last row takes that row's
+    // x with dy = 0, which adds nothing to any sum
+    auto fetch = [&](int64_t r) {
+        const bool live = r < a.rows;
+        if (!live) r = a.rows - 1;
+        mean = a.mean[r];
+        rstd = a.rstd[r];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * TR + (int)fresh(t)) * 8;
+            x[i] = dy[i] = u32x4{0, 0, 0, 0};
+            if (c < a.H) {
+                x[i] = load8(a.x + r * a.ldx, place<RAGGED>(c, a.H));
+                if (live) dy[i] = load8(a.dy + r * a.lddy, place<RAGGED>(c, a.H));
+            }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * rpw;
+    int64_t r0 = (int64_t)blockIdx.x * rpw;
+    fetch(r0 + sub);
+    for (int buf = 0; r0 < a.rows; r0 += step, buf ^= 1) {
+        const int64_t r = r0 + sub;
+        const bool live = r < a.rows;
+        u32x4 cx[V], cdy[V], dr[V];
+        const float m = mean, rs = rstd;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            cx[i] = x[i];
+            cdy[i] = dy[i];
+            // (needed only after the row's sums: no earlier request)
+            const int c = (i * TR + (int)fresh(t)) * 8;
+            if (a.dres && live && c < a.H) dr[i] = load8(a.dres + r * a.lddres, place<RAGGED>(c, a.H));
+        }
+        if (r0 + step < a.rows) fetch(r + step);
+        // dy, g and xhat of chunk i (where dy = 0, past the row or shared with the chunk before,
+        // so is all that is summed)
+        auto terms = [&](int i, float (&d)[8], float (&g)[8], float (&xh)[8]) {
+            pin(cdy[i]);
+            pin(cx[i]);
+            widen8<DT>(cdy[i], d);
+            widen8<DT>(cx[i], xh);
+            if constexpr (RAGGED) {
+                const int skip = (i * TR + (int)fresh(t)) * 8 - (a.H - 8);
+#pragma unroll
+                for (int k = 0; k < 7; ++k) d[k] = k < skip ? 0.f : d[k];
+            }
+            pin(w[i]);
+            widen8<DT>(w[i], g);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                g[k] *= d[k];
+                xh[k] = (xh[k] - m) * rs;
+            }
+        };
+        float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float d[8], g[8], xh[8];
+            terms(i, d, g, xh);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                t0 += g[k];
+                t1 = __builtin_fmaf(g[k], xh[k], t1);
+                sw[i][k] = __builtin_fmaf(d[k], xh[k], sw[i][k]);
+                sb[i][k] += d[k];
+            }
+            __builtin_amdgcn_sched_barrier(0);      // one chunk's fp32 values at a time
+        }
+        t0 = wave_sum(t0);
+        t1 = wave_sum(t1);
+        if (waves > 1) {
+            // (two sets of sums: a wave writes its next row's only after this row's barrier)
+            if ((threadIdx.x & 63) == 0) {
+                s[buf][wave][0] = t0;
+                s[buf][wave][1] = t1;
+            }
+            __syncthreads();
+            t0 = t1 = 0.f;
+            for (int k = 0; k < waves; ++k) {
+                t0 += s[buf][first + k][0];
+                t1 += s[buf][first + k][1];
+            }
+        }
+        t0 *= inv;
+        t1 *= inv;
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * TR + (int)fresh(t)) * 8;
+            if (c >= a.H) continue;
+            float d[8], g[8], xh[8];
+            terms(i, d, g, xh);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[k] = rs * (g[k] - t0 - xh[k] * t1);
+            if (a.dres) {
+                widen8<DT>(dr[i], g);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) d[k] += g[k];
+            }
+            const int at = place<RAGGED>(c, a.H);
+            store8<RAGGED>(a.dx + r * a.lddx, at, c - at, narrow8<DT>(d));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    if (!a.dweight && !a.dbias) return;
+    // the row groups' sums added in group order, then written as one row
+    auto join = [&](float (&v)[V][8], float* row) {
+        for (int k = 0; k < rpw; ++k) {
+            if (rpw > 1) __syncthreads();
+            if (sub != k) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = (i * TR + (int)fresh(t)) * 8;
+                if (c >= a.H) continue;
+                const int at = place<RAGGED>(c, a.H);
+                float* out = k + 1 < rpw ? cols : row;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (RAGGED && at + e < c) continue;
+                    if (k > 0) v[i][e] += cols[at + e];
+                    out[at + e] = v[i][e];
+                }
+            }
+        }
+    };
+    float* part = a.part + (size_t)blockIdx.x * 2 * a.H;
+    join(sw, part);
+    join(sb, part + a.H);
+}
+
+// The workgroups' partial column sums added in a fixed order: 16 threads
+// across 64 columns, 16 groups of parts, joined through LDS.
+template <int DT>
+__global__ __launch_bounds__(256) void norm_cols_sum_kernel(NormArgs a) {
+    __shared__ float s[16][65];
+    const int64_t n = 2 * (int64_t)a.H, c0 = (int64_t)blockIdx.x * 64;
+    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+    float t[4] = {};
+#pragma unroll 4
+    for (int p = group; p < a.parts; p += 16)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t c = c0 + k * 16 + lane;
+            if (c < n) t[k] += a.part[(size_t)p * n + c];
+        }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[group][k * 16 + lane] = t[k];
+    __syncthreads();
+    const int64_t c = c0 + threadIdx.x;
+    if (threadIdx.x >= 64 || c >= n) return;
+    float v = 0.f;
+    for (int g = 0; g < 16; ++g) v += s[g][threadIdx.x];
+    if (c < a.H) {
+        if (a.dweight) a.dweight[c] = to_storage<DT>(v);
+    } else if (a.dbias) {
+        a.dbias[c - a.H] = to_storage<DT>(v);
+    }
+}
+
+// ------------------------------- rows of fewer than 8 or more than 16384
+
+constexpr int LONG_ROW = 16384;
+static bool held(int H) { return H >= 8 && H <= LONG_ROW; }
+constexpr int SWEEP_NT = 256;
 
 // Sum over the workgroup, the same bits in every thread.
 __device__ __forceinline__ float block_sum(float v, float* s) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    v = wave_sum(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
     __syncthreads();
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < NORM_NT / 64; ++i) t += s[i];
-    return t;
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// One workgroup per row, any H and strides: three passes over the row, the
-// second and third from the caches.
+// One workgroup per row: three sweeps, the second and third from the caches.
 template <int DT>
-__global__ __launch_bounds__(NORM_NT) void norm_forward_kernel(NormArgs a) {
-    __shared__ float s[NORM_NT / 64];
+__global__ __launch_bounds__(SWEEP_NT) void norm_forward_sweep_kernel(NormArgs a) {
+    __shared__ float s[SWEEP_NT / 64];
     const size_t r = blockIdx.x;
     const uint16_t* x = a.x + r * a.ldx;
     float t = 0.f;
-    for (int c = threadIdx.x; c < a.H; c += NORM_NT) t += widen<DT>(x[c]);
+    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) t += widen<DT>(x[c]);
     const float mean = block_sum(t, s) / a.H;
     t = 0.f;
-    for (int c = threadIdx.x; c < a.H; c += NORM_NT) {
+    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
         const float d = widen<DT>(x[c]) - mean;
         t += d * d;
     }
     const float rstd = 1.0f / sqrtf(block_sum(t, s) / a.H + a.eps);
-    for (int c = threadIdx.x; c < a.H; c += NORM_NT) {
+    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
         float v = (widen<DT>(x[c]) - mean) * rstd;
         if (a.weight) v *= widen<DT>(a.weight[c]);
         if (a.bias) v += widen<DT>(a.bias[c]);
@@ -58,20 +407,20 @@ __global__ __launch_bounds__(NORM_NT) void norm_forward_kernel(NormArgs a) {
 
 // dx of one row per workgroup.
 template <int DT>
-__global__ __launch_bounds__(NORM_NT) void norm_dx_kernel(NormArgs a) {
-    __shared__ float s[NORM_NT / 64];
+__global__ __launch_bounds__(SWEEP_NT) void norm_dx_sweep_kernel(NormArgs a) {
+    __shared__ float s[SWEEP_NT / 64];
     const size_t r = blockIdx.x;
     const uint16_t* x = a.x + r * a.ldx;
     const uint16_t* dy = a.dy + r * a.lddy;
     const float mean = a.mean[r], rstd = a.rstd[r];
     float t0 = 0.f, t1 = 0.f;
-    for (int c = threadIdx.x; c < a.H; c += NORM_NT) {
+    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
         const float g = widen<DT>(dy[c]) * (a.weight ? widen<DT>(a.weight[c]) : 1.f);
         t0 += g;
         t1 += g * ((widen<DT>(x[c]) - mean) * rstd);
     }
     const float m0 = block_sum(t0, s) / a.H, m1 = block_sum(t1, s) / a.H;
-    for (int c = threadIdx.x; c < a.H; c += NORM_NT) {
+    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
         const float g = widen<DT>(dy[c]) * (a.weight ? widen<DT>(a.weight[c]) : 1.f);
         float v = rstd * (g - m0 - (widen<DT>(x[c]) - mean) * rstd * m1);
         if (a.dres) v += widen<DT>(a.dres[r * a.lddres + c]);
@@ -82,8 +431,8 @@ __global__ __launch_bounds__(NORM_NT) void norm_dx_kernel(NormArgs a) {
 // Column sums of dy xhat and dy over row group blockIdx.y, one column per
 // thread.
 template <int DT>
-__global__ __launch_bounds__(NORM_NT) void norm_cols_kernel(NormArgs a) {
-    const int c = blockIdx.x * NORM_NT + threadIdx.x;
+__global__ __launch_bounds__(SWEEP_NT) void norm_cols_sweep_kernel(NormArgs a) {
+    const int c = blockIdx.x * SWEEP_NT + threadIdx.x;
     if (c >= a.H) return;
     const int64_t r0 = a.rows * blockIdx.y / a.parts, r1 = a.rows * (blockIdx.y + 1) / a.parts;
     float tw = 0.f, tb = 0.f;
@@ -97,34 +446,68 @@ __global__ __launch_bounds__(NORM_NT) void norm_cols_kernel(NormArgs a) {
     p[a.H] = tb;
 }
 
-// The row groups' column sums added in group order.
-template <int DT>
-__global__ __launch_bounds__(NORM_NT) void norm_cols_sum_kernel(NormArgs a) {
-    const int c = blockIdx.x * NORM_NT + threadIdx.x;
-    if (c >= a.H) return;
-    float tw = 0.f, tb = 0.f;
-    for (int p = 0; p < a.parts; ++p) {
-        tw += a.part[(size_t)p * 2 * a.H + c];
-        tb += a.part[((size_t)p * 2 + 1) * a.H + c];
-    }
-    if (a.dweight) a.dweight[c] = to_storage<DT>(tw);
-    if (a.dbias) a.dbias[c] = to_storage<DT>(tb);
-}
+// ---------------------------------------------------------------------- host
 
-template <int DT>
-static hipError_t norm_forward_t(const NormArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(norm_forward_kernel<DT>, dim3((unsigned)a.rows), dim3(NORM_NT), 0, s, a);
+template <int DT, int TR, int V>
+static hipError_t forward_v(const NormArgs& a, int cus, hipStream_t s) {
+    // up to eight workgroups per CU, so that long batches reuse their weights
+    const int64_t groups = (a.rows + FWD_NT / TR - 1) / (FWD_NT / TR), most = (int64_t)cus * 8;
+    const dim3 grid((unsigned)(groups < most ? groups : most));
+    if (a.H % 8) hipLaunchKernelGGL((norm_forward_kernel<DT, TR, V, true>), grid, dim3(FWD_NT), 0, s, a);
+    else hipLaunchKernelGGL((norm_forward_kernel<DT, TR, V, false>), grid, dim3(FWD_NT), 0, s, a);
     return hipGetLastError();
 }
 
 template <int DT>
-static hipError_t norm_backward_t(const NormArgs& a, hipStream_t s) {
-    const unsigned cols = (unsigned)((a.H + NORM_NT - 1) / NORM_NT);
-    if (a.dweight || a.dbias) {
-        if (a.parts > 0) hipLaunchKernelGGL(norm_cols_kernel<DT>, dim3(cols, a.parts), dim3(NORM_NT), 0, s, a);
-        hipLaunchKernelGGL(norm_cols_sum_kernel<DT>, dim3(cols), dim3(NORM_NT), 0, s, a);
+static hipError_t forward_sweep(const NormArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(norm_forward_sweep_kernel<DT>, dim3((unsigned)a.rows), dim3(SWEEP_NT), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int DT>
+static hipError_t forward_t(const NormArgs& a, int cus, hipStream_t s) {
+    // a wave per row while four chunks per lane hold it, then a workgroup
+    if (a.H < 8) return forward_sweep<DT>(a, s);
+    if (a.H <= 512) return forward_v<DT, 64, 1>(a, cus, s);
+    if (a.H <= 1024) return forward_v<DT, 64, 2>(a, cus, s);
+    if (a.H <= 2048) return forward_v<DT, 64, 4>(a, cus, s);
+    if (a.H <= 4096) return forward_v<DT, 256, 2>(a, cus, s);
+    if (a.H <= 8192) return forward_v<DT, 256, 4>(a, cus, s);
+    if (a.H <= 12288) return forward_v<DT, 256, 6>(a, cus, s);
+    if (a.H <= LONG_ROW) return forward_v<DT, 256, 8>(a, cus, s);
+    return forward_sweep<DT>(a, s);
+}
+
+// Threads per row of the register-held backward: two chunks each, from a wave
+// up to the workgroup.
+static int backward_threads(int H) {
+    int tr = 64;
+    while (tr < BWD_NT && tr * 16 < H) tr *= 2;
+    return tr;
+}
+
+template <int DT, int V>
+static void backward_v(const NormArgs& a, hipStream_t s) {
+    const int tr = backward_threads(a.H);
+    const size_t lds = tr < BWD_NT && (a.dweight || a.dbias) ? (size_t)a.H * sizeof(float) : 0;
+    if (a.H % 8) hipLaunchKernelGGL((norm_backward_kernel<DT, V, true>), dim3(a.parts), dim3(BWD_NT), lds, s, a, tr);
+    else hipLaunchKernelGGL((norm_backward_kernel<DT, V, false>), dim3(a.parts), dim3(BWD_NT), lds, s, a, tr);
+}
+
+template <int DT>
+static hipError_t backward_t(const NormArgs& a, hipStream_t s) {
+    const bool sums = a.dweight || a.dbias;
+    if (held(a.H)) {
+        if (a.parts > 0) {
+            if (a.H <= 512) backward_v<DT, 1>(a, s);
+            else backward_v<DT, 2>(a, s);
+        }
+    } else if (a.parts > 0) {
+        if (sums)
+            hipLaunchKernelGGL(norm_cols_sweep_kernel<DT>, dim3((a.H + SWEEP_NT - 1) / SWEEP_NT, a.parts), dim3(SWEEP_NT), 0, s, a);
+        hipLaunchKernelGGL(norm_dx_sweep_kernel<DT>, dim3((unsigned)a.rows), dim3(SWEEP_NT), 0, s, a);
     }
-    if (a.rows > 0) hipLaunchKernelGGL(norm_dx_kernel<DT>, dim3((unsigned)a.rows), dim3(NORM_NT), 0, s, a);
+    if (sums) hipLaunchKernelGGL(norm_cols_sum_kernel<DT>, dim3((2 * a.H + 63) / 64), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -132,14 +515,21 @@ static hipError_t norm_backward_t(const NormArgs& a, hipStream_t s) {
 
 using namespace mlpc;
 
-int mlpc_norm_max_parts() { return 64; }
+// Partial rows of column sums: the workgroups of the register-held kernel, or
+// the row groups of the sweeping column kernel.
+int mlpc_norm_parts(int64_t rows, int H, int cus) {
+    const int64_t per = held(H) ? BWD_NT / backward_threads(H) : 1;
+    const int64_t groups = (rows + per - 1) / per;
+    const int64_t most = held(H) ? (cus < MAX_PARTS ? cus : MAX_PARTS) : 64;
+    return (int)(groups < most ? groups : most);
+}
 
-int mlpc_norm_parts(int64_t rows) { return (int)(rows < 64 ? rows : 64); }
+int mlpc_norm_max_parts(int H, int cus) { return mlpc_norm_parts((int64_t)1 << 32, H, cus); }
 
-hipError_t mlpc_norm_forward(const NormArgs& a, int dtype, hipStream_t s) {
-    return dtype == DT_F16 ? norm_forward_t<DT_F16>(a, s) : norm_forward_t<DT_BF16>(a, s);
+hipError_t mlpc_norm_forward(const NormArgs& a, int dtype, int cus, hipStream_t s) {
+    return dtype == DT_F16 ? forward_t<DT_F16>(a, cus, s) : forward_t<DT_BF16>(a, cus, s);
 }
 
 hipError_t mlpc_norm_backward(const NormArgs& a, int dtype, hipStream_t s) {
-    return dtype == DT_F16 ? norm_backward_t<DT_F16>(a, s) : norm_backward_t<DT_BF16>(a, s);
+    return dtype == DT_F16 ? backward_t<DT_F16>(a, s) : backward_t<DT_BF16>(a, s);
 }
