@@ -297,11 +297,21 @@ __device__ __forceinline__ void widen8(u32x4 v, float (&f)[8]) {
     }
 }
 
+// (The empty asm statements pin the values in fp32: see to_storage.)
 template <int DT>
 __device__ __forceinline__ u32x4 narrow8(const float (&f)[8]) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (uint32_t)to_storage<DT>(f[2 * i]) | ((uint32_t)to_storage<DT>(f[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) {
+        float lo = f[2 * i], hi = f[2 * i + 1];
+        pin(lo);
+        pin(hi);
+        if constexpr (DT == DT_F16) v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), f16x2));
+        else v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+    }
     return v;
 }
 

@@ -185,11 +185,13 @@ constexpr int MAX_PARTS = 256;      // workgroups that keep column sums: one per
 // thread, BWD_NT / TR rows at a time.  A workgroup walks the rows with its
 // columns' sums in registers and the next rows' loads in flight, and leaves
 // one row of partial sums: 1024 threads and one workgroup per CU keep those
-// partials (8 H bytes each) small against the rows.
+// partials (8 H bytes each) small against the rows.  With d = x - mean the
+// row needs the sums of g and g d; dx = rstd g - rstd mean_c(g) -
+// d rstd^3 mean_c(g d) + dres.
 template <int DT, int V, bool RAGGED>
 __global__ __launch_bounds__(BWD_NT) void norm_backward_kernel(NormArgs a, int TR) {
     __shared__ float s[2][BWD_NT / 64][2];
-    extern __shared__ float cols[];         // [H]: the row groups' column sums (TR < BWD_NT)
+    __shared__ float cols[BWD_NT * 8];      // one chunk of every thread's column sums
     const uint32_t t = threadIdx.x & (TR - 1);
     const int sub = uniform(threadIdx.x / TR), rpw = BWD_NT / TR;
     const int wave = threadIdx.x >> 6, first = sub * (TR / 64), waves = TR / 64;
@@ -238,38 +240,44 @@ __global__ __launch_bounds__(BWD_NT) void norm_backward_kernel(NormArgs a, int T
             if (a.dres && live && c < a.H) dr[i] = load8(a.dres + r * a.lddres, place<RAGGED>(c, a.H));
         }
         if (r0 + step < a.rows) fetch(r + step);
-        // dy, g and xhat of chunk i (where dy = 0, past the row or shared with the chunk before,
-        // so is all that is summed)
-        auto terms = [&](int i, float (&d)[8], float (&g)[8], float (&xh)[8]) {
+        // dy, g and d of chunk i (where dy = 0, past the row or shared with
+        // the chunk before, so is all that is summed)
+        auto terms = [&](int i, float (&e)[8], float (&g)[8], float (&d)[8]) {
             pin(cdy[i]);
             pin(cx[i]);
-            widen8<DT>(cdy[i], d);
-            widen8<DT>(cx[i], xh);
+            widen8<DT>(cdy[i], e);
+            widen8<DT>(cx[i], d);
             if constexpr (RAGGED) {
                 const int skip = (i * TR + (int)fresh(t)) * 8 - (a.H - 8);
 #pragma unroll
-                for (int k = 0; k < 7; ++k) d[k] = k < skip ? 0.f : d[k];
+                for (int k = 0; k < 7; ++k) e[k] = k < skip ? 0.f : e[k];
             }
             pin(w[i]);
             widen8<DT>(w[i], g);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                g[k] *= d[k];
-                xh[k] = (xh[k] - m) * rs;
+                g[k] *= e[k];
+                d[k] -= m;
             }
         };
         float t0 = 0.f, t1 = 0.f;
+        float g[V][8], d[V][8];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float d[8], g[8], xh[8];
-            terms(i, d, g, xh);
+            float e[8], u0 = 0.f, u1 = 0.f;
+            terms(i, e, g[i], d[i]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                t0 += g[k];
-                t1 = __builtin_fmaf(g[k], xh[k], t1);
-                sw[i][k] = __builtin_fmaf(d[k], xh[k], sw[i][k]);
-                sb[i][k] += d[k];
+                // (two chains each)
+                float& v0 = k & 1 ? u0 : t0;
+                float& v1 = k & 1 ? u1 : t1;
+                v0 += g[i][k];
+                v1 = __builtin_fmaf(g[i][k], d[i][k], v1);
+                sb[i][k] += e[k];
+                sw[i][k] = __builtin_fmaf(e[k] * rs, d[i][k], sw[i][k]);
             }
+            t0 += u0;
+            t1 += u1;
             __builtin_amdgcn_sched_barrier(0);      // one chunk's fp32 values at a time
         }
         t0 = wave_sum(t0);
@@ -282,84 +290,87 @@ __global__ __launch_bounds__(BWD_NT) void norm_backward_kernel(NormArgs a, int T
             }
             __syncthreads();
             t0 = t1 = 0.f;
+#pragma unroll 4
             for (int k = 0; k < waves; ++k) {
                 t0 += s[buf][first + k][0];
                 t1 += s[buf][first + k][1];
             }
         }
-        t0 *= inv;
-        t1 *= inv;
         if (!live) continue;
+        const float b0 = -rs * (t0 * inv), b1 = -(rs * rs) * (rs * (t1 * inv));
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = (i * TR + (int)fresh(t)) * 8;
             if (c >= a.H) continue;
-            float d[8], g[8], xh[8];
-            terms(i, d, g, xh);
+            float e[8];
+            // two chunks' fp32 values do not fit beside the sums: taken again from the packed ones
+            if constexpr (V > 1) terms(i, e, g[i], d[i]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) d[k] = rs * (g[k] - t0 - xh[k] * t1);
+            for (int k = 0; k < 8; ++k) e[k] = __builtin_fmaf(d[i][k], b1, __builtin_fmaf(g[i][k], rs, b0));
             if (a.dres) {
-                widen8<DT>(dr[i], g);
+                float q[8];
+                widen8<DT>(dr[i], q);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) d[k] += g[k];
+                for (int k = 0; k < 8; ++k) e[k] += q[k];
             }
             const int at = place<RAGGED>(c, a.H);
-            store8<RAGGED>(a.dx + r * a.lddx, at, c - at, narrow8<DT>(d));
+            store8<RAGGED>(a.dx + r * a.lddx, at, c - at, narrow8<DT>(e));
             __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (!a.dweight && !a.dbias) return;
-    // the row groups' sums added in group order, then written as one row
-    auto join = [&](float (&v)[V][8], float* row) {
-        for (int k = 0; k < rpw; ++k) {
-            if (rpw > 1) __syncthreads();
-            if (sub != k) continue;
+    // the row groups' sums, chunk by chunk through LDS, added in group order
+    // and written as the workgroup's row of partials
+    float* part = a.part + (size_t)blockIdx.x * 2 * a.H;
+    auto join = [&](float (&v)[8], int i, float* row) {
+        const int c = (i * TR + (int)t) * 8, at = c < a.H ? place<RAGGED>(c, a.H) : c;
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = (i * TR + (int)fresh(t)) * 8;
-                if (c >= a.H) continue;
-                const int at = place<RAGGED>(c, a.H);
-                float* out = k + 1 < rpw ? cols : row;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (RAGGED && at + e < c) continue;
-                    if (k > 0) v[i][e] += cols[at + e];
-                    out[at + e] = v[i][e];
-                }
-            }
+        for (int e = 0; e < 8; ++e)
+            if (!RAGGED || at + e >= c) cols[(sub * TR - i * TR) * 8 + at + e] = v[e];
+        __syncthreads();
+        for (int j = threadIdx.x; j < TR * 8; j += BWD_NT) {
+            if (i * TR * 8 + j >= a.H) continue;
+            float sum = cols[j];
+#pragma unroll 4
+            for (int k = 1; k < rpw; ++k) sum += cols[k * TR * 8 + j];
+            row[i * TR * 8 + j] = sum;
         }
     };
-    float* part = a.part + (size_t)blockIdx.x * 2 * a.H;
-    join(sw, part);
-    join(sb, part + a.H);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        join(sw[i], i, part);
+        join(sb[i], i, part + a.H);
+    }
 }
 
-// The workgroups' partial column sums added in a fixed order: 16 threads
-// across 64 columns, 16 groups of parts, joined through LDS.
+// The workgroups' partial column sums added in a fixed order: 32 columns by
+// 32 groups of parts, every part's load of a thread in flight at once, the
+// groups joined through LDS.
 template <int DT>
-__global__ __launch_bounds__(256) void norm_cols_sum_kernel(NormArgs a) {
-    __shared__ float s[16][65];
-    const int64_t n = 2 * (int64_t)a.H, c0 = (int64_t)blockIdx.x * 64;
-    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
-    float t[4] = {};
-#pragma unroll 4
-    for (int p = group; p < a.parts; p += 16)
+__global__ __launch_bounds__(1024) void norm_cols_sum_kernel(NormArgs a) {
+    __shared__ float s[32][33];
+    const int64_t n = 2 * (int64_t)a.H;
+    const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float v[MAX_PARTS / 32], sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t c = c0 + k * 16 + lane;
-            if (c < n) t[k] += a.part[(size_t)p * n + c];
-        }
+    for (int k = 0; k < MAX_PARTS / 32; ++k) {
+        const int p = k * 32 + group;
+        v[k] = p < a.parts && c < n ? a.part[(size_t)p * n + c] : 0.f;
+    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s[group][k * 16 + lane] = t[k];
+    for (int k = 0; k < MAX_PARTS / 32; ++k) sum += v[k];
+    s[group][lane] = sum;
     __syncthreads();
-    const int64_t c = c0 + threadIdx.x;
-    if (threadIdx.x >= 64 || c >= n) return;
-    float v = 0.f;
-    for (int g = 0; g < 16; ++g) v += s[g][threadIdx.x];
+    if (group != 0 || c >= n) return;
+    sum = 0.f;
+#pragma unroll 8
+    for (int g = 0; g < 32; ++g) sum += s[g][lane];
     if (c < a.H) {
-        if (a.dweight) a.dweight[c] = to_storage<DT>(v);
+        if (a.dweight) a.dweight[c] = to_storage<DT>(sum);
     } else if (a.dbias) {
-        a.dbias[c - a.H] = to_storage<DT>(v);
+        a.dbias[c - a.H] = to_storage<DT>(sum);
     }
 }
 
@@ -478,20 +489,19 @@ static hipError_t forward_t(const NormArgs& a, int cus, hipStream_t s) {
     return forward_sweep<DT>(a, s);
 }
 
-// Threads per row of the register-held backward: two chunks each, from a wave
-// up to the workgroup.
+// Threads per row of the register-held backward: one chunk each, from a wave
+// up to the workgroup (which then takes two).
 static int backward_threads(int H) {
     int tr = 64;
-    while (tr < BWD_NT && tr * 16 < H) tr *= 2;
+    while (tr < BWD_NT && tr * 8 < H) tr *= 2;
     return tr;
 }
 
 template <int DT, int V>
 static void backward_v(const NormArgs& a, hipStream_t s) {
     const int tr = backward_threads(a.H);
-    const size_t lds = tr < BWD_NT && (a.dweight || a.dbias) ? (size_t)a.H * sizeof(float) : 0;
-    if (a.H % 8) hipLaunchKernelGGL((norm_backward_kernel<DT, V, true>), dim3(a.parts), dim3(BWD_NT), lds, s, a, tr);
-    else hipLaunchKernelGGL((norm_backward_kernel<DT, V, false>), dim3(a.parts), dim3(BWD_NT), lds, s, a, tr);
+    if (a.H % 8) hipLaunchKernelGGL((norm_backward_kernel<DT, V, true>), dim3(a.parts), dim3(BWD_NT), 0, s, a, tr);
+    else hipLaunchKernelGGL((norm_backward_kernel<DT, V, false>), dim3(a.parts), dim3(BWD_NT), 0, s, a, tr);
 }
 
 template <int DT>
@@ -499,7 +509,7 @@ static hipError_t backward_t(const NormArgs& a, hipStream_t s) {
     const bool sums = a.dweight || a.dbias;
     if (held(a.H)) {
         if (a.parts > 0) {
-            if (a.H <= 512) backward_v<DT, 1>(a, s);
+            if (a.H <= BWD_NT * 8) backward_v<DT, 1>(a, s);
             else backward_v<DT, 2>(a, s);
         }
     } else if (a.parts > 0) {
@@ -507,7 +517,7 @@ static hipError_t backward_t(const NormArgs& a, hipStream_t s) {
             hipLaunchKernelGGL(norm_cols_sweep_kernel<DT>, dim3((a.H + SWEEP_NT - 1) / SWEEP_NT, a.parts), dim3(SWEEP_NT), 0, s, a);
         hipLaunchKernelGGL(norm_dx_sweep_kernel<DT>, dim3((unsigned)a.rows), dim3(SWEEP_NT), 0, s, a);
     }
-    if (sums) hipLaunchKernelGGL(norm_cols_sum_kernel<DT>, dim3((2 * a.H + 63) / 64), dim3(256), 0, s, a);
+    if (sums) hipLaunchKernelGGL(norm_cols_sum_kernel<DT>, dim3((2 * a.H + 31) / 32), dim3(1024), 0, s, a);
     return hipGetLastError();
 }
 
