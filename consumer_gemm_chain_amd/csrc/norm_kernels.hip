@@ -178,22 +178,20 @@ __global__ __launch_bounds__(FWD_NT, V <= 2 ? 8 : V <= 4 ? 5 : 4) void norm_forw
 
 // ------------------------------------------------------------------ backward
 
-constexpr int BWD_NT = 1024;
 constexpr int MAX_PARTS = 256;      // workgroups that keep column sums: one per CU
 
-// TR threads per row (a power of two of at least a wave), V chunks per
-// thread, BWD_NT / TR rows at a time.  A workgroup walks the rows with its
+// TR threads per row (whole waves, a divisor of NT), V chunks per thread, NT / TR rows at a time.  A workgroup walks the rows with its
 // columns' sums in registers and the next rows' loads in flight, and leaves
-// one row of partial sums: 1024 threads and one workgroup per CU keep those
+// one row of partial sums: large workgroups, one per CU, keep those
 // partials (8 H bytes each) small against the rows.  With d = x - mean the
 // row needs the sums of g and g d; dx = rstd g - rstd mean_c(g) -
 // d rstd^3 mean_c(g d) + dres.
-template <int DT, int V, bool RAGGED>
-__global__ __launch_bounds__(BWD_NT) void norm_backward_kernel(NormArgs a, int TR) {
-    __shared__ float s[2][BWD_NT / 64][2];
-    __shared__ float cols[BWD_NT * 8];      // one chunk of every thread's column sums
-    const uint32_t t = threadIdx.x & (TR - 1);
-    const int sub = uniform(threadIdx.x / TR), rpw = BWD_NT / TR;
+template <int DT, int NT, int V, bool RAGGED>
+__global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
+    __shared__ float s[2][NT / 64][2];
+    __shared__ float cols[NT * 8];      // one chunk of every thread's column sums
+    const int sub = uniform(threadIdx.x / TR), rpw = NT / TR;
+    const uint32_t t = threadIdx.x - sub * TR;
     const int wave = threadIdx.x >> 6, first = sub * (TR / 64), waves = TR / 64;
     const float inv = 1.0f / a.H;
     const uint32_t one = DT == DT_F16 ? 0x3c003c00u : 0x3f803f80u;     // 1, 1: no weight
@@ -303,8 +301,9 @@ __global__ __launch_bounds__(BWD_NT) void norm_backward_kernel(NormArgs a, int T
             const int c = (i * TR + (int)fresh(t)) * 8;
             if (c >= a.H) continue;
             float e[8];
-            // two chunks' fp32 values do not fit beside the sums: taken again from the packed ones
-            if constexpr (V > 1) terms(i, e, g[i], d[i]);
+            // 16 waves' registers do not hold two chunks' fp32 values beside
+            // the sums: taken again from the packed ones
+            if constexpr (V > 1 && NT > 768) terms(i, e, g[i], d[i]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) e[k] = __builtin_fmaf(d[i][k], b1, __builtin_fmaf(g[i][k], rs, b0));
             if (a.dres) {
@@ -329,7 +328,7 @@ __global__ __launch_bounds__(BWD_NT) void norm_backward_kernel(NormArgs a, int T
         for (int e = 0; e < 8; ++e)
             if (!RAGGED || at + e >= c) cols[(sub * TR - i * TR) * 8 + at + e] = v[e];
         __syncthreads();
-        for (int j = threadIdx.x; j < TR * 8; j += BWD_NT) {
+        for (int j = threadIdx.x; j < TR * 8; j += NT) {
             if (i * TR * 8 + j >= a.H) continue;
             float sum = cols[j];
 #pragma unroll 4
@@ -489,19 +488,26 @@ static hipError_t forward_t(const NormArgs& a, int cus, hipStream_t s) {
     return forward_sweep<DT>(a, s);
 }
 
-// Threads per row of the register-held backward: one chunk each, from a wave
-// up to the workgroup (which then takes two).
-static int backward_threads(int H) {
+// The register-held backward's workgroup, threads per row and chunks per
+// thread: one chunk each from a wave per row up to 1024 threads, then two; 768
+// threads while they hold the row, whose larger register budget keeps every
+// fp32 value of a row.
+struct BackwardShape {
+    int nt, tr, v;
+};
+
+static BackwardShape backward_shape(int H) {
+    if (H > 12288) return {1024, 1024, 2};
+    if (H > 8192) return {768, 768, 2};
     int tr = 64;
-    while (tr < BWD_NT && tr * 8 < H) tr *= 2;
-    return tr;
+    while (tr * 8 < H) tr *= 2;
+    return {1024, tr, 1};
 }
 
-template <int DT, int V>
-static void backward_v(const NormArgs& a, hipStream_t s) {
-    const int tr = backward_threads(a.H);
-    if (a.H % 8) hipLaunchKernelGGL((norm_backward_kernel<DT, V, true>), dim3(a.parts), dim3(BWD_NT), 0, s, a, tr);
-    else hipLaunchKernelGGL((norm_backward_kernel<DT, V, false>), dim3(a.parts), dim3(BWD_NT), 0, s, a, tr);
+template <int DT, int NT, int V>
+static void backward_v(const NormArgs& a, int tr, hipStream_t s) {
+    if (a.H % 8) hipLaunchKernelGGL((norm_backward_kernel<DT, NT, V, true>), dim3(a.parts), dim3(NT), 0, s, a, tr);
+    else hipLaunchKernelGGL((norm_backward_kernel<DT, NT, V, false>), dim3(a.parts), dim3(NT), 0, s, a, tr);
 }
 
 template <int DT>
@@ -509,8 +515,10 @@ static hipError_t backward_t(const NormArgs& a, hipStream_t s) {
     const bool sums = a.dweight || a.dbias;
     if (held(a.H)) {
         if (a.parts > 0) {
-            if (a.H <= BWD_NT * 8) backward_v<DT, 1>(a, s);
-            else backward_v<DT, 2>(a, s);
+            const BackwardShape b = backward_shape(a.H);
+            if (b.v == 1) backward_v<DT, 1024, 1>(a, b.tr, s);
+            else if (b.nt == 768) backward_v<DT, 768, 2>(a, b.tr, s);
+            else backward_v<DT, 1024, 2>(a, b.tr, s);
         }
     } else if (a.parts > 0) {
         if (sums)
@@ -528,7 +536,7 @@ using namespace mlpc;
 // Partial rows of column sums: the workgroups of the register-held kernel, or
 // the row groups of the sweeping column kernel.
 int mlpc_norm_parts(int64_t rows, int H, int cus) {
-    const int64_t per = held(H) ? BWD_NT / backward_threads(H) : 1;
+    const int64_t per = held(H) ? backward_shape(H).nt / backward_shape(H).tr : 1;
     const int64_t groups = (rows + per - 1) / per;
     const int64_t most = held(H) ? (cus < MAX_PARTS ? cus : MAX_PARTS) : 64;
     return (int)(groups < most ? groups : most);
