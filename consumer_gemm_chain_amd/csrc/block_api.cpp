@@ -22,11 +22,21 @@ struct mlp_norm {
     hipStream_t last_stream;
 };
 
+// How a product runs: tile configuration, tiles, parts of the reduction and
+// slabs per part.
+struct Plan {
+    int cfg;
+    uint32_t Mt, Nt, S, ksp;
+    size_t part_bytes;
+};
+
 struct mlp_linear {
     int64_t max_rows;
     int K, N, gN;
     int act, dtype, device, cus;
     int forced_cfg[3], forced_split[3];     // per pass; -1 / 0: the planner's
+    int64_t plan_rows[3];                   // the row count plan[pass] is for (-1: none)
+    Plan plan[3];
     // workspace (one allocation): zero page | dz [max_rows, gN] (activations
     // only) | column-sum partials [max parts][gN] | split partials
     void* ws;
@@ -127,12 +137,6 @@ int launched(hipError_t e) {
 constexpr size_t MAX_PART_BYTES = (size_t)64 << 20;
 constexpr uint32_t MAX_SPLIT = 32;
 
-struct Plan {
-    int cfg;
-    uint32_t Mt, Nt, S, ksp;
-    size_t part_bytes;
-};
-
 // The plan of a product of M x N columns (both halves of swiglu's B) over K
 // with configuration cfg and at most `split` parts (no part is empty).
 Plan make_plan(int cfg, int64_t M, int64_t N, int64_t K, uint32_t split) {
@@ -217,10 +221,15 @@ size_t max_part_bytes(int64_t max_rows, int64_t K, int64_t gN) {
     return most < MAX_PART_BYTES ? most : MAX_PART_BYTES;
 }
 
-int run_product(mlp_linear* h, int pass, mlpc::GemmArgs& a, hipStream_t s) {
+int run_product(mlp_linear* h, int pass, int64_t rows, mlpc::GemmArgs& a, hipStream_t s) {
     const int64_t n = a.up ? (int64_t)a.N + a.up : a.N;
-    const Plan p = h->forced_cfg[pass] < 0 ? choose_plan(a.M, n, a.K, pass, h->cus)
-                                           : make_plan(h->forced_cfg[pass], a.M, n, a.K, (uint32_t)h->forced_split[pass]);
+    if (h->plan_rows[pass] != rows) {
+        h->plan[pass] = h->forced_cfg[pass] < 0
+                            ? choose_plan(a.M, n, a.K, pass, h->cus)
+                            : make_plan(h->forced_cfg[pass], a.M, n, a.K, (uint32_t)h->forced_split[pass]);
+        h->plan_rows[pass] = rows;
+    }
+    const Plan& p = h->plan[pass];
     if (p.part_bytes > h->part_bytes)
         return fail(MLP_EINVAL, "the split needs %zu workspace bytes of %zu", p.part_bytes, h->part_bytes);
     a.Mt = p.Mt;
@@ -383,6 +392,7 @@ mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, 
     for (int i = 0; i < 3; ++i) {
         h->forced_cfg[i] = -1;
         h->forced_split[i] = 0;
+        h->plan_rows[i] = -1;
     }
     hipError_t e = hipDeviceGetAttribute(&h->cus, hipDeviceAttributeMultiprocessorCount, dev);
     if (e != hipSuccess) {
@@ -455,7 +465,7 @@ int mlp_linear_forward(mlp_linear_t h, int64_t rows, const void* x, int64_t ldx,
     a.z = static_cast<uint16_t*>(z);
     a.ldr = ldres;
     a.ldz = ldz;
-    return run_product(h, mlpc::PASS_FWD, a, s);
+    return run_product(h, mlpc::PASS_FWD, rows, a, s);
 }
 
 int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t lddy, const void* x, int64_t ldx,
@@ -511,7 +521,7 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
         a.M = (int)rows;
         a.N = h->K;
         a.K = h->gN;
-        rc = run_product(h, mlpc::PASS_DX, a, s);
+        rc = run_product(h, mlpc::PASS_DX, rows, a, s);
         if (rc != MLP_OK) return rc;
     }
     if (dw) {
@@ -525,7 +535,7 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
         a.M = h->K;
         a.N = h->gN;
         a.K = (int)rows;
-        return run_product(h, mlpc::PASS_DW, a, s);
+        return run_product(h, mlpc::PASS_DW, rows, a, s);
     }
     return MLP_OK;
 }
@@ -553,6 +563,7 @@ int mlp_linear_debug_set_plan(mlp_linear_t h, int pass, int config_id, int split
         return fail(MLP_EINVAL, "a configuration's split must be in 0..%u, got %d", MAX_SPLIT, split);
     h->forced_cfg[pass] = config_id;
     h->forced_split[pass] = split;
+    h->plan_rows[pass] = -1;
     return MLP_OK;
 }
 

@@ -101,14 +101,19 @@ def mlp_linear_debug_set_plan(h: int, op: int, config_id: int, split: int) -> in
 
 # ---- convenience wrappers over torch tensors ------------------------------------
 
-def _storage(dtype: str):
-    import torch
-    return torch.float16 if dtype == "f16" else torch.bfloat16
-
-
 class _Layer:
-    """Owns one handle; `_destroy` releases it."""
+    """Owns one handle; `_destroy` releases it.  The checks below run on every
+    call, beside a few microseconds of kernel, and touch each tensor little."""
     h = None
+
+    def _set_type(self, dtype: str):
+        import torch
+        self.dtype = dtype
+        self.torch_dtype = torch.float16 if dtype == "f16" else torch.bfloat16
+        self._f32 = torch.float32
+        # the current stream's handle without building a Stream object (2.7 us of a call)
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
 
     def close(self):
         h, self.h = self.h, None
@@ -127,35 +132,33 @@ class _Layer:
     def __exit__(self, *exc):
         self.close()
 
-    @staticmethod
-    def _stream(stream):
+    def _stream(self, stream, t):
+        """The handle of `stream`, or of the current stream of t's device."""
         if stream is not None:
             return int(getattr(stream, "cuda_stream", stream))
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return self._raw_stream(t.get_device())
 
     def _rows(self, name, t, rows, width):
-        """Pointer and row stride of a [rows, width] operand (0, 0: absent)."""
+        """Pointer and row stride of a [rows, width] operand (None, 0: absent)."""
         if t is None:
             return None, 0
-        shape, stride = t.shape, t.stride()
-        if len(shape) != 2 or shape[0] != rows or shape[1] != width:
-            raise ValueError(f"{name} has shape {tuple(shape)}, expected {(rows, width)}")
-        if not t.is_cuda or t.dtype != self.torch_dtype:
+        if t.shape != (rows, width):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, width)}")
+        if t.dtype != self.torch_dtype or not t.is_cuda:
             raise ValueError(f"{name} must be a {self.dtype} device tensor")
-        if width > 1 and stride[1] != 1:
-            raise ValueError(f"{name} must have contiguous rows, got strides {stride}")
-        if rows <= 1:       # the stride of a single row is never used
-            return t.data_ptr(), width
-        return t.data_ptr(), stride[0]
+        ld, unit = t.stride()
+        if unit != 1 and width > 1:
+            raise ValueError(f"{name} must have contiguous rows, got strides {(ld, unit)}")
+        return t.data_ptr(), ld if rows > 1 else width      # (a single row's stride is never used)
 
-    def _vector(self, name, t, n, dtype=None):
+    def _vector(self, name, t, n, dtype):
+        """Pointer of a contiguous vector (None: absent)."""
         if t is None:
             return None
-        if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        if t.shape != (n,) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous vector of {n} elements, got shape {tuple(t.shape)}")
-        if not t.is_cuda or t.dtype != (dtype or self.torch_dtype):
-            raise ValueError(f"{name} must be a {dtype or self.dtype} device tensor")
+        if t.dtype != dtype or not t.is_cuda:
+            raise ValueError(f"{name} must be a {dtype} device tensor")
         return t.data_ptr()
 
 
@@ -164,8 +167,8 @@ class MlpNorm(_Layer):
     work is enqueued on torch's current stream (or `stream`)."""
 
     def __init__(self, H: int, dtype: str = "f16", eps: float = 1e-5):
-        self.H, self.dtype, self.eps = int(H), dtype, float(eps)
-        self.torch_dtype = _storage(dtype)
+        self.H, self.eps = int(H), float(eps)
+        self._set_type(dtype)
         self.h = mlp_norm_create(H, DTYPES[dtype], eps)
 
     _destroy = staticmethod(mlp_norm_destroy)
@@ -173,27 +176,25 @@ class MlpNorm(_Layer):
     def forward(self, x, weight, bias, out, mean=None, rstd=None, stream=None):
         """out = norm(x) weight + bias ([rows, H]); `mean` and `rstd` (float32
         [rows]) receive the statistics the gradient needs."""
-        import torch
-        rows, f32 = x.shape[0], torch.float32
-        px, ldx = self._rows("x", x, rows, self.H)
-        py, ldy = self._rows("out", out, rows, self.H)
-        mlp_norm_forward(self.h, rows, px, ldx, self._vector("weight", weight, self.H),
-                         self._vector("bias", bias, self.H), py, ldy, self._vector("mean", mean, rows, f32),
-                         self._vector("rstd", rstd, rows, f32), self._stream(stream))
+        rows, H, dt, f32 = x.shape[0], self.H, self.torch_dtype, self._f32
+        px, ldx = self._rows("x", x, rows, H)
+        py, ldy = self._rows("out", out, rows, H)
+        mlp_norm_forward(self.h, rows, px, ldx, self._vector("weight", weight, H, dt),
+                         self._vector("bias", bias, H, dt), py, ldy, self._vector("mean", mean, rows, f32),
+                         self._vector("rstd", rstd, rows, f32), self._stream(stream, x))
         return out
 
     def backward(self, dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, dres=None, stream=None):
         """The gradients of `forward`; `dres` is added to dx."""
-        import torch
-        rows, f32 = x.shape[0], torch.float32
-        pdy, lddy = self._rows("dy", dy, rows, self.H)
-        px, ldx = self._rows("x", x, rows, self.H)
-        pr, ldr = self._rows("dres", dres, rows, self.H)
-        pdx, lddx = self._rows("dx", dx, rows, self.H)
-        mlp_norm_backward(self.h, rows, pdy, lddy, px, ldx, self._vector("weight", weight, self.H),
+        rows, H, dt, f32 = x.shape[0], self.H, self.torch_dtype, self._f32
+        pdy, lddy = self._rows("dy", dy, rows, H)
+        px, ldx = self._rows("x", x, rows, H)
+        pr, ldr = self._rows("dres", dres, rows, H)
+        pdx, lddx = self._rows("dx", dx, rows, H)
+        mlp_norm_backward(self.h, rows, pdy, lddy, px, ldx, self._vector("weight", weight, H, dt),
                           self._vector("mean", mean, rows, f32), self._vector("rstd", rstd, rows, f32), pr, ldr, pdx,
-                          lddx, self._vector("dweight", dweight, self.H), self._vector("dbias", dbias, self.H),
-                          self._stream(stream))
+                          lddx, self._vector("dweight", dweight, H, dt), self._vector("dbias", dbias, H, dt),
+                          self._stream(stream, x))
         return dx
 
 
@@ -202,10 +203,9 @@ class MlpLinear(_Layer):
     to `rows` rows.  W is [K, gN] (g = 2 for swiglu: gate, then up)."""
 
     def __init__(self, rows: int, K: int, N: int, act: str = "none", dtype: str = "f16"):
-        self.rows, self.K, self.N = int(rows), int(K), int(N)
-        self.act, self.dtype = act, dtype
+        self.rows, self.K, self.N, self.act = int(rows), int(K), int(N), act
         self.gN = self.N * (2 if act == "swiglu" else 1)
-        self.torch_dtype = _storage(dtype)
+        self._set_type(dtype)
         self.h = mlp_linear_create(rows, K, N, ACTS[act], DTYPES[dtype])
 
     _destroy = staticmethod(mlp_linear_destroy)
@@ -218,8 +218,8 @@ class MlpLinear(_Layer):
         pr, ldr = self._rows("residual", residual, rows, self.N)
         py, ldy = self._rows("out", out, rows, self.N)
         pz, ldz = self._rows("z", z, rows, self.gN)
-        mlp_linear_forward(self.h, rows, px, ldx, pw, ldw, self._vector("bias", bias, self.gN), pr, ldr, py, ldy,
-                           pz, ldz, self._stream(stream))
+        mlp_linear_forward(self.h, rows, px, ldx, pw, ldw, self._vector("bias", bias, self.gN, self.torch_dtype), pr,
+                           ldr, py, ldy, pz, ldz, self._stream(stream, x))
         return out
 
     def backward(self, dy, x, w, dx=None, dw=None, db=None, z=None, stream=None):
@@ -232,9 +232,8 @@ class MlpLinear(_Layer):
         pz, ldz = self._rows("z", z, rows, self.gN)
         pdx, lddx = self._rows("dx", dx, rows, self.K)
         pdw, lddw = self._rows("dw", dw, self.K, self.gN)
-        pdb = self._vector("db", db, self.gN)
-        mlp_linear_backward(self.h, rows, pdy, lddy, px, ldx, pw, ldw, pz, ldz, pdx, lddx, pdw, lddw, pdb,
-                            self._stream(stream))
+        mlp_linear_backward(self.h, rows, pdy, lddy, px, ldx, pw, ldw, pz, ldz, pdx, lddx, pdw, lddw,
+                            self._vector("db", db, self.gN, self.torch_dtype), self._stream(stream, dy))
         return dx, dw, db
 
 
