@@ -156,26 +156,28 @@ Plan make_plan(int cfg, int64_t M, int64_t N, int64_t K, uint32_t split) {
 
 bool plan_fits(const Plan& p) { return p.part_bytes <= MAX_PART_BYTES; }
 
-// Estimated microseconds of a plan, from sweeps of every configuration and
-// split over the package's sizes.  A workgroup takes `slab` microseconds per
-// 64-deep slab with the chip busy (16 x 128 and 64 x 128 tiles: two on a CU
-// take less each than one alone) and `fixed` for its prologue and epilogue.
-// Where operands come from memory, the workgroups running at once share
-// about 5 TB/s.  A split adds a launch and the partials' way out and back.
+// Estimated microseconds of a plan, fitted to sweeps of every configuration
+// and split over the package's sizes and rows from 1 to 8192 (on those the
+// cheapest plan by this estimate is within 10% of the fastest measured, most
+// within 1%).  A workgroup takes `slab` microseconds per 64-deep slab of the
+// busy chip, `alone` times that with one workgroup per CU, and `fixed` for its
+// prologue and epilogue.  Operands that no other running workgroup reads too
+// arrive at 7.1 MB per microsecond in all and 36 KB per CU (caches included).
+// A split adds a launch and the partials' way out and back.  Small products
+// take no less than the host's time for their launches.
 double plan_cost(const Plan& p, int64_t M, int64_t N, int cus) {
-    static const double slab[] = {0.37, 0.40, 0.57, 0.93, 1.52}, fixed[] = {2.0, 2.0, 2.5, 3.0, 4.5};
+    static const double slab[] = {0.349, 0.391, 0.511, 0.757, 1.277, 0.779, 0.553};
+    static const double alone[] = {1.09, 1.27, 1.07, 1.02, 1.0, 1.05, 1.35};
+    static const double fixed[] = {1.9, 1.7, 3.2, 4.1, 6.8, 3.7, 1.7};
     const mlpc::LinearCfgInfo c = mlpc_linear_config(p.cfg);
     const double parts = (double)p.Mt * p.Nt * p.S;
     const double rounds = ceil(parts / cus), active = parts < cus ? parts : cus;
-    // bytes per slab that are not another running workgroup's too
     const double bytes = 128.0 * ((double)c.BN / p.Mt + (double)c.BM / p.Nt);
-    double t = slab[p.cfg];
-    if (p.cfg <= 1 && rounds < 2) t *= 1.3;
-    const double mem = bytes * active / 5.0e6;
-    if (mem > t) t = mem;
-    double cost = rounds * (fixed[p.cfg] + p.ksp * t);
-    if (p.S > 1) cost += 4.0 + (double)M * N * 4 * p.S * 2 / 4.0e6;
-    return cost;
+    const double compute = slab[p.cfg] * (rounds < 2 ? alone[p.cfg] : 1.0);
+    const double memory = fmax(bytes * active / 7.1e6, bytes / 36.0e3);
+    double cost = rounds * (fixed[p.cfg] + p.ksp * fmax(compute, memory));
+    if (p.S > 1) cost += 3.3 + (double)M * N * 4 * p.S * 2 / 4.2e6;
+    return fmax(cost, p.S > 1 ? 9.0 : 6.0);
 }
 
 Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {

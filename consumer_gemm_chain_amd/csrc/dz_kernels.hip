@@ -1,9 +1,9 @@
 // dz_kernels.hip -- the activation's gradient dz = dy act'(z) of the linear
-// layer and the column sums of dz, its bias's gradient.
+// layer and the column sums of dz, its bias's gradient.  Bound by memory: dy
+// and z are read once, dz is written once for the two products that read it.
 #include <hip/hip_runtime.h>
 
 #include "block_launch.h"
-#include "chain_device.hpp"
 #include "linear_device.hpp"
 
 namespace mlpc {
@@ -20,51 +20,103 @@ __device__ __forceinline__ float gelu_tanh_grad(float z) {
     return z != z ? z : d;
 }
 
-// dz and the column sums of row group blockIdx.y, one dy column per thread.
-template <int DT>
+// A workgroup takes 256 columns (8 per thread) of one row group, 8 rows at a
+// time, with the columns' sums in registers.
+constexpr int DZ_COLS = 256, DZ_ROWS = 8;
+constexpr int DZ_PARTS = 64;
+
+template <int DT, int ACT>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.N) return;
+    constexpr int G = ACT == ACT_SWIGLU ? 2 : 1;
+    __shared__ float s[DZ_ROWS][DZ_COLS];
+    const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
+    const int c = blockIdx.x * DZ_COLS + lane * 8;
+    const bool in = c < a.N;
     const int64_t r0 = a.rows * blockIdx.y / a.parts, r1 = a.rows * (blockIdx.y + 1) / a.parts;
-    float t0 = 0.f, t1 = 0.f;
-    for (int64_t r = r0; r < r1; ++r) {
-        const float dy = widen<DT>(a.dy[r * a.lddy + c]);
-        float d0 = dy, d1 = 0.f;
-        if (a.act == ACT_GELU_TANH) d0 = dy * gelu_tanh_grad(widen<DT>(a.z[r * a.ldz + c]));
-        if (a.act == ACT_SWIGLU) {
-            const float gate = widen<DT>(a.z[r * a.ldz + c]), u = widen<DT>(a.z[r * a.ldz + a.N + c]);
-            const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(gate * -1.4426950408889634f));
-            d0 = dy * u * (s + gate * s * (1.f - s));
-            d1 = dy * gate * s;
-            a.dz[r * a.lddz + a.N + c] = to_storage<DT>(d1);
+    float sum[G][8] = {};
+    if (in) {
+#pragma unroll 2
+        for (int64_t r = r0 + sub; r < r1; r += DZ_ROWS) {
+            float d[G][8];
+            widen8<DT>(ld16(a.dy + r * a.lddy + c), d[0]);
+            if constexpr (ACT == ACT_GELU_TANH) {
+                float z[8];
+                widen8<DT>(ld16(a.z + r * a.ldz + c), z);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) d[0][k] *= gelu_tanh_grad(z[k]);
+            }
+            if constexpr (ACT == ACT_SWIGLU) {
+                float gate[8], up[8];
+                widen8<DT>(ld16(a.z + r * a.ldz + c), gate);
+                widen8<DT>(ld16(a.z + r * a.ldz + a.N + c), up);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float dy = d[0][k], q = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(gate[k] * -1.4426950408889634f));
+                    d[0][k] = dy * up[k] * (q + gate[k] * q * (1.f - q));
+                    d[1][k] = dy * gate[k] * q;
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                if constexpr (ACT != ACT_NONE) st16(a.dz + r * a.lddz + g * a.N + c, narrow8<DT>(d[g]));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[g][k] += d[g][k];
+            }
         }
-        if (a.dz) a.dz[r * a.lddz + c] = to_storage<DT>(d0);
-        t0 += d0;
-        t1 += d1;
     }
     if (!a.db) return;
-    const int gN = a.act == ACT_SWIGLU ? 2 * a.N : a.N;
-    a.part[(size_t)blockIdx.y * gN + c] = t0;
-    if (gN > a.N) a.part[(size_t)blockIdx.y * gN + a.N + c] = t1;
+    const int j = threadIdx.x, col = blockIdx.x * DZ_COLS + j;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[sub][lane * 8 + k] = sum[g][k];
+        __syncthreads();
+        if (col >= a.N) continue;
+        float t = s[0][j];
+#pragma unroll
+        for (int k = 1; k < DZ_ROWS; ++k) t += s[k][j];
+        if (a.parts == 1) a.db[g * a.N + col] = to_storage<DT>(t);
+        else a.part[(size_t)blockIdx.y * G * a.N + g * a.N + col] = t;
+    }
 }
 
-// The row groups' column sums added in group order.
+// The row groups' column sums added in a fixed order: 32 columns by 8 groups
+// of row groups, joined through LDS.
 template <int DT>
-__global__ __launch_bounds__(256) void db_kernel(DzArgs a) {
-    const int gN = a.act == ACT_SWIGLU ? 2 * a.N : a.N;
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= gN) return;
-    float t = 0.f;
-    for (int p = 0; p < a.parts; ++p) t += a.part[(size_t)p * gN + c];
-    a.db[c] = to_storage<DT>(t);
+__global__ __launch_bounds__(256) void db_kernel(DzArgs a, int n) {
+    __shared__ float s[8][33];
+    const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float v[DZ_PARTS / 8], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < DZ_PARTS / 8; ++k) {
+        const int p = k * 8 + group;
+        v[k] = p < a.parts && c < n ? a.part[(size_t)p * n + c] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < DZ_PARTS / 8; ++k) sum += v[k];
+    s[group][lane] = sum;
+    __syncthreads();
+    if (group != 0 || c >= n) return;
+    sum = 0.f;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) sum += s[g][lane];
+    a.db[c] = to_storage<DT>(sum);
 }
 
 template <int DT>
 static hipError_t dz_t(const DzArgs& a, hipStream_t s) {
-    const int gN = a.act == ACT_SWIGLU ? 2 * a.N : a.N;
-    if (a.parts > 0)
-        hipLaunchKernelGGL(dz_kernel<DT>, dim3((a.N + 255) / 256, a.parts), dim3(256), 0, s, a);
-    if (a.db) hipLaunchKernelGGL(db_kernel<DT>, dim3((gN + 255) / 256), dim3(256), 0, s, a);
+    const dim3 grid((a.N + DZ_COLS - 1) / DZ_COLS, a.parts);
+    if (a.parts > 0) {
+        if (a.act == ACT_NONE) hipLaunchKernelGGL((dz_kernel<DT, ACT_NONE>), grid, dim3(256), 0, s, a);
+        else if (a.act == ACT_GELU_TANH) hipLaunchKernelGGL((dz_kernel<DT, ACT_GELU_TANH>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((dz_kernel<DT, ACT_SWIGLU>), grid, dim3(256), 0, s, a);
+    }
+    if (a.db && a.parts != 1) {
+        const int n = a.act == ACT_SWIGLU ? 2 * a.N : a.N;
+        hipLaunchKernelGGL(db_kernel<DT>, dim3((n + 31) / 32), dim3(256), 0, s, a, n);
+    }
     return hipGetLastError();
 }
 
@@ -72,10 +124,16 @@ static hipError_t dz_t(const DzArgs& a, hipStream_t s) {
 
 using namespace mlpc;
 
+int mlpc_dz_max_parts() { return DZ_PARTS; }
+
+// Row groups: one while a workgroup takes at most 8 rows per thread (the
+// column sums then need no second kernel), else groups of about 32 rows.
+int mlpc_dz_parts(int64_t rows) {
+    if (rows <= 8 * DZ_ROWS) return rows > 0 ? 1 : 0;
+    const int64_t p = (rows + 31) / 32;
+    return (int)(p < DZ_PARTS ? p : DZ_PARTS);
+}
+
 hipError_t mlpc_dz(const DzArgs& a, int dtype, hipStream_t s) {
     return dtype == DT_F16 ? dz_t<DT_F16>(a, s) : dz_t<DT_BF16>(a, s);
 }
-
-int mlpc_dz_max_parts() { return 64; }
-
-int mlpc_dz_parts(int64_t rows) { return (int)(rows < 64 ? rows : 64); }

@@ -26,12 +26,22 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(GemmArgs p) {
         if (p.up) widen8<DT>(ld16(p.bias + p.up + n), bu);
     }
     auto sum = [&](const f32x4* q, float (&t)[8]) {
-        f32x4 lo = q[0], hi = q[1];
-#pragma unroll 4
-        for (uint32_t s = 1; s < p.S; ++s) {
-            const f32x4* qs = q + s * (size_t)(plane / 4);
-            lo = lo + qs[0];
-            hi = hi + qs[1];
+        // eight parts' loads in flight, added in part order
+        f32x4 lo = {}, hi = {};
+        for (uint32_t s0 = 0; s0 < p.S; s0 += 8) {
+            f32x4 l[8], h[8];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                if (s0 + k >= p.S) continue;
+                l[k] = q[(s0 + k) * (size_t)(plane / 4)];
+                h[k] = q[(s0 + k) * (size_t)(plane / 4) + 1];
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                if (s0 + k >= p.S) continue;
+                lo = lo + l[k];
+                hi = hi + h[k];
+            }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
