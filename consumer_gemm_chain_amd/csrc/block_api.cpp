@@ -22,11 +22,11 @@ struct mlp_norm {
     hipStream_t last_stream;
 };
 
-// How a product runs: tile configuration, tiles, parts of the reduction and
-// slabs per part.
+// How a product runs: tile configuration, tiles, the tiles computed whole, the
+// parts of the others' reduction and slabs per part.
 struct Plan {
     int cfg;
-    uint32_t Mt, Nt, S, ksp;
+    uint32_t Mt, Nt, direct, S, ksp;
     size_t part_bytes;
 };
 
@@ -138,19 +138,24 @@ constexpr size_t MAX_PART_BYTES = (size_t)64 << 20;
 constexpr uint32_t MAX_SPLIT = 32;
 
 // The plan of a product of M x N columns (both halves of swiglu's B) over K
-// with configuration cfg and at most `split` parts (no part is empty).
-Plan make_plan(int cfg, int64_t M, int64_t N, int64_t K, uint32_t split) {
+// with configuration cfg and at most `split` parts (no part is empty).  As
+// many tiles as fill whole rounds of the chip are never split, only those of
+// the last, partial round.
+Plan make_plan(int cfg, int64_t M, int64_t N, int64_t K, uint32_t split, int cus) {
     const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
     const uint32_t slabs = (uint32_t)(K / mlpc::BK);
     Plan p;
     p.cfg = cfg;
     p.Mt = (uint32_t)((M + c.BM - 1) / c.BM);
     p.Nt = (uint32_t)((N + c.BN - 1) / c.BN);
+    const uint32_t tiles = p.Mt * p.Nt;
     if (split > slabs) split = slabs;
     if (split < 1) split = 1;
     p.ksp = slabs ? (slabs + split - 1) / split : 0;
     p.S = slabs ? (slabs + p.ksp - 1) / p.ksp : 1;
-    p.part_bytes = p.S > 1 ? (size_t)M * N * p.S * 4 : 0;
+    p.direct = p.S > 1 ? tiles - tiles % (uint32_t)cus : 0;
+    if (p.direct == tiles) p.S = 1;
+    p.part_bytes = p.S > 1 ? (size_t)(tiles - p.direct) * p.S * c.BM * c.BN * 4 : 0;
     return p;
 }
 
@@ -162,22 +167,27 @@ bool plan_fits(const Plan& p) { return p.part_bytes <= MAX_PART_BYTES; }
 // within 1%).  A workgroup takes `slab` microseconds per 64-deep slab of the
 // busy chip, `alone` times that with one workgroup per CU, and `fixed` for its
 // prologue and epilogue.  Operands that no other running workgroup reads too
-// arrive at 7.1 MB per microsecond in all and 36 KB per CU (caches included).
+// arrive at 7.0 MB per microsecond in all and 36 KB per CU (caches included).
 // A split adds a launch and the partials' way out and back.  Small products
 // take no less than the host's time for their launches.
-double plan_cost(const Plan& p, int64_t M, int64_t N, int cus) {
-    static const double slab[] = {0.349, 0.391, 0.511, 0.757, 1.277, 0.779, 0.553};
-    static const double alone[] = {1.09, 1.27, 1.07, 1.02, 1.0, 1.05, 1.35};
-    static const double fixed[] = {1.9, 1.7, 3.2, 4.1, 6.8, 3.7, 1.7};
+double plan_cost(const Plan& p, int64_t M, int64_t N, int64_t K, int cus) {
+    static const double slab[] = {0.36, 0.38, 0.54, 0.815, 1.38, 0.88, 0.60};
+    static const double alone[] = {1.10, 1.36, 1.0, 1.03, 1.0, 1.0, 1.19};
+    static const double fixed[] = {1.8, 1.2, 3.9, 6.1, 8.9, 5.6, 1.8};
     const mlpc::LinearCfgInfo c = mlpc_linear_config(p.cfg);
-    const double parts = (double)p.Mt * p.Nt * p.S;
-    const double rounds = ceil(parts / cus), active = parts < cus ? parts : cus;
+    const uint32_t slabs = (uint32_t)(K / mlpc::BK), tiles = p.Mt * p.Nt;
     const double bytes = 128.0 * ((double)c.BN / p.Mt + (double)c.BM / p.Nt);
-    const double compute = slab[p.cfg] * (rounds < 2 ? alone[p.cfg] : 1.0);
-    const double memory = fmax(bytes * active / 7.1e6, bytes / 36.0e3);
-    double cost = rounds * (fixed[p.cfg] + p.ksp * fmax(compute, memory));
-    if (p.S > 1) cost += 3.3 + (double)M * N * 4 * p.S * 2 / 4.2e6;
-    return fmax(cost, p.S > 1 ? 9.0 : 6.0);
+    // rounds of `count` workgroups of `n` slabs each
+    auto rounds = [&](double count, uint32_t n) {
+        const double r = ceil(count / cus), active = count < cus ? count : cus;
+        const double compute = slab[p.cfg] * (tiles * p.S <= (uint32_t)cus ? alone[p.cfg] : 1.0);
+        return r * (fixed[p.cfg] + n * fmax(compute, fmax(bytes * active / 7.0e6, bytes / 36.0e3)));
+    };
+    if (p.S == 1) return fmax(rounds(tiles, slabs), 6.0);
+    const double split = tiles - p.direct;
+    const double values = split * c.BM * c.BN * fmin(1.0, (double)M / ((double)p.Mt * c.BM)) * fmin(1.0, (double)N / ((double)p.Nt * c.BN));
+    const double cost = rounds(p.direct, slabs) + rounds(split * p.S, p.ksp) + 2.3 + values * 4 * p.S * 2 / 3.9e6;
+    return fmax(cost, 9.0);
 }
 
 Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {
@@ -188,11 +198,11 @@ Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {
         if (!mlpc_linear_has(cfg, pass)) continue;
         uint32_t last = 0;
         for (uint32_t split = 1; split <= MAX_SPLIT; ++split) {
-            const Plan p = make_plan(cfg, M, N, K, split);
+            const Plan p = make_plan(cfg, M, N, K, split, cus);
             if (p.S == last) continue;
             last = p.S;
             if (!plan_fits(p)) break;
-            const double c = plan_cost(p, M, N, cus);
+            const double c = plan_cost(p, M, N, K, cus);
             if (!found || c < cost) {
                 best = p;
                 cost = c;
@@ -213,13 +223,16 @@ void pass_sizes(int pass, int64_t rows, int64_t K, int64_t gN, int64_t* m, int64
 // Largest split workspace of any plan for up to max_rows rows.
 size_t max_part_bytes(int64_t max_rows, int64_t K, int64_t gN) {
     size_t most = 0;
-    for (int pass = 0; pass < 3; ++pass) {
-        int64_t m, n, k;
-        pass_sizes(pass, max_rows, K, gN, &m, &n, &k);
-        const size_t slabs = (size_t)(k / mlpc::BK);
-        const size_t b = slabs > 1 ? (size_t)m * n * 4 * (slabs < MAX_SPLIT ? slabs : MAX_SPLIT) : 0;
-        if (b > most) most = b;
-    }
+    for (int pass = 0; pass < 3; ++pass)
+        for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
+            int64_t m, n, k;
+            pass_sizes(pass, max_rows, K, gN, &m, &n, &k);
+            const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
+            const size_t tiles = (size_t)((m + c.BM - 1) / c.BM) * (size_t)((n + c.BN - 1) / c.BN);
+            const size_t slabs = (size_t)(k / mlpc::BK);
+            const size_t b = slabs > 1 ? tiles * (slabs < MAX_SPLIT ? slabs : MAX_SPLIT) * c.BM * c.BN * 4 : 0;
+            if (b > most) most = b;
+        }
     return most < MAX_PART_BYTES ? most : MAX_PART_BYTES;
 }
 
@@ -228,7 +241,7 @@ int run_product(mlp_linear* h, int pass, int64_t rows, mlpc::GemmArgs& a, hipStr
     if (h->plan_rows[pass] != rows) {
         h->plan[pass] = h->forced_cfg[pass] < 0
                             ? choose_plan(a.M, n, a.K, pass, h->cus)
-                            : make_plan(h->forced_cfg[pass], a.M, n, a.K, (uint32_t)h->forced_split[pass]);
+                            : make_plan(h->forced_cfg[pass], a.M, n, a.K, (uint32_t)h->forced_split[pass], h->cus);
         h->plan_rows[pass] = rows;
     }
     const Plan& p = h->plan[pass];
@@ -236,8 +249,12 @@ int run_product(mlp_linear* h, int pass, int64_t rows, mlpc::GemmArgs& a, hipStr
         return fail(MLP_EINVAL, "the split needs %zu workspace bytes of %zu", p.part_bytes, h->part_bytes);
     a.Mt = p.Mt;
     a.Nt = p.Nt;
+    a.direct = p.direct;
     a.S = p.S;
     a.ksp = p.ksp;
+    const mlpc::LinearCfgInfo c = mlpc_linear_config(p.cfg);
+    a.BM = c.BM;
+    a.BN = c.BN;
     a.part = h->part;
     a.zero = h->zero;
     hipError_t e = mlpc_gemm(a, p.cfg, pass, h->dtype, s);
@@ -551,8 +568,8 @@ int mlp_linear_plan(int64_t rows, int64_t K, int64_t N, int act, int pass, int c
     pass_sizes(pass, rows, K, act == MLP_ACT_SWIGLU ? 2 * N : N, &m, &nn, &k);
     const Plan p = choose_plan(m, nn, k, pass, cus);
     const mlpc::LinearCfgInfo c = mlpc_linear_config(p.cfg);
-    const int64_t v[8] = {p.cfg, p.S, c.BM, c.BN, p.Mt, p.Nt, p.ksp, (int64_t)p.part_bytes};
-    for (int i = 0; i < n && i < 8; ++i) plan[i] = v[i];
+    const int64_t v[9] = {p.cfg, p.S, c.BM, c.BN, p.Mt, p.Nt, p.ksp, (int64_t)p.part_bytes, p.direct};
+    for (int i = 0; i < n && i < 9; ++i) plan[i] = v[i];
     return MLP_OK;
 }
 

@@ -45,9 +45,11 @@ struct GemmArgs {
     const uint16_t* res;        // nullptr: none
     uint16_t* z;                // nullptr: not saved
     int64_t ldr, ldz;
-    // plan: tiles, parts of each tile's reduction and slabs per part
-    uint32_t Mt, Nt, S, ksp;
-    float* part;                // [S][M][columns] (S > 1)
+    // plan: tiles; the first `direct` of the tile order are computed whole,
+    // the others in S parts of ksp slabs
+    uint32_t Mt, Nt, direct, S, ksp;
+    int BM, BN;                 // the configuration's tile
+    float* part;                // [Mt * Nt - direct][S][BM][BN] (S > 1)
     const void* zero;           // 16 zero bytes
 };
 

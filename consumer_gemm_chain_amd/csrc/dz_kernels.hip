@@ -20,15 +20,16 @@ __device__ __forceinline__ float gelu_tanh_grad(float z) {
     return z != z ? z : d;
 }
 
-// A workgroup takes 256 columns (8 per thread) of one row group, 8 rows at a
-// time, with the columns' sums in registers.
-constexpr int DZ_COLS = 256, DZ_ROWS = 8;
+// A workgroup takes 256 columns (8 per thread) of one row group, ROWS rows at
+// a time, with the columns' sums in registers: 8 rows, or 32 (1024 threads)
+// where one row group is the whole batch.
+constexpr int DZ_COLS = 256;
 constexpr int DZ_PARTS = 64;
 
-template <int DT, int ACT>
-__global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
+template <int DT, int ACT, int ROWS>
+__global__ __launch_bounds__(ROWS * 32) void dz_kernel(DzArgs a) {
     constexpr int G = ACT == ACT_SWIGLU ? 2 : 1;
-    __shared__ float s[DZ_ROWS][DZ_COLS];
+    __shared__ float s[ROWS][DZ_COLS];
     const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
     const int c = blockIdx.x * DZ_COLS + lane * 8;
     const bool in = c < a.N;
@@ -36,7 +37,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
     float sum[G][8] = {};
     if (in) {
 #pragma unroll 2
-        for (int64_t r = r0 + sub; r < r1; r += DZ_ROWS) {
+        for (int64_t r = r0 + sub; r < r1; r += ROWS) {
             float d[G][8];
             widen8<DT>(ld16(a.dy + r * a.lddy + c), d[0]);
             if constexpr (ACT == ACT_GELU_TANH) {
@@ -72,10 +73,10 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) s[sub][lane * 8 + k] = sum[g][k];
         __syncthreads();
-        if (col >= a.N) continue;
+        if (j >= DZ_COLS || col >= a.N) continue;
         float t = s[0][j];
-#pragma unroll
-        for (int k = 1; k < DZ_ROWS; ++k) t += s[k][j];
+#pragma unroll 8
+        for (int k = 1; k < ROWS; ++k) t += s[k][j];
         if (a.parts == 1) a.db[g * a.N + col] = to_storage<DT>(t);
         else a.part[(size_t)blockIdx.y * G * a.N + g * a.N + col] = t;
     }
@@ -105,13 +106,19 @@ __global__ __launch_bounds__(256) void db_kernel(DzArgs a, int n) {
     a.db[c] = to_storage<DT>(sum);
 }
 
+template <int DT, int ACT>
+static void dz_launch(const DzArgs& a, hipStream_t s) {
+    const dim3 grid((a.N + DZ_COLS - 1) / DZ_COLS, a.parts);
+    if (a.parts == 1 && a.rows > 8) hipLaunchKernelGGL((dz_kernel<DT, ACT, 32>), grid, dim3(1024), 0, s, a);
+    else hipLaunchKernelGGL((dz_kernel<DT, ACT, 8>), grid, dim3(256), 0, s, a);
+}
+
 template <int DT>
 static hipError_t dz_t(const DzArgs& a, hipStream_t s) {
-    const dim3 grid((a.N + DZ_COLS - 1) / DZ_COLS, a.parts);
     if (a.parts > 0) {
-        if (a.act == ACT_NONE) hipLaunchKernelGGL((dz_kernel<DT, ACT_NONE>), grid, dim3(256), 0, s, a);
-        else if (a.act == ACT_GELU_TANH) hipLaunchKernelGGL((dz_kernel<DT, ACT_GELU_TANH>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((dz_kernel<DT, ACT_SWIGLU>), grid, dim3(256), 0, s, a);
+        if (a.act == ACT_NONE) dz_launch<DT, ACT_NONE>(a, s);
+        else if (a.act == ACT_GELU_TANH) dz_launch<DT, ACT_GELU_TANH>(a, s);
+        else dz_launch<DT, ACT_SWIGLU>(a, s);
     }
     if (a.db && a.parts != 1) {
         const int n = a.act == ACT_SWIGLU ? 2 * a.N : a.N;
@@ -126,10 +133,11 @@ using namespace mlpc;
 
 int mlpc_dz_max_parts() { return DZ_PARTS; }
 
-// Row groups: one while a workgroup takes at most 8 rows per thread (the
-// column sums then need no second kernel), else groups of about 32 rows.
+// Row groups: one up to 128 rows (the column sums then need no second kernel,
+// and its launch costs more than the few rows per thread), else groups of
+// about 32 rows.
 int mlpc_dz_parts(int64_t rows) {
-    if (rows <= 8 * DZ_ROWS) return rows > 0 ? 1 : 0;
+    if (rows <= 128) return rows > 0 ? 1 : 0;
     const int64_t p = (rows + 31) / 32;
     return (int)(p < DZ_PARTS ? p : DZ_PARTS);
 }

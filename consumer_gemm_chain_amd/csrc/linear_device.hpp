@@ -423,59 +423,68 @@ __device__ __forceinline__ void linear_epilogue(const f32x4 (&acc)[C::FM][C::FN]
     });
 }
 
-// A part's fp32 accumulators to its plane of the partials [S][M][gN] (swiglu:
-// gate and up columns where W has them).
+// A part's fp32 accumulators to its tile of the partials, columns in the
+// order of the tile's B columns.
 template <class C>
 __device__ __forceinline__ void store_part(const f32x4 (&acc)[C::FM][C::FN], const GemmArgs& p, int m0, int n0,
-                                           uint32_t s) {
+                                           uint32_t slot) {
     const int lane = threadIdx.x & 63, wave = uniform_wave();
-    const int g = lane >> 4, m = m0 + wave / C::WN * C::WTM + (lane & 15);
-    const int64_t ld = p.N + p.up;
-    float* part = p.part + (size_t)s * p.M * ld;
+    const int g = lane >> 4, row = wave / C::WN * C::WTM + (lane & 15), col = wave % C::WN * C::WTN + g * 4;
+    float* part = p.part + (size_t)slot * C::BM * C::BN;
 #pragma unroll
     for (int f = 0; f < C::FN; ++f) {
         const int frag = wave % C::WN * C::FN + f;
-        const int n = (p.up ? n0 + (frag >> 1) * 16 : n0 + frag * 16) + g * 4;
-        if (n >= p.N) continue;
+        if ((p.up ? n0 + (frag >> 1) * 16 : n0 + frag * 16) + g * 4 >= p.N) continue;
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
-            if (m + i * 16 < p.M)
-                *reinterpret_cast<f32x4*>(part + (size_t)(m + i * 16) * ld + n + (p.up ? (frag & 1) * p.up : 0)) = acc[i][f];
+            if (m0 + row + i * 16 < p.M)
+                *reinterpret_cast<f32x4*>(part + (row + i * 16) * C::BN + col + f * 16) = acc[i][f];
     }
 }
 
-// Workgroup b -> part, tile row and tile column.  The dispatcher deals
-// workgroups to the 8 XCDs in turn; each XCD gets one contiguous chunk of the
-// tile order, which walks patches of PATCH row blocks column by column, so
-// the ~32 tiles an XCD runs at a time share few operand panels in its L2.
+// Tile i of the order -> tile row and column: patches of PATCH row blocks,
+// column by column, so the ~32 tiles an XCD runs at a time share few operand
+// panels in its L2.
 constexpr uint32_t PATCH = 4;
 
-__device__ __forceinline__ void tile_position(const GemmArgs& p, uint32_t b, uint32_t& mb, uint32_t& nb, uint32_t& s) {
-    const uint32_t t = xcd_chunked(b, p.Mt * p.Nt * p.S);
-    s = t % p.S;
-    const uint32_t i = t / p.S, band = i / (PATCH * p.Nt), j = i - band * PATCH * p.Nt;
+__device__ __forceinline__ void tile_at(const GemmArgs& p, uint32_t i, uint32_t& mb, uint32_t& nb) {
+    const uint32_t band = i / (PATCH * p.Nt), j = i - band * PATCH * p.Nt;
     const uint32_t h = p.Mt - band * PATCH < PATCH ? p.Mt - band * PATCH : PATCH;
     mb = band * PATCH + j % h;
     nb = j / h;
 }
 
+// Workgroup b -> tile of the order and part (whole tiles first).  The
+// dispatcher deals workgroups to the 8 XCDs in turn; each XCD gets one
+// contiguous chunk of the order.
+__device__ __forceinline__ uint32_t tile_of(const GemmArgs& p, uint32_t b, uint32_t& s) {
+    s = 0;
+    if (b < p.direct) return xcd_chunked(b, p.direct);
+    const uint32_t q = xcd_chunked(b - p.direct, (p.Mt * p.Nt - p.direct) * p.S);
+    s = q % p.S;
+    return p.direct + q / p.S;
+}
+
 template <class C, int DT, int PASS>
 __global__ __launch_bounds__(C::NT, C::OCC) void linear_kernel(GemmArgs p) {
     uint32_t mb, nb, s;
-    tile_position(p, blockIdx.x, mb, nb, s);
+    const uint32_t i = tile_of(p, blockIdx.x, s);
+    tile_at(p, i, mb, nb);
+    const bool whole = i < p.direct || p.S == 1;
     const int m0 = mb * C::BM, n0 = nb * (p.up ? C::BN / 2 : C::BN);
     f32x4 acc[C::FM][C::FN] = {};
     {
         LinTile<C, PASS> t;
         t.a.init(p.a, p.lda, m0, p.M, 0);
         t.b.init(p.b, p.ldb, n0, p.N, p.up);
-        const int slabs = p.K / BK, k0 = min((int)(s * p.ksp), slabs), k1 = min(k0 + (int)p.ksp, slabs);
+        const int slabs = p.K / BK;
+        const int k0 = whole ? 0 : min((int)(s * p.ksp), slabs), k1 = whole ? slabs : min(k0 + (int)p.ksp, slabs);
         if (k1 > k0) t.template kloop<DT>(acc, k0 * C::SPS, k1 * C::SPS);
-        if (s + 1 == p.S && p.K % BK) t.template tail<DT>(acc, slabs, p);
+        if ((whole || s + 1 == p.S) && p.K % BK) t.template tail<DT>(acc, slabs, p);
         ring_barrier<0>();      // no DMA in flight when the workgroup ends
     }
-    if (p.S > 1) store_part<C>(acc, p, m0, n0, s);
-    else linear_epilogue<C, DT, PASS>(acc, p, m0, n0);
+    if (whole) linear_epilogue<C, DT, PASS>(acc, p, m0, n0);
+    else store_part<C>(acc, p, m0, n0, (i - p.direct) * p.S + s);
 }
 
 }  // namespace mlpc

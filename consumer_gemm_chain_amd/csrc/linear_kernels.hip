@@ -18,7 +18,7 @@ static constexpr bool has(int pass) { return pass != PASS_DW || Cfg::BM >= 128; 
 
 template <int DT>
 static hipError_t launch(const GemmArgs& a, int pass, hipStream_t s) {
-    const dim3 grid(a.Mt * a.Nt * a.S);
+    const dim3 grid(a.direct + (a.Mt * a.Nt - a.direct) * a.S);
     switch (pass) {
     case PASS_FWD: hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_FWD>), grid, dim3(Cfg::NT), 0, s, a); break;
     case PASS_DX: hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_DX>), grid, dim3(Cfg::NT), 0, s, a); break;

@@ -7,18 +7,22 @@
 
 namespace mlpc {
 
-// Eight output columns per thread.  A kernel of its own rather than the last
-// part of each tile: it needs no counters and no agent-scope fences, and the
-// whole chip reads the partials.
+// A workgroup takes 256 chunks of eight output columns of one split tile.  A
+// kernel of its own rather than the last part of each tile: it needs no
+// counters and no agent-scope fences, and the whole chip reads the partials.
 template <int DT>
-__global__ __launch_bounds__(256) void linear_reduce_kernel(GemmArgs p) {
-    const int chunks = p.N / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)p.M * chunks) return;
-    const int64_t r = i / chunks;
-    const int n = (int)(i % chunks) * 8;
-    const int64_t ld = p.N + p.up, plane = p.M * ld;
-    const f32x4* src = reinterpret_cast<const f32x4*>(p.part + r * ld + n);
+__global__ __launch_bounds__(256) void linear_reduce_kernel(GemmArgs p, int per_tile) {
+    const uint32_t tile = blockIdx.x / per_tile;
+    const int chunk = (int)(blockIdx.x % per_tile) * 256 + threadIdx.x;
+    const int width = p.up ? p.BN / 2 : p.BN, row = chunk / (width / 8), oc = chunk % (width / 8) * 8;
+    uint32_t mb, nb;
+    tile_at(p, p.direct + tile, mb, nb);
+    const int r = mb * p.BM + row, n = nb * width + oc;
+    if (row >= p.BM || r >= p.M || n >= p.N) return;
+    const size_t plane = (size_t)p.BM * p.BN / 4;
+    // gate and up columns alternate in 16s
+    const int col = p.up ? (oc >> 4) * 32 + (oc & 15) : oc;
+    const f32x4* src = reinterpret_cast<const f32x4*>(p.part) + tile * p.S * plane + (row * p.BN + col) / 4;
     const u32x4 res = p.res ? ld16(p.res + (size_t)r * p.ldr + n) : u32x4{};
     float b[8] = {}, bu[8] = {}, v[8], u[8];
     if (p.bias) {
@@ -33,8 +37,8 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(GemmArgs p) {
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) {
                 if (s0 + k >= p.S) continue;
-                l[k] = q[(s0 + k) * (size_t)(plane / 4)];
-                h[k] = q[(s0 + k) * (size_t)(plane / 4) + 1];
+                l[k] = q[(s0 + k) * plane];
+                h[k] = q[(s0 + k) * plane + 1];
             }
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) {
@@ -50,7 +54,7 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(GemmArgs p) {
         }
     };
     sum(src, v);
-    if (p.up) sum(src + p.up / 4, u);
+    if (p.up) sum(src + 4, u);
     finish8<DT>(p, r, n, v, u, b, bu, res);
 }
 
@@ -59,8 +63,11 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(GemmArgs p) {
 using namespace mlpc;
 
 hipError_t mlpc_gemm_reduce(const GemmArgs& a, int dtype, hipStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)a.M * (a.N / 8) + 255) / 256));
-    if (dtype == DT_F16) hipLaunchKernelGGL(linear_reduce_kernel<DT_F16>, grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(linear_reduce_kernel<DT_BF16>, grid, dim3(256), 0, s, a);
+    // (rows past M, as in the one tile row of a short product, are not launched)
+    const int rows = a.M < a.BM ? a.M : a.BM, chunks = rows * ((a.up ? a.BN / 2 : a.BN) / 8);
+    const int per_tile = (chunks + 255) / 256;
+    const dim3 grid((a.Mt * a.Nt - a.direct) * per_tile);
+    if (dtype == DT_F16) hipLaunchKernelGGL(linear_reduce_kernel<DT_F16>, grid, dim3(256), 0, s, a, per_tile);
+    else hipLaunchKernelGGL(linear_reduce_kernel<DT_BF16>, grid, dim3(256), 0, s, a, per_tile);
     return hipGetLastError();
 }

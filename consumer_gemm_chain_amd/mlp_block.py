@@ -15,7 +15,7 @@ EXPORTS = ("mlp_norm_create", "mlp_norm_forward", "mlp_norm_backward", "mlp_norm
            "mlp_linear_create", "mlp_linear_forward", "mlp_linear_backward", "mlp_linear_destroy",
            "mlp_linear_plan", "mlp_linear_debug_set_plan")
 
-PLAN_FIELDS = ("config", "S", "BM", "BN", "Mt", "Nt", "ksp", "part_bytes")
+PLAN_FIELDS = ("config", "S", "BM", "BN", "Mt", "Nt", "ksp", "part_bytes", "direct")
 
 _lib = None
 

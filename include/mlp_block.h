@@ -119,16 +119,17 @@ int mlp_linear_destroy(mlp_linear_t h);
 
 /* The plan a call of `rows` rows makes on a GPU with `cus` compute units for
  * pass 0 (x W), 1 (dz W^T) or 2 (x^T dz), computed on the host alone: fills
- * the first min(n, 8) of
- *   { config id, parts of the reduction, BM, BN, tile rows, tile columns,
- *     64-deep slabs per part, workspace bytes of the partials }.
+ * the first min(n, 9) of
+ *   { config id, parts of a split tile's reduction, BM, BN, tile rows, tile
+ *     columns, 64-deep slabs per part, workspace bytes of the partials, tiles
+ *     computed whole although the others are split }.
  * Returns MLP_EINVAL for sizes mlp_linear_create would reject, an unknown
  * pass, cus < 8, a NULL array or n < 3. */
 int mlp_linear_plan(int64_t rows, int64_t K, int64_t N, int act, int pass, int cus, int64_t* plan, int n);
 
 /* Test and measurement hook: run `pass` of the handle's later calls with tile
- * configuration `config_id` and its reduction in at most `split` parts (0 or
- * 1: one); config_id -1 and split 0 restore the planner's choice.  A call
+ * configuration `config_id` and the reduction of the tiles of the last, partial
+ * round in at most `split` parts (0 or 1: one); config_id -1 and split 0 restore the planner's choice.  A call
  * whose partials exceed the handle's workspace is then refused.  Returns
  * MLP_EINVAL for a NULL handle, a configuration the pass does not have or a
  * split outside 0..32. */
