@@ -18,7 +18,7 @@ struct mlp_norm {
     int dtype;
     int device, cus;
     float eps;
-    float* part;                // [max parts][2][H]
+    float* part;                // [max parts][2][H]; nullptr: no gradient
     hipStream_t last_stream;
 };
 
@@ -38,7 +38,8 @@ struct mlp_linear {
     int64_t plan_rows[3];                   // the row count plan[pass] is for (-1: none)
     Plan plan[3];
     // workspace (one allocation): zero page | dz [max_rows, gN] (activations
-    // only) | column-sum partials [max parts][gN] | split partials
+    // only) | column-sum partials [max parts][gN] | split partials; dz and the
+    // column sums only with the gradient
     void* ws;
     void* zero;
     uint16_t* dz;
@@ -132,9 +133,7 @@ int launched(hipError_t e) {
 
 // ------------------------------------------------------------------ planner
 
-// Workspace a split product may take for its partials, and the parts a
-// reduction may have.
-constexpr size_t MAX_PART_BYTES = (size_t)64 << 20;
+// Parts a reduction may have.
 constexpr uint32_t MAX_SPLIT = 32;
 
 // The plan of a product of M x N columns (both halves of swiglu's B) over K
@@ -159,21 +158,29 @@ Plan make_plan(int cfg, int64_t M, int64_t N, int64_t K, uint32_t split, int cus
     return p;
 }
 
-bool plan_fits(const Plan& p) { return p.part_bytes <= MAX_PART_BYTES; }
+// What the planner considers: tiles of at most twice the rows (64-row tiles
+// always), and splits into at most one part per CU.  More never were fastest,
+// and the limits bound the workspace of the partials.
+bool config_fits(const mlpc::LinearCfgInfo& c, int64_t M) { return c.BM <= 64 || c.BM <= 2 * M; }
+
+bool split_fits(const Plan& p, int cus) { return p.S == 1 || (p.Mt * p.Nt - p.direct) * p.S <= (uint32_t)cus; }
 
 // Estimated microseconds of a plan, fitted to sweeps of every configuration
-// and split over the package's sizes and rows from 1 to 8192 (on those the
-// cheapest plan by this estimate is within 10% of the fastest measured, most
-// within 1%).  A workgroup takes `slab` microseconds per 64-deep slab of the
-// busy chip, `alone` times that with one workgroup per CU, and `fixed` for its
-// prologue and epilogue.  Operands that no other running workgroup reads too
-// arrive at 7.0 MB per microsecond in all and 36 KB per CU (caches included).
-// A split adds a launch and the partials' way out and back.  Small products
-// take no less than the host's time for their launches.
+// and split over the package's sizes and rows from 1 to 8192 (the cheapest
+// plan by this estimate is within 6% of the fastest measured on all but one of
+// them).  A workgroup takes `slab` microseconds per 64-deep slab with several
+// rounds of workgroups, `alone` times that with a single one, and `fixed` for
+// its prologue and epilogue.  Operands that no other running workgroup reads
+// too arrive at 6.8 MB per microsecond in all and 35 KB per CU (caches
+// included).  The chip's power caps the multiplication rate whatever the
+// schedule: `cap` MFLOP per microsecond.  A split adds a launch and the
+// partials' way out and back.  Small products take no less than the host's
+// time for their launches.
 double plan_cost(const Plan& p, int64_t M, int64_t N, int64_t K, int cus) {
-    static const double slab[] = {0.36, 0.38, 0.54, 0.815, 1.38, 0.88, 0.60};
-    static const double alone[] = {1.10, 1.36, 1.0, 1.03, 1.0, 1.0, 1.19};
-    static const double fixed[] = {1.8, 1.2, 3.9, 6.1, 8.9, 5.6, 1.8};
+    static const double slab[] = {0.36, 0.38, 0.54, 0.84, 1.42, 0.98, 0.61};
+    static const double alone[] = {1.07, 1.31, 0.96, 0.92, 0.91, 0.80, 1.12};
+    static const double fixed[] = {1.7, 1.1, 3.2, 6.3, 10.7, 6.0, 1.6};
+    static const double cap[] = {1150, 1150, 876, 1100, 1227, 1070, 1150};
     const mlpc::LinearCfgInfo c = mlpc_linear_config(p.cfg);
     const uint32_t slabs = (uint32_t)(K / mlpc::BK), tiles = p.Mt * p.Nt;
     const double bytes = 128.0 * ((double)c.BN / p.Mt + (double)c.BM / p.Nt);
@@ -181,13 +188,18 @@ double plan_cost(const Plan& p, int64_t M, int64_t N, int64_t K, int cus) {
     auto rounds = [&](double count, uint32_t n) {
         const double r = ceil(count / cus), active = count < cus ? count : cus;
         const double compute = slab[p.cfg] * (tiles * p.S <= (uint32_t)cus ? alone[p.cfg] : 1.0);
-        return r * (fixed[p.cfg] + n * fmax(compute, fmax(bytes * active / 7.0e6, bytes / 36.0e3)));
+        return r * (fixed[p.cfg] + n * fmax(compute, fmax(bytes * active / 6.8e6, bytes / 35.4e3)));
     };
-    if (p.S == 1) return fmax(rounds(tiles, slabs), 6.0);
+    const double power = (double)tiles * c.BM * c.BN * K * 2e-6 / cap[p.cfg];
+    if (p.S == 1) {
+        // (the host's floor, with the estimate itself to tell such plans apart)
+        const double cost = fmax(rounds(tiles, slabs), power);
+        return fmax(cost, 6.0) + 0.01 * cost;
+    }
     const double split = tiles - p.direct;
     const double values = split * c.BM * c.BN * fmin(1.0, (double)M / ((double)p.Mt * c.BM)) * fmin(1.0, (double)N / ((double)p.Nt * c.BN));
-    const double cost = rounds(p.direct, slabs) + rounds(split * p.S, p.ksp) + 2.3 + values * 4 * p.S * 2 / 3.9e6;
-    return fmax(cost, 9.0);
+    const double cost = fmax(rounds(p.direct, slabs) + rounds(split * p.S, p.ksp), power) + 3.2 + values * 4 * p.S * 2 / 4.2e6;
+    return fmax(cost, 9.0) + 0.01 * cost;
 }
 
 Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {
@@ -196,12 +208,14 @@ Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {
     bool found = false;
     for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
         if (!mlpc_linear_has(cfg, pass)) continue;
+        // (x^T dz has no short tiles)
+        if (pass != mlpc::PASS_DW && !config_fits(mlpc_linear_config(cfg), M)) continue;
         uint32_t last = 0;
         for (uint32_t split = 1; split <= MAX_SPLIT; ++split) {
             const Plan p = make_plan(cfg, M, N, K, split, cus);
             if (p.S == last) continue;
             last = p.S;
-            if (!plan_fits(p)) break;
+            if (!split_fits(p, cus)) break;
             const double c = plan_cost(p, M, N, K, cus);
             if (!found || c < cost) {
                 best = p;
@@ -221,19 +235,22 @@ void pass_sizes(int pass, int64_t rows, int64_t K, int64_t gN, int64_t* m, int64
 }
 
 // Largest split workspace of any plan for up to max_rows rows.
-size_t max_part_bytes(int64_t max_rows, int64_t K, int64_t gN) {
+size_t max_part_bytes(int64_t max_rows, int64_t K, int64_t gN, bool grad, int cus) {
     size_t most = 0;
-    for (int pass = 0; pass < 3; ++pass)
+    for (int pass = 0; pass < (grad ? 3 : 1); ++pass)
         for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
             int64_t m, n, k;
             pass_sizes(pass, max_rows, K, gN, &m, &n, &k);
             const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
-            const size_t tiles = (size_t)((m + c.BM - 1) / c.BM) * (size_t)((n + c.BN - 1) / c.BN);
+            if (!mlpc_linear_has(cfg, pass) || (pass != mlpc::PASS_DW && !config_fits(c, m))) continue;
             const size_t slabs = (size_t)(k / mlpc::BK);
-            const size_t b = slabs > 1 ? tiles * (slabs < MAX_SPLIT ? slabs : MAX_SPLIT) * c.BM * c.BN * 4 : 0;
+            if (slabs < 2) continue;
+            size_t parts = (size_t)((m + c.BM - 1) / c.BM) * (size_t)((n + c.BN - 1) / c.BN) * (slabs < MAX_SPLIT ? slabs : MAX_SPLIT);
+            if (parts > (size_t)cus) parts = (size_t)cus;
+            const size_t b = parts * c.BM * c.BN * 4;
             if (b > most) most = b;
         }
-    return most < MAX_PART_BYTES ? most : MAX_PART_BYTES;
+    return most;
 }
 
 int run_product(mlp_linear* h, int pass, int64_t rows, mlpc::GemmArgs& a, hipStream_t s) {
@@ -276,7 +293,7 @@ int release(int device, hipStream_t last, void* ws) {
 
 extern "C" {
 
-mlp_norm_t mlp_norm_create(int64_t H, int dtype, float eps) {
+mlp_norm_t mlp_norm_create(int64_t H, int dtype, float eps, int grad) {
     if (H < 1 || H > MAX_WIDTH) {
         fail(MLP_EINVAL, "H must be in 1..%lld, got %lld", (long long)MAX_WIDTH, (long long)H);
         return nullptr;
@@ -303,8 +320,8 @@ mlp_norm_t mlp_norm_create(int64_t H, int dtype, float eps) {
         delete h;
         return nullptr;
     }
-    const size_t bytes = (size_t)mlpc_norm_max_parts(h->H, h->cus) * 2 * H * sizeof(float);
-    e = hipMalloc(reinterpret_cast<void**>(&h->part), bytes);
+    const size_t bytes = grad ? (size_t)mlpc_norm_max_parts(h->H, h->cus) * 2 * H * sizeof(float) : 0;
+    if (bytes) e = hipMalloc(reinterpret_cast<void**>(&h->part), bytes);
     if (e != hipSuccess) {
         fail(MLP_ENOMEM, "hipMalloc of %zu workspace bytes failed: %s", bytes, hipGetErrorString(e));
         delete h;
@@ -346,6 +363,7 @@ int mlp_norm_backward(mlp_norm_t h, int64_t rows, const void* dy, int64_t lddy, 
                       const void* weight, const float* mean, const float* rstd, const void* dres, int64_t lddres,
                       void* dx, int64_t lddx, void* dweight, void* dbias, void* hip_stream) {
     if (!h) return fail(MLP_EINVAL, "NULL handle");
+    if (!h->part) return fail(MLP_EINVAL, "the handle was created without its gradient");
     int rc = check_rows_count(rows, MAX_ROWS);
     const bool any = rc == MLP_OK && rows > 0;
     if (any) rc = check_rows("dy", dy, lddy, h->H);
@@ -391,7 +409,7 @@ int mlp_norm_destroy(mlp_norm_t h) {
     return rc;
 }
 
-mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, int dtype) {
+mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, int dtype, int grad) {
     if (check_linear(max_rows, K, N, act) != MLP_OK) return nullptr;
     if (check_dtype(dtype) != MLP_OK) return nullptr;
     int dev = 0;
@@ -420,9 +438,9 @@ mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, 
         return nullptr;
     }
     const size_t zero_b = 256;
-    const size_t dz_b = act == MLP_ACT_NONE ? 0 : align_up((size_t)max_rows * h->gN * 2, 256);
-    const size_t col_b = align_up((size_t)mlpc_dz_max_parts() * h->gN * sizeof(float), 256);
-    h->part_bytes = max_part_bytes(max_rows, K, h->gN);
+    const size_t dz_b = !grad || act == MLP_ACT_NONE ? 0 : align_up((size_t)max_rows * h->gN * 2, 256);
+    const size_t col_b = !grad ? 0 : align_up((size_t)mlpc_dz_max_parts() * h->gN * sizeof(float), 256);
+    h->part_bytes = max_part_bytes(max_rows, K, h->gN, grad != 0, h->cus);
     const size_t bytes = zero_b + dz_b + col_b + h->part_bytes;
     e = hipMalloc(&h->ws, bytes);
     if (e != hipSuccess) {
@@ -435,7 +453,7 @@ mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, 
     p += zero_b;
     h->dz = dz_b ? reinterpret_cast<uint16_t*>(p) : nullptr;
     p += dz_b;
-    h->colsum = reinterpret_cast<float*>(p);
+    h->colsum = col_b ? reinterpret_cast<float*>(p) : nullptr;
     p += col_b;
     h->part = h->part_bytes ? reinterpret_cast<float*>(p) : nullptr;
     e = hipMemset(h->ws, 0, zero_b);
@@ -491,6 +509,7 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
                         const void* w, int64_t ldw, const void* z, int64_t ldz, void* dx, int64_t lddx, void* dw,
                         int64_t lddw, void* db, void* hip_stream) {
     if (!h) return fail(MLP_EINVAL, "NULL handle");
+    if (!h->colsum) return fail(MLP_EINVAL, "the handle was created without its gradient");
     const bool act = h->act != MLP_ACT_NONE;
     int rc = check_rows_count(rows, h->max_rows);
     const bool any = rc == MLP_OK && rows > 0;

@@ -20,23 +20,23 @@ __device__ __forceinline__ float gelu_tanh_grad(float z) {
     return z != z ? z : d;
 }
 
-// A workgroup takes 256 columns (8 per thread) of one row group, ROWS rows at
-// a time, with the columns' sums in registers: 8 rows, or 32 (1024 threads)
-// where one row group is the whole batch.
-constexpr int DZ_COLS = 256;
+// A workgroup takes COLS columns (8 per thread) of one row group, ROWS rows at
+// a time, with the columns' sums in registers: 256 columns by 8 rows, or 64 by
+// 32 where one row group is the whole (short) batch.
+constexpr int DZ_NT = 256;
 constexpr int DZ_PARTS = 64;
 
-template <int DT, int ACT, int ROWS>
-__global__ __launch_bounds__(ROWS * 32) void dz_kernel(DzArgs a) {
+template <int DT, int ACT, int COLS>
+__global__ __launch_bounds__(DZ_NT) void dz_kernel(DzArgs a) {
+    constexpr int LANES = COLS / 8, ROWS = DZ_NT / LANES;
     constexpr int G = ACT == ACT_SWIGLU ? 2 : 1;
-    __shared__ float s[ROWS][DZ_COLS];
-    const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
-    const int c = blockIdx.x * DZ_COLS + lane * 8;
+    __shared__ float s[ROWS][COLS];
+    const int lane = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+    const int c = blockIdx.x * COLS + lane * 8;
     const bool in = c < a.N;
     const int64_t r0 = a.rows * blockIdx.y / a.parts, r1 = a.rows * (blockIdx.y + 1) / a.parts;
     float sum[G][8] = {};
     if (in) {
-#pragma unroll 2
         for (int64_t r = r0 + sub; r < r1; r += ROWS) {
             float d[G][8];
             widen8<DT>(ld16(a.dy + r * a.lddy + c), d[0]);
@@ -66,14 +66,14 @@ __global__ __launch_bounds__(ROWS * 32) void dz_kernel(DzArgs a) {
         }
     }
     if (!a.db) return;
-    const int j = threadIdx.x, col = blockIdx.x * DZ_COLS + j;
+    const int j = threadIdx.x, col = blockIdx.x * COLS + j;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < 8; ++k) s[sub][lane * 8 + k] = sum[g][k];
         __syncthreads();
-        if (j >= DZ_COLS || col >= a.N) continue;
+        if (j >= COLS || col >= a.N) continue;
         float t = s[0][j];
 #pragma unroll 8
         for (int k = 1; k < ROWS; ++k) t += s[k][j];
@@ -108,9 +108,10 @@ __global__ __launch_bounds__(256) void db_kernel(DzArgs a, int n) {
 
 template <int DT, int ACT>
 static void dz_launch(const DzArgs& a, hipStream_t s) {
-    const dim3 grid((a.N + DZ_COLS - 1) / DZ_COLS, a.parts);
-    if (a.parts == 1 && a.rows > 8) hipLaunchKernelGGL((dz_kernel<DT, ACT, 32>), grid, dim3(1024), 0, s, a);
-    else hipLaunchKernelGGL((dz_kernel<DT, ACT, 8>), grid, dim3(256), 0, s, a);
+    if (a.parts == 1)
+        hipLaunchKernelGGL((dz_kernel<DT, ACT, 64>), dim3((a.N + 63) / 64), dim3(DZ_NT), 0, s, a);
+    else
+        hipLaunchKernelGGL((dz_kernel<DT, ACT, 256>), dim3((a.N + 255) / 256, a.parts), dim3(DZ_NT), 0, s, a);
 }
 
 template <int DT>

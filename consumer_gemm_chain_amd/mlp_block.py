@@ -25,11 +25,11 @@ def _library():
     if _lib is None:
         lib = load_library()
         vp, i64, ci, f = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
-        lib.mlp_norm_create.argtypes = [i64, ci, f]
+        lib.mlp_norm_create.argtypes = [i64, ci, f, ci]
         lib.mlp_norm_create.restype = vp
         lib.mlp_norm_forward.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp]
         lib.mlp_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp]
-        lib.mlp_linear_create.argtypes = [i64, i64, i64, ci, ci]
+        lib.mlp_linear_create.argtypes = [i64, i64, i64, ci, ci, ci]
         lib.mlp_linear_create.restype = vp
         lib.mlp_linear_forward.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp]
         lib.mlp_linear_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp]
@@ -52,8 +52,8 @@ def _created(h):
     return h
 
 
-def mlp_norm_create(H: int, dtype: int, eps: float) -> int:
-    return _created(_library().mlp_norm_create(int(H), int(dtype), float(eps)))
+def mlp_norm_create(H: int, dtype: int, eps: float, grad: bool = True) -> int:
+    return _created(_library().mlp_norm_create(int(H), int(dtype), float(eps), int(bool(grad))))
 
 
 def mlp_norm_forward(h, rows, x, ldx, weight, bias, y, ldy, mean, rstd, hip_stream) -> int:
@@ -70,8 +70,8 @@ def mlp_norm_destroy(h: int | None) -> int:
     return _check(_library().mlp_norm_destroy(h))
 
 
-def mlp_linear_create(max_rows: int, K: int, N: int, act: int, dtype: int) -> int:
-    return _created(_library().mlp_linear_create(int(max_rows), int(K), int(N), int(act), int(dtype)))
+def mlp_linear_create(max_rows: int, K: int, N: int, act: int, dtype: int, grad: bool = True) -> int:
+    return _created(_library().mlp_linear_create(int(max_rows), int(K), int(N), int(act), int(dtype), int(bool(grad))))
 
 
 def mlp_linear_forward(h, rows, x, ldx, w, ldw, bias, residual, ldres, y, ldy, z, ldz, hip_stream) -> int:
@@ -164,12 +164,13 @@ class _Layer:
 
 class MlpNorm(_Layer):
     """Layer norm over rows of H elements.  Outputs are the caller's tensors;
-    work is enqueued on torch's current stream (or `stream`)."""
+    work is enqueued on the current stream of x's device (or `stream`).  With
+    grad=False the handle holds no workspace and only runs forward."""
 
-    def __init__(self, H: int, dtype: str = "f16", eps: float = 1e-5):
+    def __init__(self, H: int, dtype: str = "f16", eps: float = 1e-5, grad: bool = True):
         self.H, self.eps = int(H), float(eps)
         self._set_type(dtype)
-        self.h = mlp_norm_create(H, DTYPES[dtype], eps)
+        self.h = mlp_norm_create(H, DTYPES[dtype], eps, grad)
 
     _destroy = staticmethod(mlp_norm_destroy)
 
@@ -200,13 +201,15 @@ class MlpNorm(_Layer):
 
 class MlpLinear(_Layer):
     """Linear layer K -> N with bias, activation and residual for calls of up
-    to `rows` rows.  W is [K, gN] (g = 2 for swiglu: gate, then up)."""
+    to `rows` rows.  W is [K, gN] (g = 2 for swiglu: gate, then up) and given
+    with every call: one handle serves all layers of its sizes.  With
+    grad=False it only runs forward and holds less."""
 
-    def __init__(self, rows: int, K: int, N: int, act: str = "none", dtype: str = "f16"):
+    def __init__(self, rows: int, K: int, N: int, act: str = "none", dtype: str = "f16", grad: bool = True):
         self.rows, self.K, self.N, self.act = int(rows), int(K), int(N), act
         self.gN = self.N * (2 if act == "swiglu" else 1)
         self._set_type(dtype)
-        self.h = mlp_linear_create(rows, K, N, ACTS[act], DTYPES[dtype])
+        self.h = mlp_linear_create(rows, K, N, ACTS[act], DTYPES[dtype], grad)
 
     _destroy = staticmethod(mlp_linear_destroy)
 
@@ -241,13 +244,14 @@ class MlpBlock:
     """The pre-norm MLP block y = x + act(norm(x) W1 + b1) W2 + b2 for up to
     `rows` rows, H wide with I inner columns: one norm and two linear layers,
     and their gradients.  `params` maps names to tensors: weight, bias [H],
-    w1 [H, gI], b1 [gI], w2 [I, H], b2 [H]."""
+    w1 [H, gI], b1 [gI], w2 [I, H], b2 [H].  grad=False: forward only."""
 
-    def __init__(self, rows: int, H: int, I: int, act: str = "gelu_tanh", dtype: str = "f16", eps: float = 1e-5):
+    def __init__(self, rows: int, H: int, I: int, act: str = "gelu_tanh", dtype: str = "f16", eps: float = 1e-5,
+                 grad: bool = True):
         self.H, self.I, self.act, self.dtype = int(H), int(I), act, dtype
-        self.norm = MlpNorm(H, dtype, eps)
-        self.lin1 = MlpLinear(rows, H, I, act, dtype)
-        self.lin2 = MlpLinear(rows, I, H, "none", dtype)
+        self.norm = MlpNorm(H, dtype, eps, grad)
+        self.lin1 = MlpLinear(rows, H, I, act, dtype, grad)
+        self.lin2 = MlpLinear(rows, I, H, "none", dtype, grad)
 
     def close(self):
         for layer in (self.norm, self.lin1, self.lin2):

@@ -65,10 +65,10 @@ typedef struct mlp_norm* mlp_norm_t;
 typedef struct mlp_linear* mlp_linear_t;
 
 /* Create a layer norm over rows of H elements (1 <= H <= 2^22) with `eps`
- * (finite, >= 0) on the current HIP device, and allocate the workspace of
- * its weight gradients.  Returns NULL on error with mlp_chain_last_error()
- * set. */
-mlp_norm_t mlp_norm_create(int64_t H, int dtype, float eps);
+ * (finite, >= 0) on the current HIP device.  `grad` != 0 allocates the
+ * workspace of its gradient; a handle without it only runs forward.  Returns
+ * NULL on error with mlp_chain_last_error() set. */
+mlp_norm_t mlp_norm_create(int64_t H, int dtype, float eps, int grad);
 
 /* y = norm(x) of `rows` rows.  weight and bias have H elements of the
  * storage type; NULL leaves out the scale or the shift.  mean and rstd
@@ -91,10 +91,13 @@ int mlp_norm_destroy(mlp_norm_t h);
 
 /* Create a linear layer K -> N for calls of up to max_rows rows, on the
  * current HIP device.  max_rows >= 1, K and N positive multiples of 8, each
- * below 2^22; act and dtype from the enums of mlp_chain.h.  The workspace
- * (split-K partials, counters, dz) is allocated here.  Returns NULL on error
- * with mlp_chain_last_error() set. */
-mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, int dtype);
+ * below 2^22; act and dtype from the enums of mlp_chain.h.  The workspace is
+ * allocated here: the partials of split products (a few MB for single tokens,
+ * at most 64 MB on 256 CUs) and, if `grad` != 0, what the gradient needs (dz
+ * [max_rows, gN] with an activation); a handle without it only runs forward.
+ * No weights are kept: one handle serves every layer of its sizes.  Returns
+ * NULL on error with mlp_chain_last_error() set. */
+mlp_linear_t mlp_linear_create(int64_t max_rows, int64_t K, int64_t N, int act, int dtype, int grad);
 
 /* y = act(x W + bias) + residual for `rows` <= max_rows rows.  x [rows, K],
  * W [K, gN], bias [gN] or NULL, residual [rows, N] or NULL, y [rows, N];
