@@ -7,13 +7,15 @@
 
 namespace mlpc {
 
+constexpr int RNT = 64;
+
 // A workgroup takes 256 chunks of eight output columns of one split tile.  A
 // kernel of its own rather than the last part of each tile: it needs no
 // counters and no agent-scope fences, and the whole chip reads the partials.
 template <int DT>
-__global__ __launch_bounds__(256) void linear_reduce_kernel(GemmArgs p, int per_tile) {
+__global__ __launch_bounds__(RNT) void linear_reduce_kernel(GemmArgs p, int per_tile) {
     const uint32_t tile = blockIdx.x / per_tile;
-    const int chunk = (int)(blockIdx.x % per_tile) * 256 + threadIdx.x;
+    const int chunk = (int)(blockIdx.x % per_tile) * RNT + threadIdx.x;
     const int width = p.up ? p.BN / 2 : p.BN, row = chunk / (width / 8), oc = chunk % (width / 8) * 8;
     uint32_t mb, nb;
     tile_at(p, p.direct + tile, mb, nb);
@@ -65,9 +67,9 @@ using namespace mlpc;
 hipError_t mlpc_gemm_reduce(const GemmArgs& a, int dtype, hipStream_t s) {
     // (rows past M, as in the one tile row of a short product, are not launched)
     const int rows = a.M < a.BM ? a.M : a.BM, chunks = rows * ((a.up ? a.BN / 2 : a.BN) / 8);
-    const int per_tile = (chunks + 255) / 256;
+    const int per_tile = (chunks + RNT - 1) / RNT;
     const dim3 grid((a.Mt * a.Nt - a.direct) * per_tile);
-    if (dtype == DT_F16) hipLaunchKernelGGL(linear_reduce_kernel<DT_F16>, grid, dim3(256), 0, s, a, per_tile);
-    else hipLaunchKernelGGL(linear_reduce_kernel<DT_BF16>, grid, dim3(256), 0, s, a, per_tile);
+    if (dtype == DT_F16) hipLaunchKernelGGL(linear_reduce_kernel<DT_F16>, grid, dim3(RNT), 0, s, a, per_tile);
+    else hipLaunchKernelGGL(linear_reduce_kernel<DT_BF16>, grid, dim3(RNT), 0, s, a, per_tile);
     return hipGetLastError();
 }

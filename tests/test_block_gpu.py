@@ -20,6 +20,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
+from consumer_gemm_chain_amd import mlp_block as mb  # noqa: E402
 from consumer_gemm_chain_amd import MlpBlock, MlpChainError, MlpLinear, MlpNorm  # noqa: E402
 
 DT = {"f16": torch.float16, "bf16": torch.bfloat16}
@@ -448,6 +449,82 @@ def test_activation_gradient_at_extremes(act, dtype):
         z2[0, 3] = float("nan")
         layer.backward(dy, None, None, db=db, z=z2)
         assert db[3].isnan() and not db[4:N].isnan().any()
+
+
+CONFIGS = range(7)
+
+
+@pytest.mark.parametrize("dtype,rows,K,N", [("f16", 150, 328, 264), ("bf16", 300, 640, 136), ("f16", 9, 200, 72)])
+def test_every_tile_configuration_gives_the_same_bits(dtype, rows, K, N):
+    """Unsplit, every configuration adds the same products in the same order; split in equal parts likewise."""
+    c = linear_case(rows, K, N, "swiglu", dtype, 9)
+    x, w, b, dy, z = c["x"], c["w"], c["bias"], c["dy"], c["z"]
+    # (a handle of 150 rows at least: its workspace holds the forced plans' partials)
+    with MlpLinear(max(rows, 150), K, N, "swiglu", dtype) as layer:
+        for split in (1, 2, 4):
+            seen = [None] * 3
+            for cfg in CONFIGS:
+                y, zz, dx, dw = torch.empty_like(dy), torch.empty_like(z), torch.empty_like(x), torch.empty_like(w)
+                outs = []
+                for op in range(3):
+                    try:
+                        mb.mlp_linear_debug_set_plan(layer.h, op, cfg, split)
+                    except MlpChainError:
+                        assert op == 2 and cfg < 2       # x^T dz has no short tiles
+                        outs.append(None)
+                        continue
+                    if op == 0:
+                        layer.forward(x, w, y, bias=b, residual=dy, z=zz)
+                        outs.append((y, zz))
+                    elif op == 1:
+                        layer.backward(dy, None, w, dx=dx, z=z)
+                        outs.append((dx,))
+                    else:
+                        layer.backward(dy, x, None, dw=dw, z=z)
+                        outs.append((dw,))
+                for op, got in enumerate(outs):
+                    if got is None:
+                        continue
+                    seen[op] = seen[op] or got
+                    assert all(torch.equal(p, q) for p, q in zip(seen[op], got)), (split, cfg, op)
+        for op in range(3):
+            mb.mlp_linear_debug_set_plan(layer.h, op, -1, 0)
+
+
+@pytest.mark.parametrize("cfg,rows,K,N", [(0, 1100, 200, 600), (2, 2200, 328, 2200), (6, 2200, 200, 2200), (5, 2200, 200, 4200)])
+def test_whole_tiles_beside_split_ones(cfg, rows, K, N):
+    """More tiles than the chip has CUs: the first rounds are computed whole, the rest in parts."""
+    c = linear_case(rows, K, N, "none", "f16", 10)
+    y, y1 = torch.empty_like(c["dy"]), torch.empty_like(c["dy"])
+    with MlpLinear(rows, K, N, "none", "f16") as layer:
+        mb.mlp_linear_debug_set_plan(layer.h, 0, cfg, 1)
+        layer.forward(c["x"], c["w"], y1, bias=c["bias"], residual=c["res"])
+        mb.mlp_linear_debug_set_plan(layer.h, 0, cfg, 3)
+        layer.forward(c["x"], c["w"], y, bias=c["bias"], residual=c["res"])
+    x, w = c["x"].double(), c["w"].double()
+    ref = torch.mm(x, w) + c["bias"].double() + c["res"].double()
+    tol = (K / 32 + 64) * E32 * (torch.mm(x.abs(), w.abs()) + c["bias"].double().abs()) + 2.0 ** -20 * ref.abs()
+    close(y, ref, rounded(ref, "f16") + tol, "split")
+    close(y1, ref, rounded(ref, "f16") + tol, "whole")
+
+
+def test_forward_only_handles():
+    c = linear_case(20, 264, 136, "gelu_tanh", "f16", 12)
+    y, y2 = torch.empty_like(c["dy"]), torch.empty_like(c["dy"])
+    x, w, b, dy, _ = norm_case(8, 264, "f16", 13)
+    n, n2 = torch.empty_like(x), torch.empty_like(x)
+    s = torch.ones(8, device="cuda")
+    with MlpLinear(20, 264, 136, "gelu_tanh") as full, MlpLinear(20, 264, 136, "gelu_tanh", grad=False) as lin, \
+            MlpNorm(264) as nfull, MlpNorm(264, grad=False) as norm:
+        full.forward(c["x"], c["w"], y, bias=c["bias"])
+        lin.forward(c["x"], c["w"], y2, bias=c["bias"])
+        nfull.forward(x, w, b, n)
+        norm.forward(x, w, b, n2)
+        assert torch.equal(y, y2) and torch.equal(n, n2)
+        with pytest.raises(MlpChainError, match="without its gradient"):
+            lin.backward(c["dy"], c["x"], c["w"], dx=torch.empty_like(c["x"]), z=c["z"])
+        with pytest.raises(MlpChainError, match="without its gradient"):
+            norm.backward(dy, x, w, s, s, n)
 
 
 def test_linear_outputs_left_out():
