@@ -16,9 +16,8 @@
 //     register pair makes them eight: the epilogue adds the bias and the
 //     residual and stores 16 bytes per lane without going through LDS.
 //   * Rows and columns past the matrices are clamped to the last row or
-//     8-column chunk (their results are not stored).  Reduction elements past
-//     K (K % 64 != 0) are multiplied in one last step whose out-of-range
-//     chunks come from a zero page.
+//     8-column chunk (their results are not stored).  A slab that ends past K
+//     (K % 64 != 0) takes its out-of-range chunks from a zero page.
 #pragma once
 
 #include "block_launch.h"
@@ -215,17 +214,26 @@ struct LinTile {
         if constexpr (DMA && DONE < C::LPS) static_for<DONE, C::LPS>([&](auto q) { issue<decltype(q)::value>(h, stage); });
     }
 
-    // Reduction stages h0 .. h1-1 (a whole number of slabs, at least one).
-    // Stage h lives in ring stage (h - h0) % NS.  Before the last half of a
+    // Reduction stages h0 .. h1-1 (a whole number of slabs, at least one),
+    // after the stages of slab `tail` (>= 0) that ends past K: taken first, it
+    // arrives with the ring's first fill and costs no wait of its own.  Stage
+    // i of the sequence lives in ring stage i % NS.  Before the last half of a
     // stage's MFMAs every wave has read all of it and the next stage has
-    // landed (barrier); the freed ring stage then takes stage h + NS.  Past
+    // landed (barrier); the freed ring stage then takes stage i + NS.  Past
     // the end the last stage is requested again, into ring stages that are
     // not read, so the number of requests in flight at a barrier is fixed.
     template <int DT>
-    __device__ __forceinline__ void kloop(f32x4 (&acc)[C::FM][C::FN], int h0, int h1) const {
+    __device__ __forceinline__ void kloop(f32x4 (&acc)[C::FM][C::FN], int h0, int h1, int tail, const GemmArgs& p) const {
+        static_assert(C::NS > C::SPS, "the tail's stages are requested by the first fill");
 #pragma unroll
-        for (int i = 0; i < C::NS; ++i)
-            static_for<0, C::LPS>([&](auto q) { issue<decltype(q)::value>(min(h0 + i, h1 - 1), i); });
+        for (int i = 0; i < C::NS; ++i) {
+            if (i < C::SPS && tail >= 0) issue_tail(tail * C::SPS + i, i, p);
+            else {
+                const int h = min(h0 + i - (tail >= 0 ? C::SPS : 0), h1 - 1);
+                static_for<0, C::LPS>([&](auto q) { issue<decltype(q)::value>(h, i); });
+            }
+        }
+        if (tail >= 0) h0 -= C::SPS;
         LinFrags<C> f, g;
         ring_barrier<C::LPS * (C::NS - 1)>();
         read_all<0>(0, f);
@@ -255,17 +263,19 @@ struct LinTile {
         f.ready();       // the last reads land before their registers are reused
     }
 
-    // The slab that ends past K: its stages requested together, then multiplied.
+    // A stage of the slab that ends past K.
+    __device__ __forceinline__ void issue_tail(int h, int stage, const GemmArgs& p) const {
+#pragma unroll
+        for (int q = 0; q < C::B_PER_WAVE; ++q) b.issue_tail(h, stage, q, p.ldb, p.K, p.zero);
+#pragma unroll
+        for (int q = 0; q < C::A_PER_WAVE; ++q) a.issue_tail(h, stage, q, p.lda, p.K, p.zero);
+    }
+
+    // The slab that ends past K alone (a reduction of fewer than 64).
     template <int DT>
-    __device__ __forceinline__ void tail(f32x4 (&acc)[C::FM][C::FN], int slab, const GemmArgs& p) const {
-        ring_barrier<0>();
+    __device__ __forceinline__ void only_tail(f32x4 (&acc)[C::FM][C::FN], int slab, const GemmArgs& p) const {
 #pragma unroll
-        for (int i = 0; i < C::SPS; ++i) {
-#pragma unroll
-            for (int q = 0; q < C::B_PER_WAVE; ++q) b.issue_tail(slab * C::SPS + i, i, q, p.ldb, p.K, p.zero);
-#pragma unroll
-            for (int q = 0; q < C::A_PER_WAVE; ++q) a.issue_tail(slab * C::SPS + i, i, q, p.lda, p.K, p.zero);
-        }
+        for (int i = 0; i < C::SPS; ++i) issue_tail(slab * C::SPS + i, i, p);
         ring_barrier<0>();
         static_for<0, 2>([&](auto s) {
             constexpr int S = decltype(s)::value;
@@ -479,8 +489,9 @@ __global__ __launch_bounds__(C::NT, C::OCC) void linear_kernel(GemmArgs p) {
         t.b.init(p.b, p.ldb, n0, p.N, p.up);
         const int slabs = p.K / BK;
         const int k0 = whole ? 0 : min((int)(s * p.ksp), slabs), k1 = whole ? slabs : min(k0 + (int)p.ksp, slabs);
-        if (k1 > k0) t.template kloop<DT>(acc, k0 * C::SPS, k1 * C::SPS);
-        if ((whole || s + 1 == p.S) && p.K % BK) t.template tail<DT>(acc, slabs, p);
+        const bool tail = (whole || s + 1 == p.S) && p.K % BK;
+        if (k1 > k0) t.template kloop<DT>(acc, k0 * C::SPS, k1 * C::SPS, tail ? slabs : -1, p);
+        else if (tail) t.template only_tail<DT>(acc, slabs, p);
         ring_barrier<0>();      // no DMA in flight when the workgroup ends
     }
     if (whole) linear_epilogue<C, DT, PASS>(acc, p, m0, n0);
