@@ -177,10 +177,10 @@ bool split_fits(const Plan& p, int cus) { return p.S == 1 || (p.Mt * p.Nt - p.di
 // partials' way out and back.  Small products take no less than the host's
 // time for their launches.
 double plan_cost(const Plan& p, int64_t M, int64_t N, int64_t K, int cus) {
-    static const double slab[] = {0.36, 0.38, 0.54, 0.84, 1.42, 0.98, 0.61};
-    static const double alone[] = {1.07, 1.31, 0.96, 0.92, 0.91, 0.80, 1.12};
-    static const double fixed[] = {1.7, 1.1, 3.2, 6.3, 10.7, 6.0, 1.6};
-    static const double cap[] = {1150, 1150, 876, 1100, 1227, 1070, 1150};
+    static const double slab[] = {0.36, 0.38, 0.54, 0.84, 1.42, 0.98, 0.61, 0.86};
+    static const double alone[] = {1.07, 1.31, 0.96, 0.92, 0.91, 0.80, 1.12, 1.0};
+    static const double fixed[] = {1.7, 1.1, 3.2, 6.3, 10.7, 6.0, 1.6, 2.8};
+    static const double cap[] = {1150, 1150, 876, 1100, 1227, 1070, 1150, 1150};
     const mlpc::LinearCfgInfo c = mlpc_linear_config(p.cfg);
     const uint32_t slabs = (uint32_t)(K / mlpc::BK), tiles = p.Mt * p.Nt;
     const double bytes = 128.0 * ((double)c.BN / p.Mt + (double)c.BM / p.Nt);

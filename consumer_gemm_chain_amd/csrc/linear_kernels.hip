@@ -13,20 +13,23 @@ static constexpr auto this_cfg() { MLPC_LINEAR_CONFIGS(MLPC_PICK) }
 #undef MLPC_PICK
 using Cfg = decltype(this_cfg());
 
-// x^T dz has K rows of output, never few: it goes without the short tiles.
-static constexpr bool has(int pass) { return pass != PASS_DW || Cfg::BM >= 128; }
+// x^T dz has K rows of output, never few: it goes without the short tiles.  It
+// writes as much as it reads, so it alone has the two-per-CU 256 x 128 tiles
+// (8192 x 7168 over 1000 rows: 115 us against 127 with 256 x 256; x W and
+// dz W^T run 2-15% slower on them than on configurations 3 to 5).
+static constexpr bool has(int pass) { return pass == PASS_DW ? Cfg::BM >= 128 : MLPC_LIN != 7; }
 
 template <int DT>
 static hipError_t launch(const GemmArgs& a, int pass, hipStream_t s) {
     const dim3 grid(a.direct + (a.Mt * a.Nt - a.direct) * a.S);
-    switch (pass) {
-    case PASS_FWD: hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_FWD>), grid, dim3(Cfg::NT), 0, s, a); break;
-    case PASS_DX: hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_DX>), grid, dim3(Cfg::NT), 0, s, a); break;
-    default:
-        if constexpr (has(PASS_DW)) hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_DW>), grid, dim3(Cfg::NT), 0, s, a);
-        else return hipErrorInvalidValue;
+    if constexpr (has(PASS_FWD)) {
+        if (pass == PASS_FWD) hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_FWD>), grid, dim3(Cfg::NT), 0, s, a);
+        if (pass == PASS_DX) hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_DX>), grid, dim3(Cfg::NT), 0, s, a);
     }
-    return hipGetLastError();
+    if constexpr (has(PASS_DW)) {
+        if (pass == PASS_DW) hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_DW>), grid, dim3(Cfg::NT), 0, s, a);
+    }
+    return has(pass) ? hipGetLastError() : hipErrorInvalidValue;
 }
 
 }  // namespace mlpc

@@ -25,7 +25,7 @@ LinearCfgInfo mlpc_linear_config(int cfg) {
     MLPC_LINEAR_CONFIGS(ROW)
     return LinearCfgInfo{};
 }
-bool mlpc_linear_has(int cfg, int pass) { return pass != PASS_DW || mlpc_linear_config(cfg).BM >= 128; }
+bool mlpc_linear_has(int cfg, int pass) { return pass == PASS_DW ? mlpc_linear_config(cfg).BM >= 128 : cfg != 7; }
 static hipError_t unreached() { ++failures; return hipErrorUnknown; }
 hipError_t mlpc_gemm(const GemmArgs&, int, int, int, hipStream_t) { return unreached(); }
 hipError_t mlpc_gemm_reduce(const GemmArgs&, int, hipStream_t) { return unreached(); }

@@ -60,7 +60,7 @@ def test_linear_kernels_stream_in_the_scalar_base_form(asm):
         if not name.startswith("linear") or name.endswith(".hip"):
             continue
         bodies = re.findall(r"^(_ZN4mlpc13linear_kernel\w*):(.*?)\.Lfunc_end", text, flags=re.M | re.S)
-        assert len(bodies) >= 4, name
+        assert len(bodies) >= 2, name
         for kernel, body in bodies:
             assert re.search(r"global_load_lds_dwordx4 v\d+, s\[\d+:\d+\]", body), kernel
             assert "scratch_" not in body, kernel
