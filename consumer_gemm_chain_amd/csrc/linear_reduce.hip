@@ -7,11 +7,14 @@
 
 namespace mlpc {
 
-constexpr int RNT = 64;
+constexpr int RNT = 64;     // small workgroups spread evenly over the CUs
 
-// A workgroup takes 256 chunks of eight output columns of one split tile.  A
+// A workgroup takes 64 chunks of eight output columns of one split tile.  A
 // kernel of its own rather than the last part of each tile: it needs no
-// counters and no agent-scope fences, and the whole chip reads the partials.
+// counters and no agent-scope fences, and the whole chip reads the partials
+// (x W, both kernels: 128 rows 12288 x 6144 54 -> 46 us, 300 rows 98 -> 78, one
+// row 37.7 -> 32.4 against the last part of each tile adding the others').
+// Bound by latency: 4.6 us for one row, 6.5 us for 20 MB of partials.
 template <int DT>
 __global__ __launch_bounds__(RNT) void linear_reduce_kernel(GemmArgs p, int per_tile) {
     const uint32_t tile = blockIdx.x / per_tile;
