@@ -188,8 +188,8 @@ constexpr int MAX_PARTS = 256;      // workgroups that keep column sums: one per
 // partials (8 H bytes each) small against the rows.  With d = x - mean the
 // row needs the sums of g and g d; dx = rstd g - rstd mean_c(g) -
 // d rstd^3 mean_c(g d) + dres.  Bound by memory, the partials included: with
-// dres, 8192 x 8192 bf16 106 us, 5.05 TB/s of the operands; 2048 x 12288 f16
-// 47 us for 201 MB of operands and 25 MB of partials, 4.8 TB/s; 1000 x 8192
+// dres, 8192 x 8192 bf16 102 us, 5.3 TB/s of the operands; 2048 x 12288 f16
+// 44 us for 201 MB of operands and 25 MB of partials, 5.1 TB/s; 1000 x 8192
 // 17 us (four rows per workgroup, whose loads are a chain).
 template <int DT, int NT, int V, bool RAGGED>
 __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
@@ -207,7 +207,10 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
         const int c = (i * TR + (int)fresh(t)) * 8;
         w[i] = a.weight && c < a.H ? load8(a.weight, place<RAGGED>(c, a.H)) : u32x4{one, one, one, one};
     }
-    u32x4 x[V], dy[V];
+    // the next row's dres too, requested with x and dy: 2048 x 12288 47 -> 44
+    // us; 16 waves' registers hold it only beside one chunk (with two they spill)
+    constexpr bool EARLY = V == 1 || NT <= 768;
+    u32x4 x[V], dy[V], dn[V];
     float mean = 0.f, rstd = 0.f;
     // row r's x, dy and statistics; a group past the last row takes that row's
     // x with dy = 0, which adds nothing to any sum
@@ -223,6 +226,7 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
             if (c < a.H) {
                 x[i] = load8(a.x + r * a.ldx, place<RAGGED>(c, a.H));
                 if (live) dy[i] = load8(a.dy + r * a.lddy, place<RAGGED>(c, a.H));
+                if (EARLY && a.dres && live) dn[i] = load8(a.dres + r * a.lddres, place<RAGGED>(c, a.H));
             }
         }
     };
@@ -238,9 +242,12 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
         for (int i = 0; i < V; ++i) {
             cx[i] = x[i];
             cdy[i] = dy[i];
-            // (needed only after the row's sums: no earlier request)
-            const int c = (i * TR + (int)fresh(t)) * 8;
-            if (a.dres && live && c < a.H) dr[i] = load8(a.dres + r * a.lddres, place<RAGGED>(c, a.H));
+            if constexpr (EARLY) {
+                dr[i] = dn[i];
+            } else {
+                const int c = (i * TR + (int)fresh(t)) * 8;
+                if (a.dres && live && c < a.H) dr[i] = load8(a.dres + r * a.lddres, place<RAGGED>(c, a.H));
+            }
         }
         if (r0 + step < a.rows) fetch(r + step);
         // dy, g and d of chunk i (where dy = 0, past the row or shared with
