@@ -331,9 +331,11 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
     }
     if (!a.dweight && !a.dbias) return;
     // the row groups' sums, chunk by chunk through LDS, added in group order
-    // and written as the workgroup's row of partials
+    // and written as the workgroup's row of partials, or as the gradients
+    // themselves by a workgroup that has every row
     float* part = a.part + (size_t)blockIdx.x * 2 * a.H;
-    auto join = [&](float (&v)[8], int i, float* row) {
+    auto join = [&](float (&v)[8], int i, float* row, uint16_t* out) {
+        if (a.parts == 1 && !out) return;
         const int c = (i * TR + (int)t) * 8, at = c < a.H ? place<RAGGED>(c, a.H) : c;
         __syncthreads();
 #pragma unroll
@@ -345,13 +347,14 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
             float sum = cols[j];
 #pragma unroll 4
             for (int k = 1; k < rpw; ++k) sum += cols[k * TR * 8 + j];
-            row[i * TR * 8 + j] = sum;
+            if (a.parts == 1) out[i * TR * 8 + j] = to_storage<DT>(sum);
+            else row[i * TR * 8 + j] = sum;
         }
     };
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        join(sw[i], i, part);
-        join(sb[i], i, part + a.H);
+        join(sw[i], i, part, a.dweight);
+        join(sb[i], i, part + a.H, a.dbias);
     }
 }
 
@@ -538,7 +541,7 @@ static hipError_t backward_t(const NormArgs& a, hipStream_t s) {
             hipLaunchKernelGGL(norm_cols_sweep_kernel<DT>, dim3((a.H + SWEEP_NT - 1) / SWEEP_NT, a.parts), dim3(SWEEP_NT), 0, s, a);
         hipLaunchKernelGGL(norm_dx_sweep_kernel<DT>, dim3((unsigned)a.rows), dim3(SWEEP_NT), 0, s, a);
     }
-    if (sums) hipLaunchKernelGGL(norm_cols_sum_kernel<DT>, dim3((2 * a.H + 31) / 32), dim3(1024), 0, s, a);
+    if (sums && !(held(a.H) && a.parts == 1)) hipLaunchKernelGGL(norm_cols_sum_kernel<DT>, dim3((2 * a.H + 31) / 32), dim3(1024), 0, s, a);
     return hipGetLastError();
 }
 
@@ -547,10 +550,16 @@ static hipError_t backward_t(const NormArgs& a, hipStream_t s) {
 using namespace mlpc;
 
 // Partial rows of column sums: the workgroups of the register-held kernel, or
-// the row groups of the sweeping column kernel.
+// the row groups of the sweeping column kernel.  A single workgroup, which
+// needs no second kernel, takes up to three steps where a thread holds one
+// chunk (whole calls, 3 steps, then 5: 512 columns 8.1 and 10.1 us, 8192
+// columns 10.2 and 13.5; with a workgroup per step and the second kernel 10.7).
+constexpr int ALONE_STEPS = 3;
+
 int mlpc_norm_parts(int64_t rows, int H, int cus) {
     const int64_t per = held(H) ? backward_shape(H).nt / backward_shape(H).tr : 1;
     const int64_t groups = (rows + per - 1) / per;
+    if (held(H) && groups > 0 && groups <= (backward_shape(H).v == 1 ? ALONE_STEPS : 1)) return 1;
     const int64_t most = held(H) ? (cus < MAX_PARTS ? cus : MAX_PARTS) : 64;
     return (int)(groups < most ? groups : most);
 }

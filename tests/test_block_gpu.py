@@ -200,6 +200,23 @@ def test_norm_backward_variants(H):
     check_norm_backward(4, H, "f16", offset=100.0)
 
 
+@pytest.mark.parametrize("rows,H", [(48, 512), (49, 512), (2, 512), (12, 2041), (13, 2041), (3, 8192), (4, 8192)])
+def test_norm_backward_of_a_single_workgroup(rows, H):
+    """The row counts around the last one that a single workgroup takes; its outputs one at a time."""
+    check_norm_backward(rows, H, "bf16")
+    x, w, b, dy, _ = norm_case(rows, H, "f16", 4)
+    _, mean, rstd, _ = norm_ref(x, w, b)
+    out = [[torch.full((n, H) if n else (H,), 7.0, dtype=x.dtype, device="cuda") for n in (rows, 0, 0)] for _ in range(4)]
+    with MlpNorm(H, "f16", EPS) as layer:
+        for (dx, dw, db), keep in zip(out, ((1, 1), (1, 0), (0, 1), (0, 0))):
+            layer.backward(dy, x, w, mean.float(), rstd.float(), dx, dw if keep[0] else None, db if keep[1] else None)
+        torch.cuda.synchronize()
+    for (dx, dw, db), keep in zip(out, ((1, 1), (1, 0), (0, 1), (0, 0))):
+        assert torch.equal(dx, out[0][0])
+        assert torch.equal(dw, out[0][1]) if keep[0] else (dw == 7).all()
+        assert torch.equal(db, out[0][2]) if keep[1] else (db == 7).all()
+
+
 @pytest.mark.parametrize("H", [40, 333])
 @pytest.mark.parametrize("which", ["dx", "dweight", "dbias"])
 def test_norm_gradient_against_differences(H, which):
