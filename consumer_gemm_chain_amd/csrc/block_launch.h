@@ -31,7 +31,8 @@ struct NormArgs {
 // One product D[M, N] = sum_k A(m, k) B(k, n) of the linear layer.  PASS_FWD:
 // A = x [M, K], B = W [K, N]; PASS_DX: A = dz [M, K], B = W^T, stored as
 // W [N, K]; PASS_DW: A = x^T, stored as x [K, M], B = dz [K, N].
-enum { PASS_FWD = 0, PASS_DX = 1, PASS_DW = 2 };
+// PASS_BOTH_DX and PASS_BOTH_DW are the last two as parts of one launch.
+enum { PASS_FWD = 0, PASS_DX = 1, PASS_DW = 2, PASS_BOTH_DX = 3, PASS_BOTH_DW = 4, PASSES = 5 };
 
 struct GemmArgs {
     const uint16_t* a;
@@ -86,6 +87,8 @@ int mlpc_linear_num_configs();
 mlpc::LinearCfgInfo mlpc_linear_config(int cfg);
 bool mlpc_linear_has(int cfg, int pass);
 hipError_t mlpc_gemm(const mlpc::GemmArgs& a, int cfg, int pass, int dtype, hipStream_t s);
+// Both products of the gradient in one launch.
+hipError_t mlpc_gemm_both(const mlpc::GemmArgs& dx, const mlpc::GemmArgs& dw, int cfg, int dtype, hipStream_t s);
 // Sum the parts of a split product and finish its outputs (linear_reduce.hip).
 hipError_t mlpc_gemm_reduce(const mlpc::GemmArgs& a, int dtype, hipStream_t s);
 hipError_t mlpc_dz(const mlpc::DzArgs& a, int dtype, hipStream_t s);

@@ -17,11 +17,30 @@ using Cfg = decltype(this_cfg());
 // writes as much as it reads, so it alone has the two-per-CU 256 x 128 tiles
 // (8192 x 7168 over 1000 rows: 115 us against 127 with 256 x 256; x W and
 // dz W^T run 2-15% slower on them than on configurations 3 to 5).
-static constexpr bool has(int pass) { return pass == PASS_DW ? Cfg::BM >= 128 : MLPC_LIN != 7; }
+// Both products in one launch go without the 16-row tiles and configuration 7.
+static constexpr bool HAS_BOTH = MLPC_LIN != 0 && MLPC_LIN != 7;
+
+static constexpr bool has(int pass) {
+    if (pass == PASS_BOTH_DX || pass == PASS_BOTH_DW) return HAS_BOTH;
+    return pass == PASS_DW ? Cfg::BM >= 128 : MLPC_LIN != 7;
+}
+
+// Workgroups of a product.
+static uint32_t blocks(const GemmArgs& a) { return a.direct + (a.Mt * a.Nt - a.direct) * a.S; }
+
+template <int DT>
+static hipError_t both(const GemmArgs& dx, const GemmArgs& dw, hipStream_t s) {
+    if constexpr (HAS_BOTH) {
+        const uint32_t n = blocks(dx);
+        hipLaunchKernelGGL((linear_both_kernel<Cfg, DT>), dim3(n + blocks(dw)), dim3(Cfg::NT), 0, s, dx, dw, n);
+        return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
+}
 
 template <int DT>
 static hipError_t launch(const GemmArgs& a, int pass, hipStream_t s) {
-    const dim3 grid(a.direct + (a.Mt * a.Nt - a.direct) * a.S);
+    const dim3 grid(blocks(a));
     if constexpr (has(PASS_FWD)) {
         if (pass == PASS_FWD) hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_FWD>), grid, dim3(Cfg::NT), 0, s, a);
         if (pass == PASS_DX) hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_DX>), grid, dim3(Cfg::NT), 0, s, a);
@@ -41,6 +60,10 @@ using namespace mlpc;
 
 hipError_t MLPC_CAT(mlpc_linear_launch, MLPC_LIN)(const GemmArgs& a, int pass, int dtype, hipStream_t s) {
     return dtype == DT_F16 ? launch<DT_F16>(a, pass, s) : launch<DT_BF16>(a, pass, s);
+}
+
+hipError_t MLPC_CAT(mlpc_linear_both, MLPC_LIN)(const GemmArgs& dx, const GemmArgs& dw, int dtype, hipStream_t s) {
+    return dtype == DT_F16 ? both<DT_F16>(dx, dw, s) : both<DT_BF16>(dx, dw, s);
 }
 
 LinearCfgInfo MLPC_CAT(mlpc_linear_info, MLPC_LIN)() { return LinearCfgInfo{Cfg::BM, Cfg::BN, Cfg::NT, Cfg::RING}; }

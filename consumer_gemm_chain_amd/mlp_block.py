@@ -89,7 +89,8 @@ def mlp_linear_destroy(h: int | None) -> int:
 
 
 def mlp_linear_plan(rows: int, K: int, N: int, act: int, op: int, cus: int) -> dict:
-    """The plan of pass `op` (0: x W, 1: dz W^T, 2: x^T dz) on a GPU with `cus` CUs (host only)."""
+    """The plan of pass `op` (0: x W, 1: dz W^T alone, 2: x^T dz alone, 3 and 4: dz W^T and x^T dz in one
+    launch) on a GPU with `cus` CUs (host only)."""
     arr = (ctypes.c_int64 * len(PLAN_FIELDS))()
     _check(_library().mlp_linear_plan(int(rows), int(K), int(N), int(act), int(op), int(cus), arr, len(PLAN_FIELDS)))
     return dict(zip(PLAN_FIELDS, (int(v) for v in arr)))

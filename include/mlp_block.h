@@ -121,8 +121,9 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
 int mlp_linear_destroy(mlp_linear_t h);
 
 /* The plan a call of `rows` rows makes on a GPU with `cus` compute units for
- * pass 0 (x W), 1 (dz W^T) or 2 (x^T dz), computed on the host alone: fills
- * the first min(n, 9) of
+ * pass 0 (x W), 1 (dz W^T alone), 2 (x^T dz alone), 3 or 4 (dz W^T and x^T dz
+ * of a gradient that has both, which run in one launch), computed on the host
+ * alone: fills the first min(n, 9) of
  *   { config id, parts of a split tile's reduction, BM, BN, tile rows, tile
  *     columns, 64-deep slabs per part, workspace bytes of the partials, tiles
  *     computed whole although the others are split }.
@@ -132,8 +133,10 @@ int mlp_linear_plan(int64_t rows, int64_t K, int64_t N, int act, int pass, int c
 
 /* Test and measurement hook: run `pass` of the handle's later calls with tile
  * configuration `config_id` and the reduction of the tiles of the last, partial
- * round in at most `split` parts (0 or 1: one); config_id -1 and split 0 restore the planner's choice.  A call
- * whose partials exceed the handle's workspace is then refused.  Returns
+ * round in at most `split` parts (0 or 1: one); config_id -1 and split 0 restore
+ * the planner's choice.  Passes 3 and 4 share the configuration set last; a
+ * forced pass 1 or 2 gives both products launches of their own.  A call whose
+ * partials exceed the handle's workspace is then refused.  Returns
  * MLP_EINVAL for a NULL handle, a configuration the pass does not have or a
  * split outside 0..32. */
 int mlp_linear_debug_set_plan(mlp_linear_t h, int pass, int config_id, int split);

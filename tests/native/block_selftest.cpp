@@ -25,9 +25,10 @@ LinearCfgInfo mlpc_linear_config(int cfg) {
     MLPC_LINEAR_CONFIGS(ROW)
     return LinearCfgInfo{};
 }
-bool mlpc_linear_has(int cfg, int pass) { return pass == PASS_DW ? mlpc_linear_config(cfg).BM >= 128 : cfg != 7; }
+bool mlpc_linear_has(int cfg, int pass) { return pass > PASS_DW ? cfg != 0 && cfg != 7 : pass == PASS_DW ? mlpc_linear_config(cfg).BM >= 128 : cfg != 7; }
 static hipError_t unreached() { ++failures; return hipErrorUnknown; }
 hipError_t mlpc_gemm(const GemmArgs&, int, int, int, hipStream_t) { return unreached(); }
+hipError_t mlpc_gemm_both(const GemmArgs&, const GemmArgs&, int, int, hipStream_t) { return unreached(); }
 hipError_t mlpc_gemm_reduce(const GemmArgs&, int, hipStream_t) { return unreached(); }
 hipError_t mlpc_dz(const DzArgs&, int, hipStream_t) { return unreached(); }
 int mlpc_dz_parts(int64_t) { return 1; }
@@ -45,7 +46,7 @@ int main() {
         for (int64_t k : widths)
             for (int64_t n : widths)
                 for (int act = 0; act < 3; ++act)
-                    for (int pass = 0; pass < 3; ++pass) {
+                    for (int pass = 0; pass < PASSES; ++pass) {
                         memset(plan, 0xff, sizeof plan);
                         CHECK(mlp_linear_plan(r, k, n, act, pass, 256, plan, 9) == MLP_OK);
                         CHECK(plan[0] >= 0 && plan[0] < MLPC_NUM_LINEAR_CONFIGS && plan[1] >= 1 && plan[1] <= 32);

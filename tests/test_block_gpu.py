@@ -478,8 +478,9 @@ def test_every_tile_configuration_gives_the_same_bits(dtype, rows, K, N):
     x, w, b, dy, z = c["x"], c["w"], c["bias"], c["dy"], c["z"]
     # (a handle of 150 rows at least: its workspace holds the forced plans' partials)
     with MlpLinear(max(rows, 150), K, N, "swiglu", dtype) as layer:
+        results = {}
         for split in (1, 2, 4):
-            seen = [None] * 3
+            seen = results[split] = [None] * 3
             for cfg in CONFIGS:
                 y, zz, dx, dw = torch.empty_like(dy), torch.empty_like(z), torch.empty_like(x), torch.empty_like(w)
                 outs = []
@@ -507,6 +508,20 @@ def test_every_tile_configuration_gives_the_same_bits(dtype, rows, K, N):
                     assert all(torch.equal(p, q) for p, q in zip(seen[op], got)), (split, cfg, op)
         for op in range(3):
             mb.mlp_linear_debug_set_plan(layer.h, op, -1, 0)
+        # the gradient's two products in one launch
+        for cfg in CONFIGS:
+            if cfg in (0, 7):
+                with pytest.raises(MlpChainError, match="no tile configuration"):
+                    mb.mlp_linear_debug_set_plan(layer.h, 3, cfg, 1)
+                continue
+            for sx, sw in ((1, 1), (2, 1), (1, 2), (4, 1), (1, 4)):
+                mb.mlp_linear_debug_set_plan(layer.h, 3, cfg, sx)
+                mb.mlp_linear_debug_set_plan(layer.h, 4, cfg, sw)
+                dx, dw = torch.empty_like(x), torch.empty_like(w)
+                layer.backward(dy, x, w, dx=dx, dw=dw, z=z)
+                assert torch.equal(dx, results[sx][1][0]), (cfg, sx, sw)
+                assert torch.equal(dw, results[sw][2][0]), (cfg, sx, sw)
+        mb.mlp_linear_debug_set_plan(layer.h, 3, -1, 0)
 
 
 @pytest.mark.parametrize("cfg,rows,K,N", [(0, 1100, 200, 600), (2, 2200, 328, 2200), (6, 2200, 200, 2200), (5, 2200, 200, 4200)])
@@ -524,6 +539,22 @@ def test_whole_tiles_beside_split_ones(cfg, rows, K, N):
     tol = (K / 32 + 64) * E32 * (torch.mm(x.abs(), w.abs()) + c["bias"].double().abs()) + 2.0 ** -20 * ref.abs()
     close(y, ref, rounded(ref, "f16") + tol, "split")
     close(y1, ref, rounded(ref, "f16") + tol, "whole")
+
+
+@pytest.mark.parametrize("cfg,rows,K,N,sx,sw", [(1, 2200, 1104, 600, 3, 1), (6, 2200, 2200, 2312, 1, 3), (2, 1000, 2600, 2200, 2, 2)])
+def test_both_products_of_more_tiles_than_cus(cfg, rows, K, N, sx, sw):
+    """Whole and split tiles of both products of the gradient in one launch."""
+    c = linear_case(rows, K, N, "none", "f16", 11)
+    x, w, dy = c["x"], c["w"], c["dy"]
+    dx, dw = torch.full_like(x, 7.0), torch.full_like(w, 7.0)
+    with MlpLinear(rows, K, N, "none", "f16") as layer:
+        mb.mlp_linear_debug_set_plan(layer.h, 3, cfg, sx)
+        mb.mlp_linear_debug_set_plan(layer.h, 4, cfg, sw)
+        layer.backward(dy, x, w, dx=dx, dw=dw)
+    for got, p, q in ((dx, dy.double(), w.double().t()), (dw, x.double().t(), dy.double())):
+        ref = torch.mm(p, q)
+        tol = (p.shape[1] / 32 + 64) * E32 * torch.mm(p.abs(), q.abs())
+        close(got, ref, rounded(ref, "f16") + tol, "both")
 
 
 def test_forward_only_handles():

@@ -59,7 +59,7 @@ def test_linear_kernels_stream_in_the_scalar_base_form(asm):
     for name, text in asm.items():
         if not name.startswith("linear") or name.endswith(".hip"):
             continue
-        bodies = re.findall(r"^(_ZN4mlpc13linear_kernel\w*):(.*?)\.Lfunc_end", text, flags=re.M | re.S)
+        bodies = re.findall(r"^(_ZN4mlpc\d+linear_(?:both_)?kernel\w*):(.*?)\.Lfunc_end", text, flags=re.M | re.S)
         assert len(bodies) >= 2, name
         for kernel, body in bodies:
             assert re.search(r"global_load_lds_dwordx4 v\d+, s\[\d+:\d+\]", body), kernel

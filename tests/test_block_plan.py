@@ -15,10 +15,10 @@ SIZES = ((8, 8), (64, 64), (72, 40), (512, 2048), (2048, 512), (3584, 8192), (61
 @pytest.mark.parametrize("K,N", SIZES)
 @pytest.mark.parametrize("cus", [8, 64, 256, 304])
 def test_plans_are_sound(K, N, cus):
-    for rows, act, op in itertools.product(ROWS, ("none", "swiglu"), range(3)):
+    for rows, act, op in itertools.product(ROWS, ("none", "swiglu"), range(5)):
         p = mb.mlp_linear_plan(rows, K, N, ACT[act], op, cus)
         gN = N * (2 if act == "swiglu" else 1)
-        m, n, k = ((rows, gN, K), (rows, K, gN), (K, gN, rows))[op]
+        m, n, k = ((rows, gN, K), (rows, K, gN), (K, gN, rows), (rows, K, gN), (K, gN, rows))[op]
         what = (rows, K, N, act, op, cus, p)
         assert p["Mt"] == -(-m // p["BM"]) and p["Nt"] == -(-n // p["BN"]), what
         tiles, slabs = p["Mt"] * p["Nt"], k // 64
@@ -32,7 +32,7 @@ def test_plans_are_sound(K, N, cus):
         assert p["direct"] == tiles - tiles % cus and p["direct"] < tiles, what
         assert (tiles - p["direct"]) * p["S"] <= cus, what
         assert p["part_bytes"] == (tiles - p["direct"]) * p["S"] * p["BM"] * p["BN"] * 4 <= cus * 256 * 1024, what
-        if op != 2:
+        if op not in (2, 4):
             assert p["BM"] <= max(64, 2 * rows), what
 
 
@@ -45,11 +45,19 @@ def test_plans_follow_the_rows():
     assert mb.mlp_linear_plan(8, 64, 64, 0, 0, 256)["S"] == 1
 
 
+@pytest.mark.parametrize("K,N", SIZES)
+def test_both_products_in_one_launch(K, N):
+    """One configuration for both, at most one of them split."""
+    for rows, act in itertools.product(ROWS, ("none", "swiglu")):
+        dx, dw = (mb.mlp_linear_plan(rows, K, N, ACT[act], op, 256) for op in (3, 4))
+        assert dx["config"] == dw["config"] and min(dx["S"], dw["S"]) == 1, (rows, act, dx, dw)
+
+
 @pytest.mark.parametrize("args,needle", [
     ((0, 64, 64, 0, 0, 256), "rows"),
     ((4, 60, 64, 0, 0, 256), "multiples of 8"),
     ((4, 64, 64, 5, 0, 256), "activation"),
-    ((4, 64, 64, 0, 3, 256), "pass"),
+    ((4, 64, 64, 0, 5, 256), "pass"),
     ((4, 64, 64, 0, -1, 256), "pass"),
     ((4, 64, 64, 0, 0, 4), "cus"),
 ])
