@@ -395,7 +395,7 @@ int run_product(mlp_linear* h, int pass, int64_t rows, mlpc::GemmArgs& a, hipStr
 }
 
 // Both products of the gradient.
-int run_both(mlp_linear* h, int64_t rows, mlpc::GemmArgs& dx, mlpc::GemmArgs& dw, hipStream_t s) {
+int run_both(mlp_linear* h, int64_t rows, mlpc::GemmArgs& dx, mlpc::GemmArgs& dw, const mlpc::DzArgs& dz, hipStream_t s) {
     Plan (&p)[2] = h->both;
     if (h->plan_rows[mlpc::PASS_BOTH_DX] != rows) {
         const int cfg = h->forced_cfg[mlpc::PASS_BOTH_DX];
@@ -411,7 +411,7 @@ int run_both(mlp_linear* h, int64_t rows, mlpc::GemmArgs& dx, mlpc::GemmArgs& dw
         return fail(MLP_EINVAL, "the splits need %zu workspace bytes of %zu", p[0].part_bytes + p[1].part_bytes, h->part_bytes);
     set_plan(h, p[0], 0, dx);
     set_plan(h, p[1], p[0].part_bytes, dw);
-    hipError_t e = mlpc_gemm_both(dx, dw, p[0].cfg, h->dtype, s);
+    hipError_t e = mlpc_gemm_both(dx, dw, dz, p[0].cfg, h->dtype, s);
     if (e == hipSuccess && p[0].S > 1) e = mlpc_gemm_reduce(dx, h->dtype, s);
     if (e == hipSuccess && p[1].S > 1) e = mlpc_gemm_reduce(dw, h->dtype, s);
     return launched(e);
@@ -665,8 +665,9 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
     h->last_stream = s;
     const uint16_t* dz = static_cast<const uint16_t*>(dy);
     int64_t lddz = lddy;
+    const bool both = dx && dw && rows > 0 && h->forced_cfg[mlpc::PASS_DX] < 0 && h->forced_cfg[mlpc::PASS_DW] < 0;
+    mlpc::DzArgs d{};
     if (db || (act && (dx || dw) && rows > 0)) {
-        mlpc::DzArgs d{};
         d.dy = dz;
         d.z = static_cast<const uint16_t*>(z);
         d.dz = h->dz;
@@ -679,8 +680,9 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
         d.N = h->N;
         d.act = h->act;
         d.parts = mlpc_dz_parts(rows);
-        rc = launched(mlpc_dz(d, h->dtype, s));
+        rc = launched(mlpc_dz(d, h->dtype, !both, s));
         if (rc != MLP_OK) return rc;
+        if (d.parts == 1) d.db = nullptr;
     }
     if (act) {
         dz = h->dz;
@@ -709,8 +711,8 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
         b.N = h->gN;
         b.K = (int)rows;
     }
-    if (dx && dw && rows > 0 && h->forced_cfg[mlpc::PASS_DX] < 0 && h->forced_cfg[mlpc::PASS_DW] < 0)
-        return run_both(h, rows, a, b, s);
+    if (both)
+        return run_both(h, rows, a, b, d, s);
     if (dx && rows > 0) rc = run_product(h, mlpc::PASS_DX, rows, a, s);
     if (rc == MLP_OK && dw) rc = run_product(h, mlpc::PASS_DW, rows, b, s);
     return rc;

@@ -87,10 +87,14 @@ int mlpc_linear_num_configs();
 mlpc::LinearCfgInfo mlpc_linear_config(int cfg);
 bool mlpc_linear_has(int cfg, int pass);
 hipError_t mlpc_gemm(const mlpc::GemmArgs& a, int cfg, int pass, int dtype, hipStream_t s);
-// Both products of the gradient in one launch.
-hipError_t mlpc_gemm_both(const mlpc::GemmArgs& dx, const mlpc::GemmArgs& dw, int cfg, int dtype, hipStream_t s);
+// Both products of the gradient in one launch, with the sums of dz's partial
+// column sums unless dz.db is nullptr.
+hipError_t mlpc_gemm_both(const mlpc::GemmArgs& dx, const mlpc::GemmArgs& dw, const mlpc::DzArgs& dz, int cfg, int dtype,
+                          hipStream_t s);
 // Sum the parts of a split product and finish its outputs (linear_reduce.hip).
 hipError_t mlpc_gemm_reduce(const mlpc::GemmArgs& a, int dtype, hipStream_t s);
-hipError_t mlpc_dz(const mlpc::DzArgs& a, int dtype, hipStream_t s);
+// dz and its column sums; with more than one row group `join` adds the groups'
+// in a second kernel, else they are left in a.part.
+hipError_t mlpc_dz(const mlpc::DzArgs& a, int dtype, bool join, hipStream_t s);
 int mlpc_dz_parts(int64_t rows);
 int mlpc_dz_max_parts();

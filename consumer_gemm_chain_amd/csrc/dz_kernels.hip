@@ -86,7 +86,8 @@ __global__ __launch_bounds__(DZ_NT) void dz_kernel(DzArgs a) {
 }
 
 // The row groups' column sums added in a fixed order: 32 columns by 8 groups
-// of row groups, joined through LDS.
+// of row groups, joined through LDS.  Where both products follow, their launch
+// adds them instead.
 template <int DT>
 __global__ __launch_bounds__(256) void db_kernel(DzArgs a, int n) {
     __shared__ float s[8][33];
@@ -118,13 +119,13 @@ static void dz_launch(const DzArgs& a, hipStream_t s) {
 }
 
 template <int DT>
-static hipError_t dz_t(const DzArgs& a, hipStream_t s) {
+static hipError_t dz_t(const DzArgs& a, bool join, hipStream_t s) {
     if (a.parts > 0) {
         if (a.act == ACT_NONE) dz_launch<DT, ACT_NONE>(a, s);
         else if (a.act == ACT_GELU_TANH) dz_launch<DT, ACT_GELU_TANH>(a, s);
         else dz_launch<DT, ACT_SWIGLU>(a, s);
     }
-    if (a.db && a.parts != 1) {
+    if (a.db && join && a.parts != 1) {
         const int n = a.act == ACT_SWIGLU ? 2 * a.N : a.N;
         hipLaunchKernelGGL(db_kernel<DT>, dim3((n + 31) / 32), dim3(256), 0, s, a, n);
     }
@@ -146,6 +147,6 @@ int mlpc_dz_parts(int64_t rows) {
     return (int)(p < DZ_PARTS ? p : DZ_PARTS);
 }
 
-hipError_t mlpc_dz(const DzArgs& a, int dtype, hipStream_t s) {
-    return dtype == DT_F16 ? dz_t<DT_F16>(a, s) : dz_t<DT_BF16>(a, s);
+hipError_t mlpc_dz(const DzArgs& a, int dtype, bool join, hipStream_t s) {
+    return dtype == DT_F16 ? dz_t<DT_F16>(a, join, s) : dz_t<DT_BF16>(a, join, s);
 }

@@ -7,7 +7,7 @@ using namespace mlpc;
 
 #define MLPC_DECL(id, ...)                                                            \
     hipError_t mlpc_linear_launch##id(const GemmArgs&, int, int, hipStream_t);        \
-    hipError_t mlpc_linear_both##id(const GemmArgs&, const GemmArgs&, int, hipStream_t); \
+    hipError_t mlpc_linear_both##id(const GemmArgs&, const GemmArgs&, const DzArgs&, int, hipStream_t); \
     LinearCfgInfo mlpc_linear_info##id();                                             \
     bool mlpc_linear_has##id(int);
 MLPC_LINEAR_CONFIGS(MLPC_DECL)
@@ -36,9 +36,9 @@ hipError_t mlpc_gemm(const GemmArgs& a, int cfg, int pass, int dtype, hipStream_
 #undef MLPC_CASE
 }
 
-hipError_t mlpc_gemm_both(const GemmArgs& dx, const GemmArgs& dw, int cfg, int dtype, hipStream_t s) {
+hipError_t mlpc_gemm_both(const GemmArgs& dx, const GemmArgs& dw, const DzArgs& dz, int cfg, int dtype, hipStream_t s) {
 #define MLPC_CASE(n, ...) \
-    case n: return mlpc_linear_both##n(dx, dw, dtype, s);
+    case n: return mlpc_linear_both##n(dx, dw, dz, dtype, s);
     switch (cfg) { MLPC_LINEAR_CONFIGS(MLPC_CASE) default: return hipErrorInvalidValue; }
 #undef MLPC_CASE
 }

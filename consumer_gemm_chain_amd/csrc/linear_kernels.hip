@@ -29,10 +29,10 @@ static constexpr bool has(int pass) {
 static uint32_t blocks(const GemmArgs& a) { return a.direct + (a.Mt * a.Nt - a.direct) * a.S; }
 
 template <int DT>
-static hipError_t both(const GemmArgs& dx, const GemmArgs& dw, hipStream_t s) {
+static hipError_t both(const GemmArgs& dx, const GemmArgs& dw, const DzArgs& dz, hipStream_t s) {
     if constexpr (HAS_BOTH) {
-        const uint32_t n = blocks(dx);
-        hipLaunchKernelGGL((linear_both_kernel<Cfg, DT>), dim3(n + blocks(dw)), dim3(Cfg::NT), 0, s, dx, dw, n);
+        const uint32_t n = blocks(dx), db = dz.db ? (dw.N + Cfg::NT - 1) / Cfg::NT : 0;
+        hipLaunchKernelGGL((linear_both_kernel<Cfg, DT>), dim3(db + n + blocks(dw)), dim3(Cfg::NT), 0, s, dx, dw, dz, db, n);
         return hipGetLastError();
     }
     return hipErrorInvalidValue;
@@ -62,8 +62,9 @@ hipError_t MLPC_CAT(mlpc_linear_launch, MLPC_LIN)(const GemmArgs& a, int pass, i
     return dtype == DT_F16 ? launch<DT_F16>(a, pass, s) : launch<DT_BF16>(a, pass, s);
 }
 
-hipError_t MLPC_CAT(mlpc_linear_both, MLPC_LIN)(const GemmArgs& dx, const GemmArgs& dw, int dtype, hipStream_t s) {
-    return dtype == DT_F16 ? both<DT_F16>(dx, dw, s) : both<DT_BF16>(dx, dw, s);
+hipError_t MLPC_CAT(mlpc_linear_both, MLPC_LIN)(const GemmArgs& dx, const GemmArgs& dw, const DzArgs& dz, int dtype,
+                                              hipStream_t s) {
+    return dtype == DT_F16 ? both<DT_F16>(dx, dw, dz, s) : both<DT_BF16>(dx, dw, dz, s);
 }
 
 LinearCfgInfo MLPC_CAT(mlpc_linear_info, MLPC_LIN)() { return LinearCfgInfo{Cfg::BM, Cfg::BN, Cfg::NT, Cfg::RING}; }

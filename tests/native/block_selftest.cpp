@@ -28,9 +28,9 @@ LinearCfgInfo mlpc_linear_config(int cfg) {
 bool mlpc_linear_has(int cfg, int pass) { return pass > PASS_DW ? cfg != 0 && cfg != 7 : pass == PASS_DW ? mlpc_linear_config(cfg).BM >= 128 : cfg != 7; }
 static hipError_t unreached() { ++failures; return hipErrorUnknown; }
 hipError_t mlpc_gemm(const GemmArgs&, int, int, int, hipStream_t) { return unreached(); }
-hipError_t mlpc_gemm_both(const GemmArgs&, const GemmArgs&, int, int, hipStream_t) { return unreached(); }
+hipError_t mlpc_gemm_both(const GemmArgs&, const GemmArgs&, const DzArgs&, int, int, hipStream_t) { return unreached(); }
 hipError_t mlpc_gemm_reduce(const GemmArgs&, int, hipStream_t) { return unreached(); }
-hipError_t mlpc_dz(const DzArgs&, int, hipStream_t) { return unreached(); }
+hipError_t mlpc_dz(const DzArgs&, int, bool, hipStream_t) { return unreached(); }
 int mlpc_dz_parts(int64_t) { return 1; }
 int mlpc_dz_max_parts() { return 64; }
 hipError_t mlpc_norm_forward(const NormArgs&, int, int, hipStream_t) { return unreached(); }

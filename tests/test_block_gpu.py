@@ -557,6 +557,19 @@ def test_both_products_of_more_tiles_than_cus(cfg, rows, K, N, sx, sw):
         close(got, ref, rounded(ref, "f16") + tol, "both")
 
 
+@pytest.mark.parametrize("rows,act", [(1, "none"), (128, "swiglu"), (129, "none"), (300, "gelu_tanh"), (2500, "swiglu")])
+def test_bias_gradient_does_not_depend_on_the_other_outputs(rows, act):
+    """The column sums alone and in the launch of both products: the same bits."""
+    c = linear_case(rows, 72, 1032, act, "bf16", 12)
+    x, w, dy, z = c["x"], c["w"], c["dy"], c["z"]
+    db = [torch.full_like(c["bias"], 7.0) for _ in range(3)]
+    with MlpLinear(rows, 72, 1032, act, "bf16") as layer:
+        layer.backward(dy, x, w, dx=torch.empty_like(x), dw=torch.empty_like(w), db=db[0], z=z)
+        layer.backward(dy, None, None, db=db[1], z=z)
+        layer.backward(dy, x, None, dw=torch.empty_like(w), db=db[2], z=z)
+    assert torch.equal(db[0], db[1]) and torch.equal(db[0], db[2])
+
+
 def test_forward_only_handles():
     c = linear_case(20, 264, 136, "gelu_tanh", "f16", 12)
     y, y2 = torch.empty_like(c["dy"]), torch.empty_like(c["dy"])
