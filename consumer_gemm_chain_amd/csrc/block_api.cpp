@@ -166,68 +166,6 @@ bool config_fits(const mlpc::LinearCfgInfo& c, int64_t M) { return c.BM <= 64 ||
 
 bool split_fits(const Plan& p, int cus) { return p.S == 1 || (p.Mt * p.Nt - p.direct) * p.S <= (uint32_t)cus; }
 
-// Estimated microseconds of a plan, fitted to sweeps of every configuration
-// and split over the package's sizes and rows from 1 to 8192 (the cheapest
-// plan by this estimate is within 6% of the fastest measured on all but one of
-// them).  A workgroup takes `slab` microseconds per 64-deep slab with several
-// rounds of workgroups, `alone` times that with a single one, and `fixed` for
-// its prologue and epilogue.  Operands that no other running workgroup reads
-// too arrive at 6.8 MB per microsecond in all and 35 KB per CU (caches
-// included).  The chip's power caps the multiplication rate whatever the
-// schedule: `cap` MFLOP per microsecond.  A split adds a launch and the
-// partials' way out and back.  Small products take no less than the host's
-// time for their launches.
-double plan_cost(const Plan& p, int64_t M, int64_t N, int64_t K, int cus) {
-    static const double slab[] = {0.36, 0.38, 0.54, 0.84, 1.42, 0.98, 0.61, 0.86};
-    static const double alone[] = {1.07, 1.31, 0.96, 0.92, 0.91, 0.80, 1.12, 1.0};
-    static const double fixed[] = {1.7, 1.1, 3.2, 6.3, 10.7, 6.0, 1.6, 2.8};
-    static const double cap[] = {1150, 1150, 876, 1100, 1227, 1070, 1150, 1150};
-    const mlpc::LinearCfgInfo c = mlpc_linear_config(p.cfg);
-    const uint32_t slabs = (uint32_t)(K / mlpc::BK), tiles = p.Mt * p.Nt;
-    const double bytes = 128.0 * ((double)c.BN / p.Mt + (double)c.BM / p.Nt);
-    // rounds of `count` workgroups of `n` slabs each
-    auto rounds = [&](double count, uint32_t n) {
-        const double r = ceil(count / cus), active = count < cus ? count : cus;
-        const double compute = slab[p.cfg] * (tiles * p.S <= (uint32_t)cus ? alone[p.cfg] : 1.0);
-        return r * (fixed[p.cfg] + n * fmax(compute, fmax(bytes * active / 6.8e6, bytes / 35.4e3)));
-    };
-    const double power = (double)tiles * c.BM * c.BN * K * 2e-6 / cap[p.cfg];
-    if (p.S == 1) {
-        // (the host's floor, with the estimate itself to tell such plans apart)
-        const double cost = fmax(rounds(tiles, slabs), power);
-        return fmax(cost, 6.0) + 0.01 * cost;
-    }
-    const double split = tiles - p.direct;
-    const double values = split * c.BM * c.BN * fmin(1.0, (double)M / ((double)p.Mt * c.BM)) * fmin(1.0, (double)N / ((double)p.Nt * c.BN));
-    const double cost = fmax(rounds(p.direct, slabs) + rounds(split * p.S, p.ksp), power) + 3.2 + values * 4 * p.S * 2 / 4.2e6;
-    return fmax(cost, 9.0) + 0.01 * cost;
-}
-
-Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {
-    Plan best{};
-    double cost = 0.0;
-    bool found = false;
-    for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
-        if (!mlpc_linear_has(cfg, pass)) continue;
-        // (x^T dz has no short tiles)
-        if (pass != mlpc::PASS_DW && !config_fits(mlpc_linear_config(cfg), M)) continue;
-        uint32_t last = 0;
-        for (uint32_t split = 1; split <= MAX_SPLIT; ++split) {
-            const Plan p = make_plan(cfg, M, N, K, split, cus);
-            if (p.S == last) continue;
-            last = p.S;
-            if (!split_fits(p, cus)) break;
-            const double c = plan_cost(p, M, N, K, cus);
-            if (!found || c < cost) {
-                best = p;
-                cost = c;
-                found = true;
-            }
-        }
-    }
-    return best;
-}
-
 // When the last of `slots` places for workgroups falls free, if groups of
 // equal workgroups (their number and duration) are dealt in turn to the place
 // that is free first.
@@ -267,51 +205,112 @@ double dealt(const double (*group)[2], int groups, double slots) {
     return at[levels - 1];
 }
 
-// Estimated microseconds of both products of the gradient in one launch, dz
-// W^T's workgroups first.  As plan_cost, with constants of its own fitted to
-// 190 sizes of 1 to 8192 rows (over 118 others the chosen plan is 1.4% slower
-// than the fastest on average, at worst 25%: small ones the launches bound); workgroups of different lengths share a CU, so the chip is `room`
-// places per CU on which each takes that much longer.
-double both_cost(const Plan (&p)[2], int64_t rows, int64_t K, int64_t N, int cus) {
-    static const double slab[] = {0, 0.42, 0.57, 0.81, 1.59, 0.95, 0.74, 0};
-    static const double alone[] = {0, 1.0, 0.79, 0.98, 0.98, 0.57, 1.92, 0};
-    static const double fixed[] = {0, 1.3, 3.0, 4.2, 7.8, 7.0, 1.2, 0};
-    static const double cap[] = {1, 1080, 770, 960, 1210, 1500, 1150, 1};
-    static const int per_cu[] = {0, 2, 1, 1, 1, 1, 3, 0};
-    const int cfg = p[0].cfg;
+// A plan with the sizes it is for.
+struct Work {
+    Plan p;
+    int64_t M, N, K;
+};
+
+// What a launch's time is estimated from, per tile configuration: a workgroup
+// takes `slab` microseconds per 64-deep slab among several rounds of workgroups,
+// `alone` times that with a single one, and `fixed` for its prologue and
+// epilogue; the chip's power caps the multiplication rate whatever the
+// schedule at `cap` MFLOP per microsecond.  Workgroups of a CU share it: beyond
+// the first, one adds `share` places and each takes that much longer.  Partials
+// travel at `join` MB per microsecond after a launch of `launch`; a ragged slab
+// costs `ragged` of a whole one.  Operands are read at `read` and outputs
+// written at `write` MB per microsecond at best; operands that no other running
+// workgroup reads too arrive at `all` MB per microsecond in all and `cu` KB per
+// CU (caches included).
+struct Rates {
+    double slab[8], alone[8], fixed[8], cap[8];
+    double share, launch, join, ragged, read, write, all, cu;
+};
+
+// One product: fitted to every configuration and split of 529 sizes of x W and
+// 244 of x^T dz drawn over 1 to 8192 rows.  On sizes drawn afterwards the chosen
+// plan took 0.8% and 1.7% longer than the fastest on average, at worst 28% (a
+// split where none was needed, 8.6 us).
+const Rates SINGLE = {{0.416, 0.618, 0.72, 0.884, 1.54, 0.892, 0.707, 0.718},
+                      {0.985, 0.816, 0.959, 1.17, 0.898, 0.977, 1.46, 1.33},
+                      {1.55, 2.42, 3.78, 7.78, 17.5, 8.67, 1.37, 5.78},
+                      {1150, 1150, 900, 1120, 1230, 1080, 1150, 1150},
+                      0.328, 5.48, 4.52, 1, 7.2, 2.49, 7.77, 34};
+// Both products of the gradient in one launch: the same of 541 sizes; 1.5%, at
+// worst 22%.  Configurations 0 and 7 do not have it.
+const Rates BOTH = {{0, 0.44, 0.647, 0.799, 1.65, 1.53, 0.547, 0},
+                    {0, 0.93, 0.862, 1.04, 0.848, 0.502, 1.74, 0},
+                    {0, 1.37, 3.12, 4.64, 9.04, 4.23, 1.55, 0},
+                    {1, 1080, 770, 960, 1210, 1500, 1150, 1},
+                    0.418, 6.65, 6.15, 0.324, 4.76, 3.2, 6.86, 107};
+
+// Estimated microseconds of the products `w` of one configuration in one
+// launch, and their partials' way out and back.  Small ones take no less than
+// the host's time for their launches.
+double plan_cost(const Work* w, int products, const Rates& t, int cus) {
+    static const int per_cu[] = {2, 2, 1, 1, 1, 1, 3, 2};
+    const int cfg = w[0].p.cfg;
     const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
     double total = 0.0;
-    for (const Plan& q : p) total += q.direct + (double)(q.Mt * q.Nt - q.direct) * q.S;
-    const double active = total < cus ? total : cus;
-    const double room = 1.0 + 0.42 * (fmin(per_cu[cfg], ceil(total / cus)) - 1.0);
-    double group[4][2], power = 0.0, join = 0.0, launches = 6.0;
+    for (int i = 0; i < products; ++i) total += w[i].p.direct + ((double)w[i].p.Mt * w[i].p.Nt - w[i].p.direct) * w[i].p.S;
+    const double active = fmin(total, cus);
+    const double room = 1.0 + t.share * (fmin(per_cu[cfg], ceil(total / cus)) - 1.0);
+    // (sharing does not make a workgroup faster than it is alone)
+    const double slab = t.slab[cfg] * (total <= cus ? t.alone[cfg] : fmax(1.0, t.alone[cfg] / room));
+    double group[4][2], power = 0.0, memory = 0.0, join = 0.0, launches = 6.0;
     int groups = 0;
-    for (int i = 0; i < 2; ++i) {
-        const Plan& q = p[i];
-        const int64_t m = i ? K : rows, n = i ? N : K, k = i ? rows : N;
-        const double bytes = 128.0 * ((double)c.BN / q.Mt + (double)c.BM / q.Nt), split = (double)(q.Mt * q.Nt) - q.direct;
-        const double per = fmax(slab[cfg] * (total <= cus ? alone[cfg] : 1.0), fmax(bytes * active / 6.8e6, bytes / 35.4e3));
-        const double whole = room * (fixed[cfg] + ((double)(k / mlpc::BK) + (k % mlpc::BK ? 0.4 : 0.0)) * per);
-        power += (double)q.Mt * q.Nt * c.BM * c.BN * k * 2e-6 / cap[cfg];
-        if (q.S == 1 || q.direct) {
-            group[groups][0] = q.S == 1 ? q.direct + split : q.direct;
-            group[groups++][1] = whole;
+    for (int i = 0; i < products; ++i) {
+        const Plan& p = w[i].p;
+        const double M = (double)w[i].M, N = (double)w[i].N, K = (double)w[i].K, tiles = (double)p.Mt * p.Nt, split = tiles - p.direct;
+        const double bytes = 128.0 * ((double)c.BN / p.Mt + (double)c.BM / p.Nt);
+        const double per = fmax(slab, fmax(bytes * active / (t.all * 1e6), bytes / (t.cu * 1e3)));
+        power += tiles * c.BM * c.BN * K * 2e-6 / t.cap[cfg];
+        memory += 2.0 * (M * K + K * N) / (t.read * 1e6) + 2.0 * M * N / (t.write * 1e6);
+        if (p.S == 1 || p.direct) {
+            group[groups][0] = p.S == 1 ? tiles : p.direct;
+            group[groups++][1] = room * (t.fixed[cfg] + (floor(K / mlpc::BK) + (w[i].K % mlpc::BK ? t.ragged : 0.0)) * per);
         }
-        if (q.S == 1) continue;
-        group[groups][0] = split * q.S;
-        group[groups++][1] = room * (fixed[cfg] + q.ksp * per);
-        const double values = split * c.BM * c.BN * fmin(1.0, (double)m / ((double)q.Mt * c.BM)) * fmin(1.0, (double)n / ((double)q.Nt * c.BN));
-        join += 6.9 + values * 4 * q.S * 2 / 6.2e6;
-        launches += 2.6;
+        if (p.S == 1) continue;
+        group[groups][0] = split * p.S;
+        group[groups++][1] = room * (t.fixed[cfg] + p.ksp * per);
+        const double values = split * c.BM * c.BN * fmin(1.0, M / ((double)p.Mt * c.BM)) * fmin(1.0, N / ((double)p.Nt * c.BN));
+        join += t.launch + values * 4 * p.S * 2 / (t.join * 1e6);
+        launches += 2.8;
     }
     const double run = dealt(group, groups, floor(cus * room));
-    const double memory = 2.0 * (2.0 * rows * K + 2.0 * K * N + (double)rows * N) / 4.2e6;
+    // (below the launches' floor the estimate itself tells plans apart)
     return fmax(fmax(run, fmax(power, memory)) + join, launches) + 0.01 * (run + join);
 }
 
+Plan choose_plan(int64_t M, int64_t N, int64_t K, int pass, int cus) {
+    Plan best{};
+    double cost = 0.0;
+    bool found = false;
+    for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
+        if (!mlpc_linear_has(cfg, pass)) continue;
+        // (x^T dz has no short tiles)
+        if (pass != mlpc::PASS_DW && !config_fits(mlpc_linear_config(cfg), M)) continue;
+        uint32_t last = 0;
+        for (uint32_t split = 1; split <= MAX_SPLIT; ++split) {
+            const Work w = {make_plan(cfg, M, N, K, split, cus), M, N, K};
+            if (w.p.S == last) continue;
+            last = w.p.S;
+            if (!split_fits(w.p, cus)) break;
+            const double c = plan_cost(&w, 1, SINGLE, cus);
+            if (!found || c < cost) {
+                best = w.p;
+                cost = c;
+                found = true;
+            }
+        }
+    }
+    return best;
+}
+
 // Both products of the gradient in one launch, always: against launches of
-// their own, over 118 sizes of 1 to 8192 rows drawn after the fit, 24% less time
-// on average, at worst 6% more.  At most one of the two is split.
+// their own, over 80 sizes of 1 to 8192 rows drawn after the fit, 24% less time
+// on average, at worst 17% more (6 x 4600 x 4856: 27 -> 32 us).  At most one of
+// the two is split.
 void choose_both(int64_t rows, int64_t K, int64_t N, int cus, Plan (&best)[2]) {
     double cost = 0.0;
     bool found = false;
@@ -320,15 +319,15 @@ void choose_both(int64_t rows, int64_t K, int64_t N, int cus, Plan (&best)[2]) {
         for (int which = 0; which < 2; ++which) {
             uint32_t last = which;      // (unsplit plans once)
             for (uint32_t split = 1; split <= MAX_SPLIT; ++split) {
-                const Plan p[2] = {make_plan(cfg, rows, K, N, which ? 1 : split, cus),
-                                   make_plan(cfg, K, N, rows, which ? split : 1, cus)};
-                if (p[which].S == last) continue;
-                last = p[which].S;
-                if (!split_fits(p[which], cus)) break;
-                const double c = both_cost(p, rows, K, N, cus);
+                const Work w[2] = {{make_plan(cfg, rows, K, N, which ? 1 : split, cus), rows, K, N},
+                                   {make_plan(cfg, K, N, rows, which ? split : 1, cus), K, N, rows}};
+                if (w[which].p.S == last) continue;
+                last = w[which].p.S;
+                if (!split_fits(w[which].p, cus)) break;
+                const double c = plan_cost(w, 2, BOTH, cus);
                 if (!found || c < cost) {
-                    best[0] = p[0];
-                    best[1] = p[1];
+                    best[0] = w[0].p;
+                    best[1] = w[1].p;
                     cost = c;
                     found = true;
                 }
