@@ -191,7 +191,7 @@ constexpr int MAX_PARTS = 256;      // workgroups that keep column sums: one per
 // dres, 8192 x 8192 bf16 102 us, 5.3 TB/s of the operands; 2048 x 12288 f16
 // 44 us for 201 MB of operands and 25 MB of partials, 5.1 TB/s; 1000 x 8192
 // 17 us (four rows per workgroup, whose loads are a chain).
-template <int DT, int NT, int V, bool RAGGED>
+template <int DT, int NT, int V, bool RAGGED, bool ALONE>
 __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
     __shared__ float s[2][NT / 64][2];
     __shared__ float cols[NT * 8];      // one chunk of every thread's column sums
@@ -332,10 +332,11 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
     if (!a.dweight && !a.dbias) return;
     // the row groups' sums, chunk by chunk through LDS, added in group order
     // and written as the workgroup's row of partials, or as the gradients
-    // themselves by a workgroup that has every row
+    // themselves by one that has every row (ALONE; as a branch on a.parts it cost
+    // 2048 x 12288 1 us)
     float* part = a.part + (size_t)blockIdx.x * 2 * a.H;
     auto join = [&](float (&v)[8], int i, float* row, uint16_t* out) {
-        if (a.parts == 1 && !out) return;
+        if (ALONE && !out) return;
         const int c = (i * TR + (int)t) * 8, at = c < a.H ? place<RAGGED>(c, a.H) : c;
         __syncthreads();
 #pragma unroll
@@ -347,7 +348,7 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
             float sum = cols[j];
 #pragma unroll 4
             for (int k = 1; k < rpw; ++k) sum += cols[k * TR * 8 + j];
-            if (a.parts == 1) out[i * TR * 8 + j] = to_storage<DT>(sum);
+            if constexpr (ALONE) out[i * TR * 8 + j] = to_storage<DT>(sum);
             else row[i * TR * 8 + j] = sum;
         }
     };
@@ -520,22 +521,26 @@ static BackwardShape backward_shape(int H) {
     return {1024, tr, 1};
 }
 
-template <int DT, int NT, int V>
+template <int DT, int NT, int V, bool ALONE>
 static void backward_v(const NormArgs& a, int tr, hipStream_t s) {
-    if (a.H % 8) hipLaunchKernelGGL((norm_backward_kernel<DT, NT, V, true>), dim3(a.parts), dim3(NT), 0, s, a, tr);
-    else hipLaunchKernelGGL((norm_backward_kernel<DT, NT, V, false>), dim3(a.parts), dim3(NT), 0, s, a, tr);
+    if (a.H % 8) hipLaunchKernelGGL((norm_backward_kernel<DT, NT, V, true, ALONE>), dim3(a.parts), dim3(NT), 0, s, a, tr);
+    else hipLaunchKernelGGL((norm_backward_kernel<DT, NT, V, false, ALONE>), dim3(a.parts), dim3(NT), 0, s, a, tr);
+}
+
+template <int DT, bool ALONE>
+static void backward_held(const NormArgs& a, hipStream_t s) {
+    const BackwardShape b = backward_shape(a.H);
+    if (b.v == 1) backward_v<DT, 1024, 1, ALONE>(a, b.tr, s);
+    else if (b.nt == 768) backward_v<DT, 768, 2, ALONE>(a, b.tr, s);
+    else backward_v<DT, 1024, 2, ALONE>(a, b.tr, s);
 }
 
 template <int DT>
 static hipError_t backward_t(const NormArgs& a, hipStream_t s) {
     const bool sums = a.dweight || a.dbias;
     if (held(a.H)) {
-        if (a.parts > 0) {
-            const BackwardShape b = backward_shape(a.H);
-            if (b.v == 1) backward_v<DT, 1024, 1>(a, b.tr, s);
-            else if (b.nt == 768) backward_v<DT, 768, 2>(a, b.tr, s);
-            else backward_v<DT, 1024, 2>(a, b.tr, s);
-        }
+        if (a.parts == 1) backward_held<DT, true>(a, s);
+        else if (a.parts > 1) backward_held<DT, false>(a, s);
     } else if (a.parts > 0) {
         if (sums)
             hipLaunchKernelGGL(norm_cols_sweep_kernel<DT>, dim3((a.H + SWEEP_NT - 1) / SWEEP_NT, a.parts), dim3(SWEEP_NT), 0, s, a);
