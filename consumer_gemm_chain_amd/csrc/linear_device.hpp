@@ -23,7 +23,7 @@
 // 52-59% busy at 1.8-2.1 GHz on random fp16 operands, no LDS bank conflict):
 // 2048 x 12288 x 6144 fp16 takes 272-282 us for x W, 265-275 for dz W^T, 270
 // for x^T dz (1.10-1.17 PFLOP/s), 8192 x 4096 x 4096 224 us (1.22).  Single
-// tokens stream W at 5.7 TB/s (1 x 12288 x 6144: 26.5 us in the kernel).  In
+// tokens stream W at 5.4 TB/s (1 x 12288 x 6144: 27.9 us in the kernel).  In
 // between, rows padded to the tile, the partials of split tiles and the
 // memory's latency under two or three stages in flight share the loss: 300 x
 // 8192 x 5504 takes 45-48 us for 27 GFLOP and 95 MB of operands.
@@ -68,10 +68,16 @@ __device__ __forceinline__ int kr_chunk(int k, int c) {
     return c ^ ((2 * ((k & 3) | (((k >> 3) & 1) << 2))) & (CPR - 1));
 }
 
+// Physical chunk of logical chunk c in row r of a KC stage.  32-deep rows have
+// four chunks, so rows r, r + 4, r + 8, r + 12 share banks: the XOR gives them
+// 0, 2, 3, 1, which keeps them apart whether they are read at one chunk or, as
+// the 16 lanes that ds_read_b128 serves together take them, two of them at a
+// chunk and the other two at its neighbour (conflict cycles 0.18-0.27 of the
+// busy ones with 0, 1, 2, 3, none with these; 2048 x 12288 x 6144 309 -> 308 us).
 template <int KS>
 __device__ __forceinline__ int kc_chunk(int r, int c) {
     if constexpr (KS == 64) return a_chunk(r, c);
-    else return a_chunk32(r, c);
+    else return c ^ (((r >> 3) & 1) | ((((r >> 2) ^ (r >> 3)) & 1) << 1));
 }
 
 // One operand of a tile: `lim` rows (KC) or columns (KR) from `r0` on.
