@@ -72,6 +72,19 @@ struct DzArgs {
     int parts;
 };
 
+template <class T>
+struct Param {
+    using type = T;
+};
+
+// Launch `kernel` and return the launch's own status (hipGetLastError would
+// also report what an earlier call of the thread, not ours perhaps, left).
+template <class... P>
+hipError_t launch(void (*kernel)(P...), dim3 grid, int threads, hipStream_t s, typename Param<P>::type... args) {
+    void* p[] = {&args...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), p, 0, s);
+}
+
 }  // namespace mlpc
 
 hipError_t mlpc_norm_forward(const mlpc::NormArgs& a, int dtype, int cus, hipStream_t s);

@@ -111,25 +111,24 @@ __global__ __launch_bounds__(256) void db_kernel(DzArgs a, int n) {
 }
 
 template <int DT, int ACT>
-static void dz_launch(const DzArgs& a, hipStream_t s) {
-    if (a.parts == 1)
-        hipLaunchKernelGGL((dz_kernel<DT, ACT, 64>), dim3((a.N + 63) / 64), dim3(DZ_NT), 0, s, a);
-    else
-        hipLaunchKernelGGL((dz_kernel<DT, ACT, 256>), dim3((a.N + 255) / 256, a.parts), dim3(DZ_NT), 0, s, a);
+static hipError_t dz_launch(const DzArgs& a, hipStream_t s) {
+    if (a.parts == 1) return launch(dz_kernel<DT, ACT, 64>, dim3((a.N + 63) / 64), DZ_NT, s, a);
+    return launch(dz_kernel<DT, ACT, 256>, dim3((a.N + 255) / 256, a.parts), DZ_NT, s, a);
 }
 
 template <int DT>
 static hipError_t dz_t(const DzArgs& a, bool join, hipStream_t s) {
+    hipError_t e = hipSuccess;
     if (a.parts > 0) {
-        if (a.act == ACT_NONE) dz_launch<DT, ACT_NONE>(a, s);
-        else if (a.act == ACT_GELU_TANH) dz_launch<DT, ACT_GELU_TANH>(a, s);
-        else dz_launch<DT, ACT_SWIGLU>(a, s);
+        if (a.act == ACT_NONE) e = dz_launch<DT, ACT_NONE>(a, s);
+        else if (a.act == ACT_GELU_TANH) e = dz_launch<DT, ACT_GELU_TANH>(a, s);
+        else e = dz_launch<DT, ACT_SWIGLU>(a, s);
     }
-    if (a.db && join && a.parts != 1) {
+    if (e == hipSuccess && a.db && join && a.parts != 1) {
         const int n = a.act == ACT_SWIGLU ? 2 * a.N : a.N;
-        hipLaunchKernelGGL(db_kernel<DT>, dim3((n + 31) / 32), dim3(256), 0, s, a, n);
+        e = launch(db_kernel<DT>, dim3((n + 31) / 32), 256, s, a, n);
     }
-    return hipGetLastError();
+    return e;
 }
 
 }  // namespace mlpc

@@ -32,23 +32,22 @@ template <int DT>
 static hipError_t both(const GemmArgs& dx, const GemmArgs& dw, const DzArgs& dz, hipStream_t s) {
     if constexpr (HAS_BOTH) {
         const uint32_t n = blocks(dx), db = dz.db ? (dw.N + Cfg::NT - 1) / Cfg::NT : 0;
-        hipLaunchKernelGGL((linear_both_kernel<Cfg, DT>), dim3(db + n + blocks(dw)), dim3(Cfg::NT), 0, s, dx, dw, dz, db, n);
-        return hipGetLastError();
+        return launch(linear_both_kernel<Cfg, DT>, dim3(db + n + blocks(dw)), Cfg::NT, s, dx, dw, dz, db, n);
     }
     return hipErrorInvalidValue;
 }
 
 template <int DT>
-static hipError_t launch(const GemmArgs& a, int pass, hipStream_t s) {
+static hipError_t one(const GemmArgs& a, int pass, hipStream_t s) {
     const dim3 grid(blocks(a));
     if constexpr (has(PASS_FWD)) {
-        if (pass == PASS_FWD) hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_FWD>), grid, dim3(Cfg::NT), 0, s, a);
-        if (pass == PASS_DX) hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_DX>), grid, dim3(Cfg::NT), 0, s, a);
+        if (pass == PASS_FWD) return launch(linear_kernel<Cfg, DT, PASS_FWD>, grid, Cfg::NT, s, a);
+        if (pass == PASS_DX) return launch(linear_kernel<Cfg, DT, PASS_DX>, grid, Cfg::NT, s, a);
     }
     if constexpr (has(PASS_DW)) {
-        if (pass == PASS_DW) hipLaunchKernelGGL((linear_kernel<Cfg, DT, PASS_DW>), grid, dim3(Cfg::NT), 0, s, a);
+        if (pass == PASS_DW) return launch(linear_kernel<Cfg, DT, PASS_DW>, grid, Cfg::NT, s, a);
     }
-    return has(pass) ? hipGetLastError() : hipErrorInvalidValue;
+    return hipErrorInvalidValue;
 }
 
 }  // namespace mlpc
@@ -59,7 +58,7 @@ using namespace mlpc;
 #define MLPC_CAT(a, b) MLPC_CAT2(a, b)
 
 hipError_t MLPC_CAT(mlpc_linear_launch, MLPC_LIN)(const GemmArgs& a, int pass, int dtype, hipStream_t s) {
-    return dtype == DT_F16 ? launch<DT_F16>(a, pass, s) : launch<DT_BF16>(a, pass, s);
+    return dtype == DT_F16 ? one<DT_F16>(a, pass, s) : one<DT_BF16>(a, pass, s);
 }
 
 hipError_t MLPC_CAT(mlpc_linear_both, MLPC_LIN)(const GemmArgs& dx, const GemmArgs& dw, const DzArgs& dz, int dtype,

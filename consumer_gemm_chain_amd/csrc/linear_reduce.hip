@@ -72,7 +72,5 @@ hipError_t mlpc_gemm_reduce(const GemmArgs& a, int dtype, hipStream_t s) {
     const int rows = a.M < a.BM ? a.M : a.BM, chunks = rows * ((a.up ? a.BN / 2 : a.BN) / 8);
     const int per_tile = (chunks + RNT - 1) / RNT;
     const dim3 grid((a.Mt * a.Nt - a.direct) * per_tile);
-    if (dtype == DT_F16) hipLaunchKernelGGL(linear_reduce_kernel<DT_F16>, grid, dim3(RNT), 0, s, a, per_tile);
-    else hipLaunchKernelGGL(linear_reduce_kernel<DT_BF16>, grid, dim3(RNT), 0, s, a, per_tile);
-    return hipGetLastError();
+    return launch(dtype == DT_F16 ? linear_reduce_kernel<DT_F16> : linear_reduce_kernel<DT_BF16>, grid, RNT, s, a, per_tile);
 }

@@ -480,15 +480,13 @@ static hipError_t forward_v(const NormArgs& a, int cus, hipStream_t s) {
     // up to eight workgroups per CU, so that long batches reuse their weights
     const int64_t groups = (a.rows + FWD_NT / TR - 1) / (FWD_NT / TR), most = (int64_t)cus * 8;
     const dim3 grid((unsigned)(groups < most ? groups : most));
-    if (a.H % 8) hipLaunchKernelGGL((norm_forward_kernel<DT, TR, V, true>), grid, dim3(FWD_NT), 0, s, a);
-    else hipLaunchKernelGGL((norm_forward_kernel<DT, TR, V, false>), grid, dim3(FWD_NT), 0, s, a);
-    return hipGetLastError();
+    if (a.H % 8) return launch(norm_forward_kernel<DT, TR, V, true>, grid, FWD_NT, s, a);
+    return launch(norm_forward_kernel<DT, TR, V, false>, grid, FWD_NT, s, a);
 }
 
 template <int DT>
 static hipError_t forward_sweep(const NormArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(norm_forward_sweep_kernel<DT>, dim3((unsigned)a.rows), dim3(SWEEP_NT), 0, s, a);
-    return hipGetLastError();
+    return launch(norm_forward_sweep_kernel<DT>, dim3((unsigned)a.rows), SWEEP_NT, s, a);
 }
 
 template <int DT>
@@ -522,32 +520,32 @@ static BackwardShape backward_shape(int H) {
 }
 
 template <int DT, int NT, int V, bool ALONE>
-static void backward_v(const NormArgs& a, int tr, hipStream_t s) {
-    if (a.H % 8) hipLaunchKernelGGL((norm_backward_kernel<DT, NT, V, true, ALONE>), dim3(a.parts), dim3(NT), 0, s, a, tr);
-    else hipLaunchKernelGGL((norm_backward_kernel<DT, NT, V, false, ALONE>), dim3(a.parts), dim3(NT), 0, s, a, tr);
+static hipError_t backward_v(const NormArgs& a, int tr, hipStream_t s) {
+    if (a.H % 8) return launch(norm_backward_kernel<DT, NT, V, true, ALONE>, dim3(a.parts), NT, s, a, tr);
+    return launch(norm_backward_kernel<DT, NT, V, false, ALONE>, dim3(a.parts), NT, s, a, tr);
 }
 
 template <int DT, bool ALONE>
-static void backward_held(const NormArgs& a, hipStream_t s) {
+static hipError_t backward_held(const NormArgs& a, hipStream_t s) {
     const BackwardShape b = backward_shape(a.H);
-    if (b.v == 1) backward_v<DT, 1024, 1, ALONE>(a, b.tr, s);
-    else if (b.nt == 768) backward_v<DT, 768, 2, ALONE>(a, b.tr, s);
-    else backward_v<DT, 1024, 2, ALONE>(a, b.tr, s);
+    if (b.v == 1) return backward_v<DT, 1024, 1, ALONE>(a, b.tr, s);
+    if (b.nt == 768) return backward_v<DT, 768, 2, ALONE>(a, b.tr, s);
+    return backward_v<DT, 1024, 2, ALONE>(a, b.tr, s);
 }
 
 template <int DT>
 static hipError_t backward_t(const NormArgs& a, hipStream_t s) {
     const bool sums = a.dweight || a.dbias;
+    hipError_t e = hipSuccess;
     if (held(a.H)) {
-        if (a.parts == 1) backward_held<DT, true>(a, s);
-        else if (a.parts > 1) backward_held<DT, false>(a, s);
+        if (a.parts == 1) return backward_held<DT, true>(a, s);
+        if (a.parts > 1) e = backward_held<DT, false>(a, s);
     } else if (a.parts > 0) {
-        if (sums)
-            hipLaunchKernelGGL(norm_cols_sweep_kernel<DT>, dim3((a.H + SWEEP_NT - 1) / SWEEP_NT, a.parts), dim3(SWEEP_NT), 0, s, a);
-        hipLaunchKernelGGL(norm_dx_sweep_kernel<DT>, dim3((unsigned)a.rows), dim3(SWEEP_NT), 0, s, a);
+        if (sums) e = launch(norm_cols_sweep_kernel<DT>, dim3((a.H + SWEEP_NT - 1) / SWEEP_NT, a.parts), SWEEP_NT, s, a);
+        if (e == hipSuccess) e = launch(norm_dx_sweep_kernel<DT>, dim3((unsigned)a.rows), SWEEP_NT, s, a);
     }
-    if (sums && !(held(a.H) && a.parts == 1)) hipLaunchKernelGGL(norm_cols_sum_kernel<DT>, dim3((2 * a.H + 31) / 32), dim3(1024), 0, s, a);
-    return hipGetLastError();
+    if (e == hipSuccess && sums) e = launch(norm_cols_sum_kernel<DT>, dim3((2 * a.H + 31) / 32), 1024, s, a);
+    return e;
 }
 
 }  // namespace mlpc
