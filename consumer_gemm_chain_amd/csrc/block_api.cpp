@@ -59,6 +59,9 @@ int fail(int code, const char* fmt, ...) {
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
+    // an error of the runtime is reported here, not once more by the caller's
+    // next look at the thread's last error
+    if (code == MLP_EHIP || code == MLP_ENOMEM) (void)hipGetLastError();
     return mlpc_set_error(code, buf);
 }
 

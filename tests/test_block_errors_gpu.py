@@ -7,7 +7,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from consumer_gemm_chain_amd import MlpLinear, MlpNorm  # noqa: E402
+from consumer_gemm_chain_amd import MlpChainError, MlpLinear, MlpNorm  # noqa: E402
 from consumer_gemm_chain_amd import mlp_chain as mc  # noqa: E402
 
 OUT_OF_MEMORY = 2       # hipErrorOutOfMemory
@@ -48,3 +48,13 @@ def test_an_error_left_by_another_call_is_not_reported(runtime):
         lin.backward(dy, x, None, dw=lw, db=lb, z=dy)
         assert runtime.hipGetLastError() == OUT_OF_MEMORY
         torch.cuda.synchronize()
+
+
+def test_a_handle_that_does_not_fit_leaves_no_error(runtime):
+    """create refuses, and torch's next launch does not find the failed allocation."""
+    with pytest.raises(MlpChainError, match="hipMalloc"):
+        MlpLinear(1 << 24, 8, 1 << 21, "gelu_tanh")
+    assert runtime.hipGetLastError() == 0
+    with pytest.raises(MlpChainError, match="hipMalloc"):
+        MlpLinear(1 << 24, 8, 1 << 21, "gelu_tanh")
+    assert bool((torch.ones(8, device="cuda") + 1 == 2).all())
