@@ -28,23 +28,21 @@
 #include <string.h>
 
 #include <new>
-#include <string>
 
 #include "../../include/mlp_chain.h"
 #include "chain_launch.h"
 
 namespace {
 
-thread_local std::string g_err;
+// (fixed storage: reporting an error allocates nothing, so nothing can throw)
+thread_local char g_err[512];
 
 int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int code, const char* fmt, ...) {
-    char buf[512];
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
     va_end(ap);
-    g_err = buf;
     return code;
 }
 
@@ -57,7 +55,7 @@ uint32_t cdiv(int64_t a, int64_t b) { return (uint32_t)((a + b - 1) / b); }
 }  // namespace
 
 int mlpc_set_error(int code, const char* msg) {
-    g_err = msg;
+    snprintf(g_err, sizeof g_err, "%s", msg);
     return code;
 }
 
@@ -611,14 +609,14 @@ int check_chain_args(int64_t M, int64_t H, int64_t I, int act, int policy) {
 
 extern "C" {
 
-const char* mlp_chain_last_error(void) { return g_err.c_str(); }
+const char* mlp_chain_last_error(void) { return g_err; }
 
 mlp_chain_t mlp_chain_create(int64_t M, int64_t H, int64_t I, int act, int dtype, int policy) {
     return mlp_chain_create_layers(M, H, I, act, dtype, policy, 1);
 }
 
 mlp_chain_t mlp_chain_create_layers(int64_t M, int64_t H, int64_t I, int act, int dtype, int policy, int layers) {
-    g_err.clear();
+    g_err[0] = 0;
     if (check_chain_args(M, H, I, act, policy) != MLP_OK) return nullptr;
     if (layers < 1 || layers > (int)mlpc::MAX_LAYERS) {
         fail(MLP_EINVAL, "layers must be in 1..%u, got %d", mlpc::MAX_LAYERS, layers);
