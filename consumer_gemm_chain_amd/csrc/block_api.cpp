@@ -19,7 +19,7 @@ struct mlp_norm {
     int device, cus;
     float eps;
     float* part;                // [max parts][2][H]; nullptr: no gradient
-    hipStream_t last_stream;
+    hipStream_t last_stream;    // of the last gradient: the forward pass leaves the handle alone
 };
 
 // How a product runs: tile configuration, tiles, the tiles computed whole, the
@@ -419,11 +419,12 @@ int run_both(mlp_linear* h, int64_t rows, mlpc::GemmArgs& dx, mlpc::GemmArgs& dw
     return launched(e);
 }
 
-// Wait for the handle's last call and release its workspace.
+// Wait for the last call that used the workspace, if there is one, and release it.
 int release(int device, hipStream_t last, void* ws) {
+    if (!ws) return MLP_OK;
     DeviceGuard g(device);
     const hipError_t e1 = hipStreamSynchronize(last);
-    const hipError_t e2 = ws ? hipFree(ws) : hipSuccess;
+    const hipError_t e2 = hipFree(ws);
     if (e1 != hipSuccess || e2 != hipSuccess)
         return fail(MLP_EHIP, "destroy: %s", hipGetErrorString(e1 != hipSuccess ? e1 : e2));
     return MLP_OK;
@@ -483,7 +484,6 @@ int mlp_norm_forward(mlp_norm_t h, int64_t rows, const void* x, int64_t ldx, con
     DeviceGuard g(h->device);
     if (!g.ok) return fail(MLP_EHIP, "cannot select the handle's device %d", h->device);
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    h->last_stream = s;
     mlpc::NormArgs a{};
     a.x = static_cast<const uint16_t*>(x);
     a.weight = static_cast<const uint16_t*>(weight);

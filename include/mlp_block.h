@@ -47,8 +47,9 @@
  * be captured into a HIP graph) and depends on nothing from earlier calls.
  * A handle owns its workspace, so calls on one handle that may use it (every
  * call of a linear handle, the gradients of a norm) must be ordered on one
- * stream; separate handles are independent.  destroy waits for the stream of
- * the handle's last call.
+ * stream; separate handles are independent, and so are a norm's forward
+ * passes, from any thread and on any stream.  destroy waits for the stream of
+ * the handle's last call that may use the workspace.
  */
 #ifndef MLP_BLOCK_H
 #define MLP_BLOCK_H

@@ -127,8 +127,30 @@ static void errors_are_reported_once() {
     sync_fails = hipSuccess;
 }
 
+// destroy waits for the work that may still use the workspace it frees: the
+// last gradient, on whatever stream a forward pass (which uses none) came after.
+static void destroy_waits_for_the_workspace() {
+    hipStream_t one = reinterpret_cast<hipStream_t>(stat), other = reinterpret_cast<hipStream_t>(buf);
+    mlp_norm_t n = mlp_norm_create(64, 0, 1e-5f, 1);
+    CHECK(norm_backward(n, one) == MLP_OK && norm_forward(n, other) == MLP_OK);
+    waited.clear();
+    CHECK(mlp_norm_destroy(n) == MLP_OK);
+    CHECK(waited.size() == 1 && waited[0] == one);
+    // a handle without a workspace has nothing to wait for
+    n = mlp_norm_create(64, 0, 1e-5f, 0);
+    CHECK(norm_forward(n, one) == MLP_OK);
+    waited.clear();
+    CHECK(mlp_norm_destroy(n) == MLP_OK && waited.empty());
+    mlp_linear_t l = mlp_linear_create(4, 64, 64, 0, 0, 1);
+    CHECK(linear_forward(l, one) == MLP_OK && linear_forward(l, other) == MLP_OK);
+    waited.clear();
+    CHECK(mlp_linear_destroy(l) == MLP_OK);
+    CHECK(waited.size() == 1 && waited[0] == other);
+}
+
 int main() {
     errors_are_reported_once();
+    destroy_waits_for_the_workspace();
     CHECK(blocks == 0);
     printf("%d failures\n", failures);
     return failures != 0;
