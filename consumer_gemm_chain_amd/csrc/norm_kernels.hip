@@ -405,30 +405,36 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+// At most this many workgroups, which then walk the rows: a launch of one per
+// row would pass HIP's limit of 2^32 threads at 2^24 rows.
+constexpr int64_t SWEEP_GRID = 1 << 16;
+static dim3 sweep_grid(int64_t rows) { return dim3((unsigned)(rows < SWEEP_GRID ? rows : SWEEP_GRID)); }
+
 // One workgroup per row: three sweeps, the second and third from the caches.
 template <int DT>
 __global__ __launch_bounds__(SWEEP_NT) void norm_forward_sweep_kernel(NormArgs a) {
     __shared__ float s[SWEEP_NT / 64];
-    const size_t r = blockIdx.x;
-    const uint16_t* x = a.x + r * a.ldx;
-    float t = 0.f;
-    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) t += widen<DT>(x[c]);
-    const float mean = block_sum(t, s) / a.H;
-    t = 0.f;
-    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
-        const float d = widen<DT>(x[c]) - mean;
-        t += d * d;
-    }
-    const float rstd = 1.0f / sqrtf(block_sum(t, s) / a.H + a.eps);
-    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
-        float v = (widen<DT>(x[c]) - mean) * rstd;
-        if (a.weight) v *= widen<DT>(a.weight[c]);
-        if (a.bias) v += widen<DT>(a.bias[c]);
-        a.y[r * a.ldy + c] = to_storage<DT>(v);
-    }
-    if (threadIdx.x == 0) {
-        if (a.mean) a.mean[r] = mean;
-        if (a.rstd) a.rstd[r] = rstd;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const uint16_t* x = a.x + r * a.ldx;
+        float t = 0.f;
+        for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) t += widen<DT>(x[c]);
+        const float mean = block_sum(t, s) / a.H;
+        t = 0.f;
+        for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
+            const float d = widen<DT>(x[c]) - mean;
+            t += d * d;
+        }
+        const float rstd = 1.0f / sqrtf(block_sum(t, s) / a.H + a.eps);
+        for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
+            float v = (widen<DT>(x[c]) - mean) * rstd;
+            if (a.weight) v *= widen<DT>(a.weight[c]);
+            if (a.bias) v += widen<DT>(a.bias[c]);
+            a.y[r * a.ldy + c] = to_storage<DT>(v);
+        }
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[r] = mean;
+            if (a.rstd) a.rstd[r] = rstd;
+        }
     }
 }
 
@@ -436,22 +442,23 @@ __global__ __launch_bounds__(SWEEP_NT) void norm_forward_sweep_kernel(NormArgs a
 template <int DT>
 __global__ __launch_bounds__(SWEEP_NT) void norm_dx_sweep_kernel(NormArgs a) {
     __shared__ float s[SWEEP_NT / 64];
-    const size_t r = blockIdx.x;
-    const uint16_t* x = a.x + r * a.ldx;
-    const uint16_t* dy = a.dy + r * a.lddy;
-    const float mean = a.mean[r], rstd = a.rstd[r];
-    float t0 = 0.f, t1 = 0.f;
-    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
-        const float g = widen<DT>(dy[c]) * (a.weight ? widen<DT>(a.weight[c]) : 1.f);
-        t0 += g;
-        t1 += g * ((widen<DT>(x[c]) - mean) * rstd);
-    }
-    const float m0 = block_sum(t0, s) / a.H, m1 = block_sum(t1, s) / a.H;
-    for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
-        const float g = widen<DT>(dy[c]) * (a.weight ? widen<DT>(a.weight[c]) : 1.f);
-        float v = rstd * (g - m0 - (widen<DT>(x[c]) - mean) * rstd * m1);
-        if (a.dres) v += widen<DT>(a.dres[r * a.lddres + c]);
-        a.dx[r * a.lddx + c] = to_storage<DT>(v);
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const uint16_t* x = a.x + r * a.ldx;
+        const uint16_t* dy = a.dy + r * a.lddy;
+        const float mean = a.mean[r], rstd = a.rstd[r];
+        float t0 = 0.f, t1 = 0.f;
+        for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
+            const float g = widen<DT>(dy[c]) * (a.weight ? widen<DT>(a.weight[c]) : 1.f);
+            t0 += g;
+            t1 += g * ((widen<DT>(x[c]) - mean) * rstd);
+        }
+        const float m0 = block_sum(t0, s) / a.H, m1 = block_sum(t1, s) / a.H;
+        for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
+            const float g = widen<DT>(dy[c]) * (a.weight ? widen<DT>(a.weight[c]) : 1.f);
+            float v = rstd * (g - m0 - (widen<DT>(x[c]) - mean) * rstd * m1);
+            if (a.dres) v += widen<DT>(a.dres[r * a.lddres + c]);
+            a.dx[r * a.lddx + c] = to_storage<DT>(v);
+        }
     }
 }
 
@@ -486,7 +493,7 @@ static hipError_t forward_v(const NormArgs& a, int cus, hipStream_t s) {
 
 template <int DT>
 static hipError_t forward_sweep(const NormArgs& a, hipStream_t s) {
-    return launch(norm_forward_sweep_kernel<DT>, dim3((unsigned)a.rows), SWEEP_NT, s, a);
+    return launch(norm_forward_sweep_kernel<DT>, sweep_grid(a.rows), SWEEP_NT, s, a);
 }
 
 template <int DT>
@@ -542,7 +549,7 @@ static hipError_t backward_t(const NormArgs& a, hipStream_t s) {
         if (a.parts > 1) e = backward_held<DT, false>(a, s);
     } else if (a.parts > 0) {
         if (sums) e = launch(norm_cols_sweep_kernel<DT>, dim3((a.H + SWEEP_NT - 1) / SWEEP_NT, a.parts), SWEEP_NT, s, a);
-        if (e == hipSuccess) e = launch(norm_dx_sweep_kernel<DT>, dim3((unsigned)a.rows), SWEEP_NT, s, a);
+        if (e == hipSuccess) e = launch(norm_dx_sweep_kernel<DT>, sweep_grid(a.rows), SWEEP_NT, s, a);
     }
     if (e == hipSuccess && sums) e = launch(norm_cols_sum_kernel<DT>, dim3((2 * a.H + 31) / 32), 1024, s, a);
     return e;
