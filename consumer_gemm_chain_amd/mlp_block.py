@@ -245,7 +245,8 @@ class MlpBlock:
     """The pre-norm MLP block y = x + act(norm(x) W1 + b1) W2 + b2 for up to
     `rows` rows, H wide with I inner columns: one norm and two linear layers,
     and their gradients.  `params` maps names to tensors: weight, bias [H],
-    w1 [H, gI], b1 [gI], w2 [I, H], b2 [H].  grad=False: forward only."""
+    w1 [H, gI], b1 [gI], w2 [I, H], b2 [H]; None leaves out the norm's scale or
+    shift or a bias.  grad=False: forward only."""
 
     def __init__(self, rows: int, H: int, I: int, act: str = "gelu_tanh", dtype: str = "f16", eps: float = 1e-5,
                  grad: bool = True):
@@ -279,10 +280,10 @@ class MlpBlock:
         return (y, (x, n, a, z, mean, rstd)) if save else y
 
     def backward(self, dy, params, saved):
-        """dx and the gradients of every parameter, by name."""
+        """dx and the gradients of every parameter, by name (None for an absent one)."""
         import torch
         x, n, a, z, mean, rstd = saved
-        grads = {k: torch.empty_like(v) for k, v in params.items()}
+        grads = {k: None if v is None else torch.empty_like(v) for k, v in params.items()}
         da, dn, dx = torch.empty_like(a), torch.empty_like(n), torch.empty_like(x)
         self.lin2.backward(dy, a, params["w2"], dx=da, dw=grads["w2"], db=grads["b2"])
         self.lin1.backward(da, n, params["w1"], dx=dn, dw=grads["w1"], db=grads["b1"], z=z)
