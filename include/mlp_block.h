@@ -29,7 +29,12 @@
  * rounded to the storage type before the two products of the linear
  * gradient, whose operands the matrix cores take in 16 bits; dbias sums it
  * unrounded.  Reductions have a fixed order: the same call gives the same
- * bits.  NaN and infinity pass through as in the formulas.
+ * bits.  The outputs that the formulas make depend on a NaN or an infinity are
+ * not finite either, the others are not touched by it; gelu_tanh's gradient at
+ * an infinite z is its limit, dy or 0 (the formula has no value there).  fp32
+ * bounds what is between: a dz or an output beyond the storage type is
+ * infinite, a variance beyond fp32 (elements past 1e19, bf16) makes a row's
+ * rstd 0.
  *
  * Row counts: any R >= 0 per call, up to the handle's limit.  With R = 0
  * nothing is read and operands of R rows may be NULL; the forward passes
