@@ -50,6 +50,7 @@ __device__ __forceinline__ void store8(uint16_t* row, int c, int skip, u32x4 v) 
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float uniform(float v) { return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v))); }
 
 // v + v rotated by N lanes within each row of 16.
 template <int N>
@@ -84,7 +85,7 @@ template <int DT, int TR, int V, bool RAGGED>
 __global__ __launch_bounds__(FWD_NT, V <= 2 ? 8 : V <= 4 ? 5 : 4) void norm_forward_kernel(NormArgs a) {
     constexpr int RPW = FWD_NT / TR;
     __shared__ float s[2][FWD_NT / 64];
-    const int t = threadIdx.x % TR, sub = uniform(threadIdx.x / TR);
+    const int t = threadIdx.x % TR, sub = uniform((int)(threadIdx.x / TR));
     u32x4 w[V], b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -185,9 +186,9 @@ constexpr int MAX_PARTS = 256;      // workgroups that keep column sums: one per
 // TR threads per row (whole waves, a divisor of NT), V chunks per thread, NT / TR rows at a time.  A workgroup walks the rows with its
 // columns' sums in registers and the next rows' loads in flight, and leaves
 // one row of partial sums: large workgroups, one per CU, keep those
-// partials (8 H bytes each) small against the rows.  With d = x - mean the
-// row needs the sums of g and g d; dx = rstd g - rstd mean_c(g) -
-// d rstd^3 mean_c(g d) + dres.  Bound by memory, the partials included: with
+// partials (8 H bytes each) small against the rows.  A row needs the sums of g
+// and g xhat; xhat itself is kept, for with (x - mean) and a factor of rstd^2
+// rows with an rstd past 1.8e19 would overflow.  Bound by memory, the partials included: with
 // dres, 8192 x 8192 bf16 102 us, 5.3 TB/s of the operands; 2048 x 12288 f16
 // 44 us for 201 MB of operands and 25 MB of partials, 5.1 TB/s; 1000 x 8192
 // 17 us (four rows per workgroup, whose loads are a chain).
@@ -195,7 +196,7 @@ template <int DT, int NT, int V, bool RAGGED, bool ALONE>
 __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
     __shared__ float s[2][NT / 64][2];
     __shared__ float cols[NT * 8];      // one chunk of every thread's column sums
-    const int sub = uniform(threadIdx.x / TR), rpw = NT / TR;
+    const int sub = uniform((int)(threadIdx.x / TR)), rpw = NT / TR;
     const uint32_t t = threadIdx.x - sub * TR;
     const int wave = threadIdx.x >> 6, first = sub * (TR / 64), waves = TR / 64;
     const float inv = 1.0f / a.H;
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
         const int64_t r = r0 + sub;
         const bool live = r < a.rows;
         u32x4 cx[V], cdy[V], dr[V];
-        const float m = mean, rs = rstd;
+        const float m = uniform(mean), rs = uniform(rstd);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             cx[i] = x[i];
@@ -250,13 +251,13 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
             }
         }
         if (r0 + step < a.rows) fetch(r + step);
-        // dy, g and d of chunk i (where dy = 0, past the row or shared with
+        // dy, g and xhat of chunk i (where dy = 0, past the row or shared with
         // the chunk before, so is all that is summed)
-        auto terms = [&](int i, float (&e)[8], float (&g)[8], float (&d)[8]) {
+        auto terms = [&](int i, float (&e)[8], float (&g)[8], float (&xhat)[8]) {
             pin(cdy[i]);
             pin(cx[i]);
             widen8<DT>(cdy[i], e);
-            widen8<DT>(cx[i], d);
+            widen8<DT>(cx[i], xhat);
             if constexpr (RAGGED) {
                 const int skip = (i * TR + (int)fresh(t)) * 8 - (a.H - 8);
 #pragma unroll
@@ -267,24 +268,24 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 g[k] *= e[k];
-                d[k] -= m;
+                xhat[k] = (xhat[k] - m) * rs;
             }
         };
         float t0 = 0.f, t1 = 0.f;
-        float g[V][8], d[V][8];
+        float g[V][8], xhat[V][8];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float e[8], u0 = 0.f, u1 = 0.f;
-            terms(i, e, g[i], d[i]);
+            terms(i, e, g[i], xhat[i]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 // (two chains each)
                 float& v0 = k & 1 ? u0 : t0;
                 float& v1 = k & 1 ? u1 : t1;
                 v0 += g[i][k];
-                v1 = __builtin_fmaf(g[i][k], d[i][k], v1);
+                v1 = __builtin_fmaf(g[i][k], xhat[i][k], v1);
                 sb[i][k] += e[k];
-                sw[i][k] = __builtin_fmaf(e[k] * rs, d[i][k], sw[i][k]);
+                sw[i][k] = __builtin_fmaf(e[k], xhat[i][k], sw[i][k]);
             }
             t0 += u0;
             t1 += u1;
@@ -307,7 +308,7 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
             }
         }
         if (!live) continue;
-        const float b0 = -rs * (t0 * inv), b1 = -(rs * rs) * (rs * (t1 * inv));
+        const float b0 = -rs * (t0 * inv), b1 = -rs * (t1 * inv);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = (i * TR + (int)fresh(t)) * 8;
@@ -315,9 +316,9 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
             float e[8];
             // 16 waves' registers do not hold two chunks' fp32 values beside
             // the sums: taken again from the packed ones
-            if constexpr (V > 1 && NT > 768) terms(i, e, g[i], d[i]);
+            if constexpr (V > 1 && NT > 768) terms(i, e, g[i], xhat[i]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) e[k] = __builtin_fmaf(d[i][k], b1, __builtin_fmaf(g[i][k], rs, b0));
+            for (int k = 0; k < 8; ++k) e[k] = __builtin_fmaf(xhat[i][k], b1, __builtin_fmaf(g[i][k], rs, b0));
             if (a.dres) {
                 float q[8];
                 widen8<DT>(dr[i], q);

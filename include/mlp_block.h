@@ -33,8 +33,8 @@
  * not finite either, the others are not touched by it; gelu_tanh's gradient at
  * an infinite z is its limit, dy or 0 (the formula has no value there).  fp32
  * bounds what is between: a dz or an output beyond the storage type is
- * infinite, a variance beyond fp32 (elements past 1e19, bf16) makes a row's
- * rstd 0.
+ * infinite, and a row whose sum of (x - mean)^2 passes 3.4e38 (bf16) gets an
+ * rstd of 0.
  *
  * Row counts: any R >= 0 per call, up to the handle's limit.  With R = 0
  * nothing is read and operands of R rows may be NULL; the forward passes
