@@ -106,6 +106,7 @@ class _Layer:
     """Owns one handle; `_destroy` releases it.  The checks below run on every
     call, beside a few microseconds of kernel, and touch each tensor little."""
     h = None
+    device = None       # the handle's: the current one when it was created
 
     def _set_type(self, dtype: str):
         import torch
@@ -139,14 +140,18 @@ class _Layer:
             return int(getattr(stream, "cuda_stream", stream))
         return self._raw_stream(t.get_device())
 
+    def _hold(self, h):
+        import torch
+        self.h, self.device = h, torch.cuda.current_device()
+
     def _rows(self, name, t, rows, width):
         """Pointer and row stride of a [rows, width] operand (None, 0: absent)."""
         if t is None:
             return None, 0
         if t.shape != (rows, width):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, width)}")
-        if t.dtype != self.torch_dtype or not t.is_cuda:
-            raise ValueError(f"{name} must be a {self.dtype} device tensor")
+        if t.dtype != self.torch_dtype or t.get_device() != self.device:
+            raise ValueError(f"{name} must be a {self.dtype} tensor on the handle's device {self.device}")
         ld, unit = t.stride()
         if unit != 1 and width > 1:
             raise ValueError(f"{name} must have contiguous rows, got strides {(ld, unit)}")
@@ -158,20 +163,21 @@ class _Layer:
             return None
         if t.shape != (n,) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous vector of {n} elements, got shape {tuple(t.shape)}")
-        if t.dtype != dtype or not t.is_cuda:
-            raise ValueError(f"{name} must be a {dtype} device tensor")
+        if t.dtype != dtype or t.get_device() != self.device:
+            raise ValueError(f"{name} must be a {dtype} tensor on the handle's device {self.device}")
         return t.data_ptr()
 
 
 class MlpNorm(_Layer):
-    """Layer norm over rows of H elements.  Outputs are the caller's tensors;
-    work is enqueued on the current stream of x's device (or `stream`).  With
+    """Layer norm over rows of H elements, on the device that is current when it
+    is made.  Outputs are the caller's tensors; work is enqueued on the current
+    stream of that device (or `stream`).  With
     grad=False the handle holds no workspace and only runs forward."""
 
     def __init__(self, H: int, dtype: str = "f16", eps: float = 1e-5, grad: bool = True):
         self.H, self.eps = int(H), float(eps)
         self._set_type(dtype)
-        self.h = mlp_norm_create(H, DTYPES[dtype], eps, grad)
+        self._hold(mlp_norm_create(H, DTYPES[dtype], eps, grad))
 
     _destroy = staticmethod(mlp_norm_destroy)
 
@@ -210,7 +216,7 @@ class MlpLinear(_Layer):
         self.rows, self.K, self.N, self.act = int(rows), int(K), int(N), act
         self.gN = self.N * (2 if act == "swiglu" else 1)
         self._set_type(dtype)
-        self.h = mlp_linear_create(rows, K, N, ACTS[act], DTYPES[dtype], grad)
+        self._hold(mlp_linear_create(rows, K, N, ACTS[act], DTYPES[dtype], grad))
 
     _destroy = staticmethod(mlp_linear_destroy)
 
