@@ -4,6 +4,7 @@ text summaries.
 
     python rocprof_harness.py [--workload 1] [--M 2048] [--policy tile_sync]
                               [--raw-dir gpurun_out/prof] [--summary-dir profiles]
+    python rocprof_harness.py --block      # the block operators instead: the cases of perf/operators.py
 
 Each measurement is its own profiler run of `bench.py --kernels-only` (the
 headline policy's persistent kernel and the planned stream-ordered pair,
@@ -20,6 +21,10 @@ bench.py reports it as the roofline's `traffic` only while both still hold.
 Matrix-core utilisation and HBM bytes per second follow from the counters and
 the profiled durations; at small M (weight streaming) the GB/s figure is the
 one that matters, at large M the matrix-core one.
+
+With --block the profiled program is this file with --block-cases, which runs
+every listed case of perf/operators.py through the package; one table of all
+of these measurements goes to <summary-dir>/block_kernels.md.
 
 The harness itself never touches the GPU: it only starts the profiler runs
 as child processes and parses their CSV output.
@@ -93,14 +98,132 @@ def _chain_rows(disp):
     return g
 
 
+BLOCK_PASSES = 21     # per case, over three sets of inputs in turn
+
+
+def block_operators():
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    return ops
+
+
+def run_block_cases():
+    """The profiled program: the passes of each case one after another; inputs
+    are made between the cases, by kernels that are not the package's."""
+    import torch
+    ops = block_operators()
+    for case in ops.listed():
+        states = [ops.prepare(case, seed) for seed in range(3)]
+        torch.cuda.synchronize()
+        for k in range(BLOCK_PASSES):
+            ops.run(states[k % 3])
+        torch.cuda.synchronize()
+        print(case["name"], flush=True)
+
+
+def block_short_name(k):
+    """`linear<16, 128, 1, 2, 4, 64, 1, 0, 0>` from the demangled name."""
+    k = k.split("mlpc::", 1)[1].split("(")[0].replace("mlpc::", "").replace("LinCfg<", "")
+    for a, b in ((">, ", ", "), ("_kernel<", "<"), ("true", "1"), ("false", "0")):
+        k = k.replace(a, b)
+    return k
+
+
+def _by_case(dispatches):
+    """The package's dispatches, (kernel, workgroups, ...) in order, grouped by (case, kernel, workgroups): a case ends
+    where another kernel follows the package's."""
+    groups, case, ours = collections.OrderedDict(), -1, False
+    for d in dispatches:
+        own = "mlpc::" in d[0]
+        case += own and not ours
+        ours = own
+        if own:
+            groups.setdefault((case, block_short_name(d[0]), d[1]), []).append(d[2:])
+    return groups
+
+
+def profile_block(args):
+    raw = os.path.join(args.raw_dir, "block")
+    os.makedirs(raw, exist_ok=True)
+    os.makedirs(args.summary_dir, exist_ok=True)
+    py = sys.executable or "python3"
+    copy = [py, "bench.py", "--copy-mib", str(COPY_MIB)]
+    cases = [py, "rocprof_harness.py", "--block-cases"]
+    mfma = ["SQ_VALU_MFMA_BUSY_CYCLES", "SQ_BUSY_CU_CYCLES", "GRBM_GUI_ACTIVE", "SQ_LDS_BANK_CONFLICT"]
+    runs = {"kt": (["--kernel-trace"], cases), "mfma": (["--pmc", *mfma], cases), "fetch": (["--pmc", "FETCH_SIZE"], cases),
+            "write": (["--pmc", "WRITE_SIZE"], cases), "cfetch": (["--pmc", "FETCH_SIZE"], copy),
+            "cwrite": (["--pmc", "WRITE_SIZE"], copy)}
+    for name, (extra, program) in runs.items():
+        cmd = ["rocprofv3", "--output-format", "csv", "-d", os.path.join(raw, name), "-o", name, *extra, "--", *program]
+        rc = _run(cmd, os.path.join(raw, name + ".log"), 300)
+        if rc != 0:
+            raise SystemExit(f"profiler run {name} ended with status {rc}; see {raw}/{name}.log")
+
+    def size(r, what):
+        return int(r[f"{what}_X"]) * int(r[f"{what}_Y"]) * int(r[f"{what}_Z"])
+    trace = sorted(csv.DictReader(open(_find(raw, "kt", "kernel_trace.csv"))), key=lambda r: int(r["Start_Timestamp"]))
+    times = _by_case((r["Kernel_Name"], size(r, "Grid_Size") // size(r, "Workgroup_Size"),
+                      (int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3) for r in trace)
+    count = {n: [d for _, d in sorted(_counters(_find(raw, n, "counter_collection.csv")).items())] for n in runs if n != "kt"}
+    factor = {}
+    for n, counter in (("cfetch", "FETCH_SIZE"), ("cwrite", "WRITE_SIZE")):
+        factor[counter] = COPY_MIB * 1024 / statistics.mean(d[3][counter] for d in count[n] if "copyBuffer" in d[0])
+    mf, fetch, write = (_by_case(count[n]) for n in ("mfma", "fetch", "write"))
+    names = [c["name"] for c in block_operators().listed()]
+    rows = []
+    for key, ts in times.items():
+        us = statistics.median(t for t, in ts)
+        cyc = statistics.median(c["GRBM_GUI_ACTIVE"] / XCDS for _, c in mf[key])
+        of = lambda counter: statistics.median(c[counter] for _, c in mf[key])  # noqa: E731
+        ghz = cyc / statistics.median(t for t, _ in mf[key]) / 1e3
+        busy, cu = of("SQ_VALU_MFMA_BUSY_CYCLES") / (SIMDS * cyc), of("SQ_BUSY_CU_CYCLES") / (CUS * cyc)
+        mb = [statistics.median(c[k] for _, c in g[key]) * factor[k] * 1024 / 1e6
+              for g, k in ((fetch, "FETCH_SIZE"), (write, "WRITE_SIZE"))]
+        rows.append(f"| {names[key[0]]} | {key[1]} | {key[2]} | {us:.1f} | {f'{busy:.2f}' if busy >= 0.005 else '-'} | {cu:.2f} | "
+                    f"{f'{ghz:.2f}' if us > 100 else '-'} | {of('SQ_LDS_BANK_CONFLICT') / of('SQ_BUSY_CU_CYCLES'):.3f} | "
+                    f"{mb[0]:.1f} | {mb[1]:.1f} | {sum(mb) / us:.2f} |")
+    with open(os.path.join(args.summary_dir, "block_kernels.md"), "w") as fh:
+        fh.write(f"""# Block operators: kernels of the listed cases, one MI355X
+
+    python rocprof_harness.py --block
+      -> rocprofv3 --kernel-trace -- rocprof_harness.py --block-cases
+      -> rocprofv3 --pmc {' '.join(mfma)} -- rocprof_harness.py --block-cases
+      -> rocprofv3 --pmc FETCH_SIZE (then WRITE_SIZE) -- rocprof_harness.py --block-cases
+      -> rocprofv3 --pmc FETCH_SIZE (then WRITE_SIZE) -- bench.py --copy-mib {COPY_MIB}
+
+Every listed case of perf/operators.py, {BLOCK_PASSES} passes over three sets of inputs in turn; medians per (case, kernel,
+workgroups). The profiled runs of the large products are up to 15% slower than unprofiled ones (the clock).
+
+cycles = GRBM_GUI_ACTIVE / {XCDS}, GHz = cycles / duration (kernels of more than 100 us), MFMA busy =
+SQ_VALU_MFMA_BUSY_CYCLES / ({SIMDS} SIMDs x cycles), CU busy = SQ_BUSY_CU_CYCLES / ({CUS} x cycles). MB read and written =
+FETCH_SIZE x {factor['FETCH_SIZE']:.3f} and WRITE_SIZE x {factor['WRITE_SIZE']:.3f} (calibrated on the copy), across the L2 boundary, the Infinity Cache included.
+`linear<BM, BN, waves M, waves N, stages, stage depth, waves per SIMD, type (0 fp16, 1 bf16), pass (0 x W, 1 dz W^T,
+2 x^T dz)>`; `linear_both<...>`: dz W^T and x^T dz in one launch; `norm_forward<type, threads per row, chunks, ragged>`,
+`norm_backward<type, threads, chunks, ragged, single workgroup>`; `dz<type, activation, columns>`.
+
+| case | kernel | workgroups | us | MFMA busy | CU busy | GHz | LDS conflict cycles / CU busy | MB read | MB written | TB/s |
+|---|---|---|---|---|---|---|---|---|---|---|
+""" + "\n".join(rows) + "\n")
+    print(f"summary written to {args.summary_dir}/block_kernels.md", flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
+    ap.add_argument("--block", action="store_true")
+    ap.add_argument("--block-cases", action="store_true", help="the program that --block profiles")
     ap.add_argument("--workload", type=int, default=1)
     ap.add_argument("--M", type=int, default=2048)
     ap.add_argument("--policy", default="tile_sync")
     ap.add_argument("--raw-dir", default=os.path.join("gpurun_out", "prof"))
     ap.add_argument("--summary-dir", default="profiles")
     args = ap.parse_args()
+    if args.block_cases:
+        return run_block_cases()
+    if args.block:
+        return profile_block(args)
 
     from consumer_gemm_chain_amd import gen
     import bench
