@@ -20,13 +20,14 @@
 //     (K % 64 != 0) takes its out-of-range chunks from a zero page.
 //
 // What bounds it: with 500 rows and more the chip's power (the matrix cores
-// 52-59% busy at 1.8-2.1 GHz on random fp16 operands, no LDS bank conflict):
-// 2048 x 12288 x 6144 fp16 takes 272-282 us for x W, 265-275 for dz W^T, 270
-// for x^T dz (1.10-1.17 PFLOP/s), 8192 x 4096 x 4096 224 us (1.22).  Single
-// tokens stream W at 5.4 TB/s (1 x 12288 x 6144: 27.9 us in the kernel).  In
-// between, rows padded to the tile, the partials of split tiles and the
-// memory's latency under two or three stages in flight share the loss: 300 x
-// 8192 x 5504 takes 45-48 us for 27 GFLOP and 95 MB of operands.
+// 50-60% busy at 1.8-2.1 GHz on random operands, no LDS bank conflict): a call
+// of 2048 x 12288 x 6144 fp16 with the planned tiles took 272-290 us for x W,
+// 265-285 for dz W^T and 270-277 for x^T dz on three cards (1.07-1.17 PFLOP/s),
+// 8192 x 4096 x 4096 224-235 us (1.17-1.22).  Single tokens stream W at 5.4
+// TB/s (1 x 12288 x 6144: 27.8 us in the kernel).  In between, rows padded to
+// the tile, the partials of split tiles and the memory's latency under two or
+// three stages in flight share the loss: 300 x 8192 x 5504 takes 45-48 us in
+// the kernel for 27 GFLOP and 95 MB of operands.
 #pragma once
 
 #include "block_launch.h"
@@ -72,8 +73,10 @@ __device__ __forceinline__ int kr_chunk(int k, int c) {
 // four chunks, so rows r, r + 4, r + 8, r + 12 share banks: the XOR gives them
 // 0, 2, 3, 1, which keeps them apart whether they are read at one chunk or, as
 // the 16 lanes that ds_read_b128 serves together take them, two of them at a
-// chunk and the other two at its neighbour (conflict cycles 0.18-0.27 of the
-// busy ones with 0, 1, 2, 3, none with these; 2048 x 12288 x 6144 309 -> 308 us).
+// chunk and the other two at its neighbour.  With the chain's a_chunk32, which
+// gives those rows 0, 1, 2, 3, conflicts take 0.17 (x W) and 0.26 (dz W^T) of
+// the busy cycles on 256 x 256 tiles, with these none; the times, which power
+// bounds, are the same (2048 x 12288 x 6144: x W 280 us, dz W^T 316 either way).
 template <int KS>
 __device__ __forceinline__ int kc_chunk(int r, int c) {
     if constexpr (KS == 64) return a_chunk(r, c);

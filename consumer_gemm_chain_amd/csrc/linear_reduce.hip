@@ -14,7 +14,7 @@ constexpr int RNT = 64;     // small workgroups spread evenly over the CUs
 // counters and no agent-scope fences, and the whole chip reads the partials
 // (x W, both kernels: 128 rows 12288 x 6144 54 -> 46 us, 300 rows 98 -> 78, one
 // row 37.7 -> 32.4 against the last part of each tile adding the others').
-// Bound by latency: 4.6 us for one row, 6.5 us for 20 MB of partials.
+// Bound by latency: 4.8 us for one row, 6.4 us for 20 MB of partials.
 template <int DT>
 __global__ __launch_bounds__(RNT) void linear_reduce_kernel(GemmArgs p, int per_tile) {
     const uint32_t tile = blockIdx.x / per_tile;

@@ -190,8 +190,8 @@ constexpr int MAX_PARTS = 256;      // workgroups that keep column sums: one per
 // and g xhat; xhat itself is kept, for with (x - mean) and a factor of rstd^2
 // rows with an rstd past 1.8e19 would overflow.  Bound by memory, the partials included: with
 // dres, 8192 x 8192 bf16 102 us, 5.3 TB/s of the operands; 2048 x 12288 f16
-// 44 us for 201 MB of operands and 25 MB of partials, 5.1 TB/s; 1000 x 8192
-// 17 us (four rows per workgroup, whose loads are a chain).
+// 44.6 us for 201 MB of operands and 25 MB of partials, 5.1 TB/s; 1000 x 8192
+// 16.6 us (four rows per workgroup, whose loads are a chain).
 template <int DT, int NT, int V, bool RAGGED, bool ALONE>
 __global__ __launch_bounds__(NT) void norm_backward_kernel(NormArgs a, int TR) {
     __shared__ float s[2][NT / 64][2];
@@ -393,6 +393,10 @@ __global__ __launch_bounds__(1024) void norm_cols_sum_kernel(NormArgs a) {
 
 // ------------------------------- rows of fewer than 8 or more than 16384
 
+// Right for every size, not fast: bound by the latency of 2-byte accesses.  Whole
+// calls, forward and gradient, f16: 2048 x 20000 145 and 240 us (floors 32 and 63),
+// 256 x 40000 147 and 248 (8 and 16), 8192 x 4 8.5 and 22.
+
 constexpr int LONG_ROW = 16384;
 static bool held(int H) { return H >= 8 && H <= LONG_ROW; }
 constexpr int SWEEP_NT = 256;
@@ -514,7 +518,9 @@ static hipError_t forward_t(const NormArgs& a, int cus, hipStream_t s) {
 // The register-held backward's workgroup, threads per row and chunks per
 // thread: one chunk each from a wave per row up to 1024 threads, then two; 768
 // threads while they hold the row, whose larger register budget keeps every
-// fp32 value of a row (2048 x 12288 with dres: 53 us, with 1024 threads 73).
+// fp32 value of a row (whole calls with dres: 2048 x 12288 50.4 us, with 1024
+// threads 72; 2048 x 9216 40.1 and 59.9).  Two chunks in 1024 threads spill up
+// to 12 registers (2048 x 16384 90 us).
 struct BackwardShape {
     int nt, tr, v;
 };
