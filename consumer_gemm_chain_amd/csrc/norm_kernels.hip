@@ -395,7 +395,7 @@ __global__ __launch_bounds__(1024) void norm_cols_sum_kernel(NormArgs a) {
 
 // Right for every size, not fast: bound by the latency of 2-byte accesses.  Whole
 // calls, forward and gradient, f16: 2048 x 20000 145 and 240 us (floors 32 and 63),
-// 256 x 40000 147 and 248 (8 and 16), 8192 x 4 8.5 and 22.
+// 256 x 40000 146 and 249 (8 and 16), 8192 x 4 8.8 and 23.
 
 constexpr int LONG_ROW = 16384;
 static bool held(int H) { return H >= 8 && H <= LONG_ROW; }
@@ -410,6 +410,30 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+struct Two {
+    float a, b;
+};
+
+// Sums of both values of f over first, first + step, .. below end, in chains of
+// 64 additions: with one chain of 16384 over a row of 2^22, whose mean is 1000
+// times its spread, rstd is off by 3e-5.
+template <class I, class F>
+__device__ __forceinline__ Two chained_sum(I first, I end, int step, F f) {
+    Two t = {0.f, 0.f};
+    for (I b = first; b < end; b += 64 * step) {
+        Two u = {0.f, 0.f};
+        const I stop = min(b + 64 * step, end);
+        for (I i = b; i < stop; i += step) {
+            const Two v = f(i);
+            u.a += v.a;
+            u.b += v.b;
+        }
+        t.a += u.a;
+        t.b += u.b;
+    }
+    return t;
+}
+
 // At most this many workgroups, which then walk the rows: a launch of one per
 // row would pass HIP's limit of 2^32 threads at 2^24 rows.
 constexpr int64_t SWEEP_GRID = 1 << 16;
@@ -421,15 +445,13 @@ __global__ __launch_bounds__(SWEEP_NT) void norm_forward_sweep_kernel(NormArgs a
     __shared__ float s[SWEEP_NT / 64];
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const uint16_t* x = a.x + r * a.ldx;
-        float t = 0.f;
-        for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) t += widen<DT>(x[c]);
-        const float mean = block_sum(t, s) / a.H;
-        t = 0.f;
-        for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
+        const Two sum = chained_sum((int)threadIdx.x, a.H, SWEEP_NT, [&](int c) { return Two{widen<DT>(x[c]), 0.f}; });
+        const float mean = block_sum(sum.a, s) / a.H;
+        const Two var = chained_sum((int)threadIdx.x, a.H, SWEEP_NT, [&](int c) {
             const float d = widen<DT>(x[c]) - mean;
-            t += d * d;
-        }
-        const float rstd = 1.0f / sqrtf(block_sum(t, s) / a.H + a.eps);
+            return Two{d * d, 0.f};
+        });
+        const float rstd = 1.0f / sqrtf(block_sum(var.a, s) / a.H + a.eps);
         for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
             float v = (widen<DT>(x[c]) - mean) * rstd;
             if (a.weight) v *= widen<DT>(a.weight[c]);
@@ -451,13 +473,11 @@ __global__ __launch_bounds__(SWEEP_NT) void norm_dx_sweep_kernel(NormArgs a) {
         const uint16_t* x = a.x + r * a.ldx;
         const uint16_t* dy = a.dy + r * a.lddy;
         const float mean = a.mean[r], rstd = a.rstd[r];
-        float t0 = 0.f, t1 = 0.f;
-        for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
+        const Two sum = chained_sum((int)threadIdx.x, a.H, SWEEP_NT, [&](int c) {
             const float g = widen<DT>(dy[c]) * (a.weight ? widen<DT>(a.weight[c]) : 1.f);
-            t0 += g;
-            t1 += g * ((widen<DT>(x[c]) - mean) * rstd);
-        }
-        const float m0 = block_sum(t0, s) / a.H, m1 = block_sum(t1, s) / a.H;
+            return Two{g, g * ((widen<DT>(x[c]) - mean) * rstd)};
+        });
+        const float m0 = block_sum(sum.a, s) / a.H, m1 = block_sum(sum.b, s) / a.H;
         for (int c = threadIdx.x; c < a.H; c += SWEEP_NT) {
             const float g = widen<DT>(dy[c]) * (a.weight ? widen<DT>(a.weight[c]) : 1.f);
             float v = rstd * (g - m0 - (widen<DT>(x[c]) - mean) * rstd * m1);
@@ -474,15 +494,13 @@ __global__ __launch_bounds__(SWEEP_NT) void norm_cols_sweep_kernel(NormArgs a) {
     const int c = blockIdx.x * SWEEP_NT + threadIdx.x;
     if (c >= a.H) return;
     const int64_t r0 = a.rows * blockIdx.y / a.parts, r1 = a.rows * (blockIdx.y + 1) / a.parts;
-    float tw = 0.f, tb = 0.f;
-    for (int64_t r = r0; r < r1; ++r) {
+    const Two sum = chained_sum(r0, r1, 1, [&](int64_t r) {
         const float dy = widen<DT>(a.dy[r * a.lddy + c]);
-        tw += dy * ((widen<DT>(a.x[r * a.ldx + c]) - a.mean[r]) * a.rstd[r]);
-        tb += dy;
-    }
+        return Two{dy * ((widen<DT>(a.x[r * a.ldx + c]) - a.mean[r]) * a.rstd[r]), dy};
+    });
     float* p = a.part + (size_t)blockIdx.y * 2 * a.H + c;
-    p[0] = tw;
-    p[a.H] = tb;
+    p[0] = sum.a;
+    p[a.H] = sum.b;
 }
 
 // ---------------------------------------------------------------------- host
