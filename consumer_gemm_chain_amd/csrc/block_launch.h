@@ -77,8 +77,8 @@ struct Param {
     using type = T;
 };
 
-// Launch `kernel` and return the launch's own status (hipGetLastError would
-// also report what an earlier call of the thread, not ours perhaps, left).
+// Launch `kernel` and return the launch's own status: hipGetLastError would
+// also report an error that an earlier call of the thread, ours or not, left.
 template <class... P>
 hipError_t launch(void (*kernel)(P...), dim3 grid, int threads, hipStream_t s, typename Param<P>::type... args) {
     void* p[] = {&args...};

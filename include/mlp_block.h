@@ -36,7 +36,7 @@
  * infinite, and a row whose sum of (x - mean)^2 passes 3.4e38 (bf16) gets an
  * rstd of 0.
  *
- * Row counts: any R >= 0 per call, up to the handle's limit.  With R = 0
+ * Row counts: any R >= 0 per call, up to 2^24 and a linear handle's limit.  With R = 0
  * nothing is read and operands of R rows may be NULL; the forward passes
  * write nothing, the gradients of weights and biases are zero.
  *
