@@ -80,6 +80,10 @@ struct DeviceGuard {
 
 constexpr int64_t MAX_WIDTH = (int64_t)1 << 22;
 constexpr int64_t MAX_ROWS = (int64_t)1 << 24;
+// The norm's offsets are 64-bit throughout (2^24 rows of this stride stay in
+// range); the linear layer's DMA has 32-bit offsets within a tile of 256 rows.
+constexpr int64_t MAX_NORM_LD = (int64_t)1 << 36;
+constexpr int64_t MAX_LINEAR_LD = (int64_t)1 << 23;
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -88,18 +92,18 @@ bool misaligned(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) != 
 // A 2-d operand of the norm: rows of H elements `ld` apart.
 int check_rows(const char* name, const void* p, int64_t ld, int64_t H) {
     if (!p || misaligned(p, 2)) return fail(MLP_EINVAL, "%s must be a non-NULL 2-byte aligned device pointer", name);
-    if (ld < H || ld > MAX_WIDTH * 4)
+    if (ld < H || ld > MAX_NORM_LD)
         return fail(MLP_EINVAL, "the row stride of %s must be in %lld..%lld elements, got %lld", name, (long long)H,
-                    (long long)(MAX_WIDTH * 4), (long long)ld);
+                    (long long)MAX_NORM_LD, (long long)ld);
     return MLP_OK;
 }
 
 // A 2-d operand of the linear layer: 16-byte rows of `width` elements.
 int check_matrix(const char* name, const void* p, int64_t ld, int64_t width) {
     if (!p || misaligned(p, 16)) return fail(MLP_EINVAL, "%s must be a non-NULL 16-byte aligned device pointer", name);
-    if (ld < width || ld % 8 || ld > MAX_WIDTH * 2)
+    if (ld < width || ld % 8 || ld > MAX_LINEAR_LD)
         return fail(MLP_EINVAL, "the row stride of %s must be a multiple of 8 in %lld..%lld elements, got %lld", name,
-                    (long long)width, (long long)(MAX_WIDTH * 2), (long long)ld);
+                    (long long)width, (long long)MAX_LINEAR_LD, (long long)ld);
     return MLP_OK;
 }
 
