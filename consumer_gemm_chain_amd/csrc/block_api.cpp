@@ -80,10 +80,18 @@ struct DeviceGuard {
 
 constexpr int64_t MAX_WIDTH = (int64_t)1 << 22;
 constexpr int64_t MAX_ROWS = (int64_t)1 << 24;
-// The norm's offsets are 64-bit throughout (2^24 rows of this stride stay in
-// range); the linear layer's DMA has 32-bit offsets within a tile of 256 rows.
-constexpr int64_t MAX_NORM_LD = (int64_t)1 << 36;
-constexpr int64_t MAX_LINEAR_LD = (int64_t)1 << 23;
+// Row strides: offsets are 64-bit (2^24 rows of MAX_LD stay in range), but for
+// the products' operands, whose DMA has 32-bit byte offsets within a tile: of up
+// to 256 rows, or of 64 rows and all columns (at most 2^23) where the reduction
+// runs across rows.
+constexpr int64_t MAX_LD = (int64_t)1 << 36;
+constexpr int64_t MAX_DMA_LD = (int64_t)1 << 23;
+
+// The largest stride of a product's operand of `rows` rows.
+int64_t dma_ld(int64_t rows) {
+    const int64_t few = (((int64_t)1 << 31) - ((int64_t)1 << 24)) / (rows < 256 ? rows : 256);
+    return few > MAX_DMA_LD ? few : MAX_DMA_LD;
+}
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -92,18 +100,18 @@ bool misaligned(const void* p, unsigned a) { return ((uintptr_t)p & (a - 1)) != 
 // A 2-d operand of the norm: rows of H elements `ld` apart.
 int check_rows(const char* name, const void* p, int64_t ld, int64_t H) {
     if (!p || misaligned(p, 2)) return fail(MLP_EINVAL, "%s must be a non-NULL 2-byte aligned device pointer", name);
-    if (ld < H || ld > MAX_NORM_LD)
+    if (ld < H || ld > MAX_LD)
         return fail(MLP_EINVAL, "the row stride of %s must be in %lld..%lld elements, got %lld", name, (long long)H,
-                    (long long)MAX_NORM_LD, (long long)ld);
+                    (long long)MAX_LD, (long long)ld);
     return MLP_OK;
 }
 
-// A 2-d operand of the linear layer: 16-byte rows of `width` elements.
-int check_matrix(const char* name, const void* p, int64_t ld, int64_t width) {
+// A 2-d operand of the linear layer: 16-byte rows of `width` elements, at most `most` apart.
+int check_matrix(const char* name, const void* p, int64_t ld, int64_t width, int64_t most) {
     if (!p || misaligned(p, 16)) return fail(MLP_EINVAL, "%s must be a non-NULL 16-byte aligned device pointer", name);
-    if (ld < width || ld % 8 || ld > MAX_LINEAR_LD)
+    if (ld < width || ld % 8 || ld > most)
         return fail(MLP_EINVAL, "the row stride of %s must be a multiple of 8 in %lld..%lld elements, got %lld", name,
-                    (long long)width, (long long)MAX_LINEAR_LD, (long long)ld);
+                    (long long)width, (long long)most, (long long)ld);
     return MLP_OK;
 }
 
@@ -617,11 +625,11 @@ int mlp_linear_forward(mlp_linear_t h, int64_t rows, const void* x, int64_t ldx,
     if (!h) return fail(MLP_EINVAL, "NULL handle");
     int rc = check_rows_count(rows, h->max_rows);
     if (rc != MLP_OK || rows == 0) return rc;
-    rc = check_matrix("x", x, ldx, h->K);
-    if (rc == MLP_OK) rc = check_matrix("w", w, ldw, h->gN);
-    if (rc == MLP_OK) rc = check_matrix("y", y, ldy, h->N);
-    if (rc == MLP_OK && residual) rc = check_matrix("residual", residual, ldres, h->N);
-    if (rc == MLP_OK && z) rc = check_matrix("z", z, ldz, h->gN);
+    rc = check_matrix("x", x, ldx, h->K, dma_ld(rows));
+    if (rc == MLP_OK) rc = check_matrix("w", w, ldw, h->gN, MAX_DMA_LD);
+    if (rc == MLP_OK) rc = check_matrix("y", y, ldy, h->N, MAX_LD);
+    if (rc == MLP_OK && residual) rc = check_matrix("residual", residual, ldres, h->N, MAX_LD);
+    if (rc == MLP_OK && z) rc = check_matrix("z", z, ldz, h->gN, MAX_LD);
     if (rc != MLP_OK) return rc;
     if (misaligned(bias, 16)) return fail(MLP_EINVAL, "bias must be 16-byte aligned");
     if (residual == y && ldres != ldy) return fail(MLP_EINVAL, "y in the residual's buffer needs its row stride");
@@ -657,12 +665,13 @@ int mlp_linear_backward(mlp_linear_t h, int64_t rows, const void* dy, int64_t ld
     const bool act = h->act != MLP_ACT_NONE;
     int rc = check_rows_count(rows, h->max_rows);
     const bool any = rc == MLP_OK && rows > 0;
-    if (any) rc = check_matrix("dy", dy, lddy, h->N);
-    if (any && rc == MLP_OK && act) rc = check_matrix("z", z, ldz, h->gN);
-    if (any && rc == MLP_OK && dx) rc = check_matrix("dx", dx, lddx, h->K);
-    if (any && rc == MLP_OK && dx) rc = check_matrix("w", w, ldw, h->gN);
-    if (any && rc == MLP_OK && dw) rc = check_matrix("x", x, ldx, h->K);
-    if (rc == MLP_OK && dw) rc = check_matrix("dw", dw, lddw, h->gN);
+    // (without an activation dy is dz, an operand of the products)
+    if (any) rc = check_matrix("dy", dy, lddy, h->N, act ? MAX_LD : dma_ld(rows));
+    if (any && rc == MLP_OK && act) rc = check_matrix("z", z, ldz, h->gN, MAX_LD);
+    if (any && rc == MLP_OK && dx) rc = check_matrix("dx", dx, lddx, h->K, MAX_LD);
+    if (any && rc == MLP_OK && dx) rc = check_matrix("w", w, ldw, h->gN, MAX_DMA_LD);
+    if (any && rc == MLP_OK && dw) rc = check_matrix("x", x, ldx, h->K, dma_ld(rows));
+    if (rc == MLP_OK && dw) rc = check_matrix("dw", dw, lddw, h->gN, MAX_LD);
     if (rc != MLP_OK) return rc;
     if (misaligned(db, 16)) return fail(MLP_EINVAL, "db must be 16-byte aligned");
     DeviceGuard g(h->device);

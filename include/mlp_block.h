@@ -42,9 +42,11 @@
  *
  * Pointers are DEVICE pointers owned by the caller.  In the linear layer
  * they are 16-byte aligned, K and N are multiples of 8 and so are the row
- * strides (16-byte rows), which are at most 2^23.  The norm takes any H >= 1,
- * any row stride from H to 2^36 and 2-byte aligned rows; 16-byte aligned rows
- * with H a multiple of 8 run fastest.  y may be the residual's own buffer and a norm's dx may be dres's
+ * strides (16-byte rows).  These are at most 2^36, but W's at most 2^23, and
+ * x's, and dy's without an activation, at most the larger of 2^23 and
+ * (2^31 - 2^24) / rows.  The norm takes any H >= 1, any row stride from H to
+ * 2^36 and 2-byte aligned rows; 16-byte aligned rows with H a multiple of 8
+ * run fastest.  y may be the residual's own buffer and a norm's dx may be dres's
  * (same row stride); no other outputs may overlap an operand.
  *
  * Streams, handles, errors: as in mlp_chain.h.  Every entry point but create

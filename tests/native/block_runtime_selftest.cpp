@@ -148,7 +148,34 @@ static void destroy_waits_for_the_workspace() {
     CHECK(waited.size() == 1 && waited[0] == other);
 }
 
+// The strides a linear layer takes: an operand's DMA offsets, which are 32-bit
+// (rows of a tile for x W and dz W^T; 64 rows and the columns for x^T dz), hold
+// for every stride that is not refused.
+static void strides() {
+    const int64_t rows[] = {1, 2, 7, 40, 63, 64, 65, 200, 255, 256, 257, 5000};
+    for (int64_t r : rows) {
+        mlp_linear_t l = mlp_linear_create(r, 64, 64, 0, 0, 1);
+        auto x = [&](int64_t ld) { return mlp_linear_forward(l, r, buf, ld, buf, 64, nullptr, nullptr, 0, buf, 64, nullptr, 0, nullptr); };
+        auto dy = [&](int64_t ld) { return mlp_linear_backward(l, r, buf, ld, buf, 64, buf, 64, nullptr, 0, buf, 64, buf, 64, nullptr, nullptr); };
+        auto dwx = [&](int64_t ld) { return mlp_linear_backward(l, r, buf, 64, buf, ld, buf, 64, nullptr, 0, nullptr, 0, buf, 64, nullptr, nullptr); };
+        CHECK(x((int64_t)1 << 23) == MLP_OK && dy((int64_t)1 << 23) == MLP_OK && dwx((int64_t)1 << 23) == MLP_OK);
+        int64_t most = 8;       // by bisection
+        for (int64_t step = (int64_t)1 << 40; step >= 8; step /= 2)
+            if (x(most + step) == MLP_OK) most += step;
+        CHECK(dy(most) == MLP_OK && dwx(most) == MLP_OK && dy(most + 8) == MLP_EINVAL && dwx(most + 8) == MLP_EINVAL);
+        const int64_t tile = r < 256 ? r : 256, deep = r < 64 ? r : 64, columns = (int64_t)1 << 23;
+        CHECK(((tile - 1) * most + 64) * 2 < (int64_t)1 << 32 && ((deep - 1) * most + columns) * 2 <= (int64_t)1 << 32);
+        // the other operands' offsets are 64-bit, W's stride is limited alone
+        const int64_t far = (int64_t)1 << 36;
+        CHECK(mlp_linear_forward(l, r, buf, 64, buf, 64, nullptr, buf, far, buf + 8, far, buf, far, nullptr) == MLP_OK);
+        CHECK(mlp_linear_forward(l, r, buf, 64, buf, (1 << 23) + 8, nullptr, nullptr, 0, buf, 64, nullptr, 0, nullptr) == MLP_EINVAL);
+        CHECK(mlp_linear_forward(l, r, buf, 64, buf, 64, nullptr, nullptr, 0, buf, far + 8, nullptr, 0, nullptr) == MLP_EINVAL);
+        CHECK(mlp_linear_destroy(l) == MLP_OK);
+    }
+}
+
 int main() {
+    strides();
     errors_are_reported_once();
     destroy_waits_for_the_workspace();
     CHECK(blocks == 0);

@@ -6,9 +6,10 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from consumer_gemm_chain_amd import MlpNorm  # noqa: E402
+from consumer_gemm_chain_amd import MlpChainError, MlpLinear, MlpNorm  # noqa: E402
+from consumer_gemm_chain_amd import mlp_block as mb  # noqa: E402
 from tests.test_block_gpu import (EPS, check_linear_backward, check_linear_forward, check_norm_backward,  # noqa: E402
-                                  check_norm_forward, norm_case, norm_ref)
+                                  check_norm_forward, linear_case, norm_case, norm_ref)
 
 MOST = 1 << 24
 
@@ -50,3 +51,31 @@ def test_norm_of_one_token_of_each_long_sequence(H):
             layer.backward(place(3, dy), place(2, x), w, mean.float(), rstd.float(), dx, dw, db, dres=place(4, dres))
             outs.append((y, dx, dw, db))
     assert all(torch.equal(p, q) for p, q in zip(*outs)) and bool(outs[0][0].isfinite().all())
+
+
+@pytest.mark.parametrize("act", ["none", "gelu_tanh", "swiglu"])
+@pytest.mark.parametrize("rows", [1, 20, 70])
+def test_linear_layer_of_one_token_of_each_long_sequence(rows, act):
+    """Every operand but the weights in rows further apart than 2^23 elements; strides that 32-bit offsets within a
+    tile would not reach are refused."""
+    K, N = 328, 264
+    ld = (1 << 24) + 24
+    c = linear_case(rows, K, N, act, "f16", 5)
+    gN, w, bias = c["gN"], c["w"], c["bias"]
+    base = torch.empty(rows * ld, dtype=torch.float16, device="cuda").view(rows, ld)
+    at = lambda k, n: base[:, k * 4096:k * 4096 + n]  # noqa: E731
+    z = c["z"] if act != "none" else None
+    outs = []
+    with MlpLinear(300, K, N, act, "f16") as layer:
+        for far in (False, True):
+            place = (lambda k, t: at(k, t.shape[1]).copy_(t)) if far else (lambda k, t: t.clone())
+            y, h, dx = (place(k, torch.zeros(rows, n, device="cuda").half()) for k, n in enumerate((N, gN, K)))
+            dw, db = torch.zeros_like(w), torch.zeros_like(bias)
+            layer.forward(place(3, c["x"]), w, y, bias=bias, residual=place(4, c["res"]), z=h)
+            layer.backward(place(5, c["dy"]), place(3, c["x"]), w, dx=dx, dw=dw, db=db, z=place(6, z) if z is not None else None)
+            outs.append((y, h, dx, dw, db))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(*outs)) and bool(outs[0][0].isfinite().all())
+        p = base.data_ptr()
+        with pytest.raises(MlpChainError, match="row stride of x"):
+            mb.mlp_linear_forward(layer.h, 300, p, ld, w.data_ptr(), gN, None, None, 0, p, N, None, 0, None)
