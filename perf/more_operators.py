@@ -263,7 +263,8 @@ def _run_plain(state):
         z_at = z.gather(1, at)[:, 0]
         top = z.max(1, keepdim=True)[0]
         lse = (z - top).exp().sum(1).log() + top[:, 0]
-        return {"loss": torch.where(target >= 0, lse - z_at, 0.0), "lse": lse}
+        # rows that are left out: zeros
+        return {"loss": torch.where(target >= 0, lse - z_at, 0.0), "lse": torch.where(target >= 0, lse, 0.0)}
     dloss, dt = torch.where(target >= 0, t["dloss"], 0.0), t["x"].dtype
     p = torch.exp(z - t["lse"][:, None])
     dlse = torch.where(target >= 0, t["dlse"], 0.0) if t["dlse"] is not None else torch.zeros_like(dloss)
@@ -389,7 +390,7 @@ def _exact_loss(case, seed):
     if case["op"] == "loss_fwd":
         lse = torch.logsumexp(z, 1)
         picked = z[torch.arange(len(target), device=z.device), target.clamp(min=0)]
-        return {"loss": (lse - picked) * counted, "lse": lse}
+        return {"loss": (lse - picked) * counted, "lse": lse * counted}
     # p from the lse that the gradient is given
     z = torch.exp_(z.sub_(t["lse"].double()[:, None]))
     a = t["dloss"].double() + (t["dlse"].double() if t["dlse"] is not None else 0.0)
@@ -402,9 +403,11 @@ def _exact_loss(case, seed):
 def work(case):
     if case["op"].startswith("loss"):
         R, H, V = case["rows"], case["H"], case["V"]
+        counted = max(1, round(R * (1 - case["ignored"])))      # rows that are left out need no products
         if case["op"] == "loss_fwd":
-            return {"bytes": 2 * H * (R + V) + 16 * R, "flops": 2 * R * H * V}
-        return {"bytes": 4 * H * (R + V) + (20 if case["zloss"] else 16) * R, "flops": 6 * R * H * V}
+            return {"bytes": 2 * H * (counted + V) + 16 * R, "flops": 2 * counted * H * V}
+        return {"bytes": 2 * H * (counted + V) + 2 * H * (R + V) + (20 if case["zloss"] else 16) * R,
+                "flops": 6 * counted * H * V}
     n = sum(math.prod(s) for s in _shapes(case))
     if case["op"] == "grad_norm":
         return {"bytes": 2 * n, "flops": 2 * n}
