@@ -5,8 +5,10 @@ The compute path is the HIP library ``lib/libmlp_chain.so`` (built from
 ``mlp_chain`` is its ctypes binding and ``gen`` the seeded input
 generator.  ``mlp_block`` binds the operators around the chain's products
 (layer norm, linear layer, the whole pre-norm block) declared in
-``include/mlp_block.h``.  Importing the package does not load the library; the first
-binding call does, and fails loudly if it has not been built.
+``include/mlp_block.h``, and ``mlp_train`` those of a training step (cross
+entropy, gradient norm, AdamW) declared in ``include/mlp_train.h``.  Importing
+the package does not load the library; the first binding call does, and fails
+loudly if it has not been built.
 """
 from .mlp_chain import (  # noqa: F401
     ACTS, DTYPES, POLICIES, MLP_OK, MLP_EINVAL, MLP_ENOMEM, MLP_EHIP, MLP_ETIMEOUT,
@@ -17,3 +19,4 @@ from .mlp_chain import (  # noqa: F401
     mlp_chain_debug_read_intermediate, mlp_chain_debug_set_split, mlp_chain_debug_set_trace,
 )
 from .mlp_block import MlpBlock, MlpLinear, MlpNorm  # noqa: F401
+from .mlp_train import MlpAdamW, MlpGradNorm, MlpLoss  # noqa: F401

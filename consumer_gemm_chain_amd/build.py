@@ -31,6 +31,9 @@ KERNELS = "chain_kernels.hip"     # compiled once per tile configuration
 BLOCK_SOURCES = ["block_api.cpp", "linear_dispatch.cpp", "linear_reduce.hip", "norm_kernels.hip",
                  "dz_kernels.hip"]
 LINEAR_KERNELS = "linear_kernels.hip"   # compiled once per configuration of linear_configs.h
+# loss and optimizer (include/mlp_train.h)
+TRAIN_SOURCES = ["train_api.cpp", "loss_dispatch.cpp", "loss_rows.hip", "optim_kernels.hip"]
+LOSS_KERNELS = "loss_kernels.hip"       # compiled once per configuration of linear_configs.h
 
 
 def num_configs(header: str = "chain_configs.h") -> int:
@@ -58,7 +61,7 @@ def _compile(job, verbose: bool) -> str:
     src, cfg, chaos = job
     tag = os.path.basename(src) + ("" if cfg is None else f".cfg{cfg}") + (".chaos" if chaos else "")
     obj = os.path.join(BUILD, tag + ".o")
-    macro = "MLPC_LIN" if src == LINEAR_KERNELS else "MLPC_CFG"
+    macro = {LINEAR_KERNELS: "MLPC_LIN", LOSS_KERNELS: "MLPC_LOSS"}.get(src, "MLPC_CFG")
     defs = ([] if cfg is None else [f"-D{macro}={cfg}"]) + (["-DMLPC_CHAOS=1"] if chaos else [])
     cmd = [hipcc(), "-x", "hip", *FLAGS, *defs, "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
@@ -85,6 +88,8 @@ def build(verbose: bool = False) -> str:
     api = [(src, None, False) for src in SOURCES]
     block = [(src, None, False) for src in BLOCK_SOURCES]
     block += [(LINEAR_KERNELS, c, False) for c in range(num_configs("linear_configs.h"))]
+    block += [(src, None, False) for src in TRAIN_SOURCES]
+    block += [(LOSS_KERNELS, c, False) for c in range(num_configs("linear_configs.h"))]
     jobs = kern + chaos + api + block
     workers = min(len(jobs), max(1, min(8, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:

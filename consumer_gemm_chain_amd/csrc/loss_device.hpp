@@ -1,0 +1,253 @@
+// loss_device.hpp -- the products of a vocabulary head's cross entropy on
+// gfx950, on the linear layer's tiles (linear_device.hpp): z = x W^T with a
+// softmax's maximum and sum, or its gradient dz, in the epilogue, and the
+// products dz W and dz^T x of a piece of dz.
+//
+//   z     x [n, H] and W [V, H] both have the reduction contiguous
+//   dx    dz [n, vn] contiguous, W [vn, H] across rows; fp32 sums over the
+//         pieces of the vocabulary (and parts of a piece) stay in the workspace
+//   dW    dz and x both across rows (the n packed rows); one output of V rows
+//
+// The number n of rows that count is known on the device alone: the grid is
+// for every row, and tiles past n end at once.
+#pragma once
+
+#include "linear_device.hpp"
+#include "train_launch.h"
+
+namespace mlpc {
+
+constexpr float LOG2E = 1.4426950408889634f;
+
+// Rows to reduce or multiply, as a scalar.
+__device__ __forceinline__ int packed_rows(const LossArgs& p) {
+    return p.info ? __builtin_amdgcn_readfirstlane(p.info->n) : (int)p.rows;
+}
+
+// x's packed rows: x itself if every row counts.
+__device__ __forceinline__ const uint16_t* packed_x(const LossArgs& p, int n, int64_t& ld) {
+    const bool all = n == (int)p.rows;
+    ld = all ? p.ldx : p.H;
+    return all ? p.x : p.packed;
+}
+
+// The reduction of a tile: stages k0 .. k1 of `slabs` whole slabs and the one
+// that ends past K, for the last part.
+template <class C, int DT, int PASS>
+__device__ __forceinline__ void loss_reduce(f32x4 (&acc)[C::FM][C::FN], const LinTile<C, PASS>& t, const GemmArgs& g, int k0,
+                                            int k1, bool last) {
+    const int slabs = g.K / BK;
+    const bool tail = last && g.K % BK;
+    if (k1 > k0) t.template kloop<DT>(acc, k0 * C::SPS, k1 * C::SPS, tail ? slabs : -1, g);
+    else if (tail) t.template only_tail<DT>(acc, slabs, g);
+    ring_barrier<0>();          // no DMA in flight, and the ring is free
+}
+
+// Maximum and sum of exp(z - maximum), joined.
+__device__ __forceinline__ void softmax_join(float& m, float& s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    // (of nothing but -inf: no exponential of inf - inf)
+    const float at = top == -INFINITY ? 0.f : top;
+    s = s * __builtin_amdgcn_exp2f((m - at) * LOG2E) + s2 * __builtin_amdgcn_exp2f((m2 - at) * LOG2E);
+    m = top;
+}
+
+// The tile's rows: maximum and sum of exp over its columns, and z at the
+// target.  A lane holds 4 FN columns of FM rows; lanes 16 apart share a row,
+// and so do the WN waves of a row of waves, which join through LDS.
+template <class C>
+__device__ __forceinline__ void softmax_epilogue(const f32x4 (&acc)[C::FM][C::FN], const LossArgs& p, int n, uint32_t nb, int m0,
+                                                 int n0) {
+    const int lane = threadIdx.x & 63, wave = uniform_wave(), g = lane >> 4;
+    const int row = wave / C::WN * C::WTM + (lane & 15), col = n0 + wave % C::WN * C::WTN + g * 4;
+    float2* s = reinterpret_cast<float2*>(linear_ring<C>());      // [BM][WN]
+#pragma unroll
+    for (int f = 0; f < C::FM; ++f) {
+        const int r = m0 + row + f * 16;
+        int target = -1;
+        if (r < n) {
+            if (p.info) target = p.row[r].target;
+            else {
+                const int64_t t = p.target[r];
+                target = t >= 0 && t < p.V ? (int)t : -1;
+            }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < C::FN; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (col + c * 16 + k < p.vn) {
+                    top = fmaxf(top, acc[f][c][k]);
+                    if (col + c * 16 + k == target) p.picked[r] = acc[f][c][k];
+                }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float at = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < C::FN; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (col + c * 16 + k < p.vn) sum += __builtin_amdgcn_exp2f((acc[f][c][k] - at) * LOG2E);
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (g == 0) s[(row + f * 16) * C::WN + wave % C::WN] = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < C::BM; i += C::NT) {
+        if (m0 + i >= n) break;
+        float2 t = s[i * C::WN];
+#pragma unroll
+        for (int w = 1; w < C::WN; ++w) softmax_join(t.x, t.y, s[i * C::WN + w].x, s[i * C::WN + w].y);
+        p.part[(size_t)(m0 + i) * p.tiles + nb] = t;
+    }
+}
+
+// dz of the tile, rounded to the storage type; columns between V and the next
+// multiple of 8 are zeros, which the products read.
+template <class C, int DT>
+__device__ __forceinline__ void dz_epilogue(const f32x4 (&acc)[C::FM][C::FN], const LossArgs& p, int n, int m0, int n0) {
+    const int lane = threadIdx.x & 63, wave = uniform_wave(), g = lane >> 4;
+    const int row = m0 + wave / C::WN * C::WTM + (lane & 15);
+    const int col = n0 + wave % C::WN * C::WTN + (g & 1) * 16 + (g >> 1) * 8;
+#pragma unroll
+    for (int f = 0; f < C::FM; ++f) {
+        const int r = row + f * 16;
+        LossRow q = {};
+        if (r < n) q = p.row[r];
+        const int target = q.target - p.v0;
+        static_for<0, C::FN / 2>([&](auto i) {
+            constexpr int I = decltype(i)::value;
+            float v[8];
+            pair8(acc[f][2 * I], acc[f][2 * I + 1], v);
+            const int c = col + I * 32;
+            if (r >= n || c >= p.vn) return;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[k] = q.a * __builtin_amdgcn_exp2f((v[k] - q.lse) * LOG2E);
+                if (c + k == target) v[k] -= q.b;
+                if (c + k >= p.vn) v[k] = 0.f;
+            }
+            st16(p.dz + (size_t)r * p.lddz + c, narrow8<DT>(v));
+        });
+    }
+}
+
+// A tile of z = x W^T.
+template <class C, int DT, bool GRAD>
+__global__ __launch_bounds__(C::NT, C::OCC) void loss_logits_kernel(LossArgs p) {
+    const int n = packed_rows(p);
+    GemmArgs g{};
+    g.a = packed_x(p, n, g.lda);
+    g.b = p.w + (size_t)p.v0 * p.ldw;
+    g.ldb = p.ldw;
+    g.K = p.H;
+    g.zero = p.zero;
+    g.Mt = (n + C::BM - 1) / C::BM;
+    g.Nt = p.Nt;
+    if (blockIdx.x >= g.Mt * g.Nt) return;
+    uint32_t mb, nb;
+    tile_at(g, xcd_chunked(blockIdx.x, g.Mt * g.Nt), mb, nb);
+    const int m0 = mb * C::BM, n0 = nb * C::BN;
+    f32x4 acc[C::FM][C::FN] = {};
+    LinTile<C, PASS_DX> t;
+    t.a.init(g.a, g.lda, m0, n, 0);
+    t.b.init(g.b, g.ldb, n0, p.vn, 0);
+    loss_reduce<C, DT>(acc, t, g, 0, p.H / BK, true);
+    if constexpr (GRAD) dz_epilogue<C, DT>(acc, p, n, m0, n0);
+    else softmax_epilogue<C>(acc, p, n, nb, m0, n0);
+}
+
+// A part of a tile of dz W: added to the sums of the pieces before.
+template <class C, int DT>
+__device__ __forceinline__ void loss_dx_tile(const LossArgs& p, int n, uint32_t block) {
+    GemmArgs g{};
+    g.a = p.dz;
+    g.lda = p.lddz;
+    g.b = p.w + (size_t)p.v0 * p.ldw;
+    g.ldb = p.ldw;
+    g.K = p.vn;
+    g.zero = p.zero;
+    g.Mt = (n + C::BM - 1) / C::BM;
+    g.Nt = p.dxNt;
+    const uint32_t blocks = g.Mt * g.Nt * p.S;
+    if (block >= blocks) return;
+    const uint32_t q = xcd_chunked(block, blocks), part = q % p.S;
+    uint32_t mb, nb;
+    tile_at(g, q / p.S, mb, nb);
+    const int m0 = mb * C::BM, n0 = nb * C::BN, slabs = p.vn / BK;
+    f32x4 acc[C::FM][C::FN] = {};
+    {
+        LinTile<C, PASS_FWD> t;
+        t.a.init(g.a, g.lda, m0, n, 0);
+        t.b.init(g.b, g.ldb, n0, p.H, 0);
+        const int k0 = min((int)(part * p.ksp), slabs), k1 = min(k0 + (int)p.ksp, slabs);
+        loss_reduce<C, DT>(acc, t, g, k0, k1, part + 1 == p.S);
+    }
+    const int lane = threadIdx.x & 63, wave = uniform_wave();
+    const int row = m0 + wave / C::WN * C::WTM + (lane & 15), col = n0 + wave % C::WN * C::WTN + (lane >> 4) * 4;
+    float* sums = p.sums + (size_t)part * p.rows * p.H;
+#pragma unroll
+    for (int f = 0; f < C::FM; ++f) {
+        const int r = row + f * 16;
+        if (r >= n) continue;
+#pragma unroll
+        for (int c = 0; c < C::FN; ++c) {
+            if (col + c * 16 >= p.H) continue;
+            f32x4* at = reinterpret_cast<f32x4*>(sums + (size_t)r * p.H + col + c * 16);
+            *at = p.first ? acc[f][c] : *at + acc[f][c];
+        }
+    }
+}
+
+// A tile of dz^T x.
+template <class C, int DT>
+__device__ __forceinline__ void loss_dw_tile(const LossArgs& p, int n, uint32_t block) {
+    GemmArgs g{};
+    g.a = p.dz;
+    g.lda = p.lddz;
+    g.b = packed_x(p, n, g.ldb);
+    g.K = n;
+    g.zero = p.zero;
+    g.Mt = p.dwMt;
+    g.Nt = p.dwNt;
+    uint32_t mb, nb;
+    tile_at(g, xcd_chunked(block, g.Mt * g.Nt), mb, nb);
+    const int m0 = mb * C::BM, n0 = nb * C::BN;
+    f32x4 acc[C::FM][C::FN] = {};
+    {
+        LinTile<C, PASS_DW> t;
+        t.a.init(g.a, g.lda, m0, (p.vn + 7) & ~7, 0);
+        t.b.init(g.b, g.ldb, n0, p.H, 0);
+        loss_reduce<C, DT>(acc, t, g, 0, n / BK, true);
+    }
+    const float unit = p.info->unit;
+    const int lane = threadIdx.x & 63, wave = uniform_wave(), l = lane >> 4;
+    const int row = m0 + wave / C::WN * C::WTM + (lane & 15);
+    const int col = n0 + wave % C::WN * C::WTN + (l & 1) * 16 + (l >> 1) * 8;
+    static_for<0, C::FN / 2>([&](auto i) {
+        constexpr int I = decltype(i)::value;
+#pragma unroll
+        for (int f = 0; f < C::FM; ++f) {
+            float v[8];
+            pair8(acc[f][2 * I], acc[f][2 * I + 1], v);
+            const int r = row + f * 16, c = col + I * 32;
+            if (r >= p.vn || c >= p.H) continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= unit;
+            st16(p.dw + (size_t)(p.v0 + r) * p.lddw + c, narrow8<DT>(v));
+        }
+    });
+}
+
+// Both products of a piece: the first dx_blocks workgroups (a multiple of 8,
+// the XCDs that the others are dealt to) dz W, the others dz^T x.
+template <class C, int DT>
+__global__ __launch_bounds__(C::NT, C::OCC) void loss_products_kernel(LossArgs p, uint32_t dx_blocks) {
+    const int n = packed_rows(p);
+    if (blockIdx.x < dx_blocks) loss_dx_tile<C, DT>(p, n, blockIdx.x);
+    else loss_dw_tile<C, DT>(p, n, blockIdx.x - dx_blocks);
+}
+
+}  // namespace mlpc

@@ -1,0 +1,304 @@
+// optim_kernels.hip -- the norm of all gradients and the AdamW step, over
+// tables of tensors that travel with the launch.
+#include <hip/hip_runtime.h>
+
+#include "linear_device.hpp"
+#include "train_launch.h"
+
+namespace mlpc {
+
+constexpr int ONT = 256;
+
+// Elements need no more than their own alignment: gfx950 loads and stores 8 or
+// 16 bytes at any address.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+// The entry of a table whose chunks begin at first[i] that chunk c belongs to
+// (scalar): lanes compare, their ballot counts.
+__device__ __forceinline__ int entry_of(const uint32_t* first, int count, uint32_t c) {
+    const int lane = threadIdx.x & 63;
+    int t = 0;
+    for (int i = 0; i < count; i += 64) t += __popcll(__ballot(i + lane < count && first[i + lane] <= c));
+    return __builtin_amdgcn_readfirstlane(t - 1);
+}
+
+// ---------------------------------------------------------------------- norm
+
+// Sum over a wave in a fixed order.
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+
+// A workgroup's share of the launch's chunks, neighbours, to its partial sum.
+template <int DT>
+__global__ __launch_bounds__(ONT) void norm_sum_kernel(NormTable a) {
+    __shared__ double s[ONT / 64];
+    const uint32_t c0 = (uint32_t)((uint64_t)a.chunks * blockIdx.x / gridDim.x);
+    const uint32_t c1 = (uint32_t)((uint64_t)a.chunks * (blockIdx.x + 1) / gridDim.x);
+    double sum = 0.0;
+    for (uint32_t c = c0; c < c1; ++c) {
+        const int i = entry_of(a.first, a.count, c);
+        const int64_t n = a.n[i], at = (int64_t)(c - a.first[i]) * NORM_CHUNK;
+        const uint16_t* g = a.grad[i];
+#pragma unroll
+        for (int k = 0; k < NORM_CHUNK / (8 * ONT); ++k) {
+            const int64_t e = at + (k * ONT + threadIdx.x) * 8;
+            if (e + 8 <= n) {
+                float f[8];
+                widen8<DT>(*reinterpret_cast<const u32x4_any*>(g + e), f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)f[j], (double)f[j], sum);
+            } else {
+                for (int64_t j = e; j < n; ++j) {
+                    const double f = widen<DT>(g[j]);
+                    sum = __builtin_fma(f, f, sum);
+                }
+            }
+        }
+    }
+    sum = wave_sum64(sum);
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    sum = (s[0] + s[1]) + (s[2] + s[3]);
+    a.part[blockIdx.x] = a.add ? a.part[blockIdx.x] + sum : sum;
+}
+
+// The partial sums to the norm and the gradients' scale.
+__global__ __launch_bounds__(ONT) void norm_join_kernel(NormJoin a) {
+    __shared__ double s[ONT / 64];
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < a.parts; i += ONT) sum += a.part[i];
+    sum = wave_sum64(sum);
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    const double norm = fabs(a.unscale) * sqrt((s[0] + s[1]) + (s[2] + s[3]));
+    *a.norm = (float)norm;
+    if (!a.scale) return;
+    const double clip = norm > a.max_norm ? a.max_norm / norm : 1.0;
+    *a.scale = (float)norm < INFINITY ? (float)(a.unscale * clip) : NAN;
+}
+
+// --------------------------------------------------------------------- adamw
+
+// 32 well mixed bits of 32: two rounds of shift, xor and product with an odd
+// number (the fraction bits of the square roots of 2 and 3).
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x = (x ^ (x >> 16)) * 0x6A09E667u;
+    x = (x ^ (x >> 15)) * 0xBB67AE85u;
+    return x ^ (x >> 16);
+}
+
+// What every workgroup of the step needs, once: its number, the bias
+// corrections in 64 bits, and whether it is left out.
+__global__ __launch_bounds__(64) void adamw_begin_kernel(AdamBegin a) {
+    if (threadIdx.x != 0) return;
+    const float scale = a.scale ? *a.scale : 1.f;
+    AdamStep q{};
+    q.run = fabsf(scale) < INFINITY;
+    if (q.run) {
+        const int64_t t = *a.t + 1;
+        *a.t = t;
+        const double lr = a.lr * (a.lr_scale ? (double)*a.lr_scale : 1.0);
+        q.scale = scale;
+        q.lr = lr;
+        q.size = (float)(lr / (1.0 - pow(a.beta1, (double)t)));
+        q.root = (float)(1.0 / sqrt(1.0 - pow(a.beta2, (double)t)));
+        q.key = mix((uint32_t)t + a.seed);
+    }
+    *a.step = q;
+}
+
+// sqrt of a number that may be too small for the hardware's.
+__device__ __forceinline__ float root_of(float v) {
+    const bool small = v < 0x1p-96f;
+    const float r = __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v);
+    return small ? r * 0x1p-32f : r;
+}
+
+// Largest of a block of 32 lanes, in all of them.
+__device__ __forceinline__ float block_max(float v) {
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+// The power of two with which `top` stays within a type whose largest number
+// is 1.75 2^EXP, and its inverse.
+template <int EXP>
+__device__ __forceinline__ float block_scale(float top, float& inverse) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, top);
+    int e = (int)(b >> 23) - EXP + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = e < 1 ? 1 : e;
+    if (top == 0.f) e = 127;
+    inverse = __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
+    return __builtin_bit_cast(float, (uint32_t)e << 23);
+}
+
+// v >= 0 times the block's inverse scale in e5m2, rounded up or down with the
+// 16 random bits: they are added below the kept fraction.  Subnormal numbers
+// are rounded in the binade above, whose step is theirs.
+__device__ __forceinline__ uint32_t chance_e5m2(float v, float inverse, uint32_t r) {
+    const float y = v * inverse;        // (may underflow)
+    const bool small = y < 0x1p-14f;
+    const uint32_t b = __builtin_bit_cast(uint32_t, small ? y + 0x1p-14f : y);
+    uint32_t code = ((b + (r << 5)) >> 21) - (small ? (113u << 2) : (112u << 2));
+    if (code == 0 && v > 0.f) code = 1;
+    return v < INFINITY ? code : 0x7fu;
+}
+
+// AdamW of one chunk of a tensor: 8 elements per thread.
+template <int DT, int BITS, bool WHOLE>
+__device__ __forceinline__ void adamw_chunk(const AdamTable& a, const AdamStep& q, int i, uint32_t c) {
+    const int64_t n = a.n[i], e = (int64_t)c * ADAM_CHUNK + threadIdx.x * 8;
+    const int left = WHOLE ? 8 : (int)(n - e < 0 ? 0 : n - e < 8 ? n - e : 8);
+    const uint16_t* grad = a.grad[i] + e;
+    uint16_t* w16 = a.w[i] + e;
+    float* master = a.master[i] ? a.master[i] + e : nullptr;
+    float g[8], w[8], m[8], v[8];
+    auto load = [&](const float* p, float (&f)[8]) {
+        if (left == 8) {
+            const f32x4 lo = reinterpret_cast<const f32x4_any*>(p)[0], hi = reinterpret_cast<const f32x4_any*>(p)[1];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = lo[k], f[4 + k] = hi[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = k < left ? p[k] : 0.f;
+        }
+    };
+    auto load16 = [&](const uint16_t* p, float (&f)[8]) {
+        if (left == 8) widen8<DT>(*reinterpret_cast<const u32x4_any*>(p), f);
+        else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = k < left ? widen<DT>(p[k]) : 0.f;
+        }
+    };
+    auto load8 = [&](const uint8_t* p) {
+        uint64_t b = 0;
+        if (left == 8) {
+            const u32x2_any t = *reinterpret_cast<const u32x2_any*>(p);
+            return u32x2{t[0], t[1]};
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < left) b |= (uint64_t)p[k] << (8 * k);
+        return u32x2{(uint32_t)b, (uint32_t)(b >> 32)};
+    };
+    auto store = [&](float* p, const float (&f)[8]) {
+        if (left == 8) {
+            reinterpret_cast<f32x4_any*>(p)[0] = f32x4{f[0], f[1], f[2], f[3]};
+            reinterpret_cast<f32x4_any*>(p)[1] = f32x4{f[4], f[5], f[6], f[7]};
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < left) p[k] = f[k];
+        }
+    };
+    auto store8 = [&](uint8_t* p, u32x2 t) {
+        if (left == 8) {
+            *reinterpret_cast<u32x2_any*>(p) = u32x2_any{t[0], t[1]};
+            return;
+        }
+        const uint64_t b = (uint64_t)t[1] << 32 | t[0];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < left) p[k] = (uint8_t)(b >> (8 * k));
+    };
+    load16(grad, g);
+    if (master) load(master, w);
+    else load16(w16, w);
+    const int64_t block = e / 256;
+    if constexpr (BITS == 32) {
+        load(static_cast<const float*>(a.m[i]) + e, m);
+        load(static_cast<const float*>(a.v[i]) + e, v);
+    } else {
+        const u32x2 mc = load8(static_cast<const uint8_t*>(a.m[i]) + e), vc = load8(static_cast<const uint8_t*>(a.v[i]) + e);
+        const float ms = left ? a.m_scale[i][block] : 0.f, vs = left ? a.v_scale[i][block] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const auto m0 = __builtin_amdgcn_cvt_pk_f32_fp8(mc[k], false), m1 = __builtin_amdgcn_cvt_pk_f32_fp8(mc[k], true);
+            const auto v0 = __builtin_amdgcn_cvt_pk_f32_bf8(vc[k], false), v1 = __builtin_amdgcn_cvt_pk_f32_bf8(vc[k], true);
+            m[4 * k] = m0[0] * ms, m[4 * k + 1] = m0[1] * ms, m[4 * k + 2] = m1[0] * ms, m[4 * k + 3] = m1[1] * ms;
+            v[4 * k] = v0[0] * vs, v[4 * k + 1] = v0[1] * vs, v[4 * k + 2] = v1[0] * vs, v[4 * k + 3] = v1[1] * vs;
+        }
+    }
+    const float keep = (float)(1.0 - q.lr * a.decay[i]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float s = g[k] * q.scale;
+        m[k] = m[k] * a.beta1 + s * a.rest1;
+        v[k] = v[k] * a.beta2 + (s * s) * a.rest2;
+        // (a hardware reciprocal: an ulp of the step's change)
+        w[k] = w[k] * keep - q.size * (m[k] * __builtin_amdgcn_rcpf(root_of(v[k]) * q.root + a.eps));
+    }
+    if (master) store(master, w);
+    if (left == 8) *reinterpret_cast<u32x4_any*>(w16) = narrow8<DT>(w);
+    else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < left) w16[k] = to_storage<DT>(w[k]);
+    }
+    if constexpr (BITS == 32) {
+        store(static_cast<float*>(a.m[i]) + e, m);
+        store(static_cast<float*>(a.v[i]) + e, v);
+    } else {
+        float mt = 0.f, vt = 0.f, mi, vi;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            // (numbers only, of elements that are there)
+            mt = k < left && fabsf(m[k]) < INFINITY ? fmaxf(mt, fabsf(m[k])) : mt;
+            vt = k < left && v[k] < INFINITY ? fmaxf(vt, v[k]) : vt;
+        }
+        mt = block_max(mt);
+        vt = block_max(vt);
+        const float ms = block_scale<8>(mt, mi), vs = block_scale<15>(vt, vi);
+        u32x2 mc = {0, 0}, vc = {0, 0};
+        const uint32_t key = mix(q.key + 0x9E3779B9u * (uint32_t)(a.number + i));
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            const uint32_t r = mix((uint32_t)((e + k) >> 1) + key);
+            vc[k / 4] |= (chance_e5m2(v[k], vi, r & 0xffffu) | chance_e5m2(v[k + 1], vi, r >> 16) << 8) << (8 * (k % 4));
+            const float lo = fabsf(m[k]) < INFINITY ? m[k] * mi : NAN, hi = fabsf(m[k + 1]) < INFINITY ? m[k + 1] * mi : NAN;
+            if (k % 4 == 0) mc[k / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, mc[k / 4], false);
+            else mc[k / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, mc[k / 4], true);
+        }
+        store8(static_cast<uint8_t*>(a.m[i]) + e, mc);
+        store8(static_cast<uint8_t*>(a.v[i]) + e, vc);
+        if ((threadIdx.x & 31) == 0 && left) {
+            a.m_scale[i][block] = ms;
+            a.v_scale[i][block] = vs;
+        }
+    }
+}
+
+template <int DT, int BITS>
+__global__ __launch_bounds__(ONT) void adamw_kernel(AdamTable a) {
+    const AdamStep q = *a.step;
+    if (!q.run) return;
+    const int i = entry_of(a.first, a.count, blockIdx.x);
+    const uint32_t c = blockIdx.x - a.first[i];
+    if ((int64_t)(c + 1) * ADAM_CHUNK <= a.n[i]) adamw_chunk<DT, BITS, true>(a, q, i, c);
+    else adamw_chunk<DT, BITS, false>(a, q, i, c);
+}
+
+}  // namespace mlpc
+
+using namespace mlpc;
+
+hipError_t mlpc_norm_sum(const NormTable& a, int dtype, int parts, hipStream_t s) {
+    return launch(dtype == DT_F16 ? norm_sum_kernel<DT_F16> : norm_sum_kernel<DT_BF16>, dim3(parts), ONT, s, a);
+}
+
+hipError_t mlpc_norm_join(const NormJoin& a, hipStream_t s) { return launch(norm_join_kernel, dim3(1), ONT, s, a); }
+
+hipError_t mlpc_adamw_begin(const AdamBegin& a, hipStream_t s) { return launch(adamw_begin_kernel, dim3(1), 64, s, a); }
+
+hipError_t mlpc_adamw(const AdamTable& a, int dtype, int bits, hipStream_t s) {
+    if (bits == 32) return launch(dtype == DT_F16 ? adamw_kernel<DT_F16, 32> : adamw_kernel<DT_BF16, 32>, dim3(a.chunks), ONT, s, a);
+    return launch(dtype == DT_F16 ? adamw_kernel<DT_F16, 8> : adamw_kernel<DT_BF16, 8>, dim3(a.chunks), ONT, s, a);
+}

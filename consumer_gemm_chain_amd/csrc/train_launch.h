@@ -1,0 +1,134 @@
+// train_launch.h -- internal interface between the C ABI of the training
+// step's operators (train_api.cpp) and their kernels (loss_kernels.hip,
+// loss_rows.hip, optim_kernels.hip).  Not part of the public ABI.
+#pragma once
+
+#include "../../include/mlp_train.h"
+#include "block_launch.h"
+
+namespace mlpc {
+
+// What the loss's kernels know of a call's rows, made on the device: the rows
+// that count are packed (row r is packed row place[r]), and the products run
+// over the `n` packed rows only.
+struct LossInfo {
+    int n;
+    float unit;             // dz is held in units of this
+};
+
+struct LossRow {            // of a packed row, for dz
+    float lse, a, b;        // dz = a exp(z - lse) - b [v = target], in units
+    int target;
+};
+
+struct LossArgs {
+    int64_t rows;
+    int H, V;
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* w;
+    int64_t ldw;
+    const int64_t* target;
+    const float *lse_in, *dloss, *dlse;     // backward; dloss, dlse: nullptr
+    float *loss, *lse;                      // forward; loss: nullptr
+    uint16_t *dx, *dw;                      // nullptr: not computed
+    int64_t lddx, lddw;
+    // workspace
+    LossInfo* info;         // nullptr: every row is packed row r (forward)
+    int* place;             // [rows] (info)
+    LossRow* row;           // [rows] packed (info); the forward pass uses its target alone
+    uint16_t* packed;       // [rows, H] packed rows of x, unless all count
+    float2* part;           // [rows][Nt] maximum and sum of exp(z - maximum) of each tile's columns
+    float* picked;          // [rows] z at the target
+    uint16_t* dz;           // [rows, lddz] of a piece
+    int64_t lddz;
+    float* sums;            // [S][rows, H] dx in units, of the pieces so far
+    const void* zero;
+    // a piece of the vocabulary
+    int v0, vn;
+    bool first;             // sums start here
+    // plan: tiles of the launch's products; dx's reduction in S parts of ksp slabs
+    uint32_t Mt, Nt;        // x W^T
+    uint32_t dxMt, dxNt, S, ksp;
+    uint32_t dwMt, dwNt;
+    int tiles;              // of the forward pass: Nt
+};
+
+// Tables of tensors travel as kernel arguments (at most 4 KB), so a call needs
+// no copy and no memory of its own; entry i's chunks begin at first[i].
+constexpr int NORM_CHUNK = 8192;        // elements
+constexpr int NORM_PARTS = 2048;        // workgroups, and partial sums
+
+struct NormTable {
+    static constexpr int MAX = 192;
+    const uint16_t* grad[MAX];
+    int64_t n[MAX];
+    uint32_t first[MAX];
+    int count;
+    uint32_t chunks;
+    bool add;               // to the partial sums of earlier tables
+    double* part;           // [NORM_PARTS]
+};
+
+struct NormJoin {
+    const double* part;
+    int parts;
+    double unscale, max_norm;
+    float *norm, *scale;    // scale: nullptr
+};
+
+constexpr int ADAM_CHUNK = 2048;        // elements of a workgroup
+
+// Of a step, made on the device.
+struct AdamStep {
+    double lr;
+    float scale, size, root;    // gradients' factor; lr / (1 - beta1^t); 1 / sqrt(1 - beta2^t)
+    uint32_t key;               // of the random bits
+    bool run;
+};
+
+struct AdamBegin {
+    AdamStep* step;
+    int64_t* t;
+    const float *scale, *lr_scale;      // nullptr: 1
+    double lr, beta1, beta2;
+    uint32_t seed;
+};
+
+struct AdamTable {
+    static constexpr int MAX = 48;
+    const uint16_t* grad[MAX];
+    uint16_t* w[MAX];
+    float* master[MAX];
+    void *m[MAX], *v[MAX];
+    float *m_scale[MAX], *v_scale[MAX];
+    double decay[MAX];
+    int64_t n[MAX];
+    uint32_t first[MAX];
+    int count, number;      // number: of the first entry in the call
+    uint32_t chunks;
+    float beta1, rest1, beta2, rest2, eps;
+    const AdamStep* step;
+};
+
+static_assert(sizeof(NormTable) <= 4096 && sizeof(AdamTable) <= 4096, "kernel arguments");
+
+}  // namespace mlpc
+
+// Pack the rows that count, find dz's unit (backward) and gather x.
+hipError_t mlpc_loss_rows(const mlpc::LossArgs& a, bool backward, int dtype, hipStream_t s);
+// z's tiles of a piece: their maxima, sums and picked elements, or dz.
+hipError_t mlpc_loss_logits(const mlpc::LossArgs& a, int cfg, bool backward, int dtype, hipStream_t s);
+// dx's sums and dw of a piece, each unless its pointer is nullptr.
+hipError_t mlpc_loss_products(const mlpc::LossArgs& a, int cfg, int dtype, hipStream_t s);
+// loss and lse from the tiles'.
+hipError_t mlpc_loss_join(const mlpc::LossArgs& a, hipStream_t s);
+// dx from its sums.
+hipError_t mlpc_loss_dx(const mlpc::LossArgs& a, int dtype, hipStream_t s);
+
+// The partial sums of a table's squares, by `parts` workgroups, and their join.
+hipError_t mlpc_norm_sum(const mlpc::NormTable& a, int dtype, int parts, hipStream_t s);
+hipError_t mlpc_norm_join(const mlpc::NormJoin& a, hipStream_t s);
+// The step's number and factors, and a table's tensors.
+hipError_t mlpc_adamw_begin(const mlpc::AdamBegin& a, hipStream_t s);
+hipError_t mlpc_adamw(const mlpc::AdamTable& a, int dtype, int bits, hipStream_t s);
