@@ -1,15 +1,15 @@
 // loss_kernels.hip -- the products of the cross entropy, one object per tile
-// configuration (-DMLPC_LOSS=<id>, linear_configs.h).
+// configuration (-DMLPC_LOSS=<id>, loss_configs.h).
 #include <hip/hip_runtime.h>
 
-#include "linear_configs.h"
+#include "loss_configs.h"
 #include "loss_device.hpp"
 
 namespace mlpc {
 
 #define MLPC_PICK(id, bm, bn, wm, wn, ns, ks, occ) \
     if constexpr (id == MLPC_LOSS) return LinCfg<bm, bn, wm, wn, ns, ks, occ>{};
-static constexpr auto this_cfg() { MLPC_LINEAR_CONFIGS(MLPC_PICK) }
+static constexpr auto this_cfg() { MLPC_LOSS_CONFIGS(MLPC_PICK) }
 #undef MLPC_PICK
 using Cfg = decltype(this_cfg());
 

@@ -71,8 +71,11 @@ __global__ __launch_bounds__(ONT) void norm_sum_kernel(NormTable a) {
 // The partial sums to the norm and the gradients' scale.
 __global__ __launch_bounds__(ONT) void norm_join_kernel(NormJoin a) {
     __shared__ double s[ONT / 64];
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < a.parts; i += ONT) sum += a.part[i];
+    double p[NORM_PARTS / ONT], sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < NORM_PARTS / ONT; ++k) p[k] = k * ONT + threadIdx.x < a.parts ? a.part[k * ONT + threadIdx.x] : 0.0;
+#pragma unroll
+    for (int k = 0; k < NORM_PARTS / ONT; ++k) sum += p[k];
     sum = wave_sum64(sum);
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = sum;
     __syncthreads();
@@ -121,36 +124,32 @@ __device__ __forceinline__ float root_of(float v) {
     return small ? r * 0x1p-32f : r;
 }
 
-// Largest of a block of 32 lanes, in all of them.
-__device__ __forceinline__ float block_max(float v) {
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+// Largest of a block of 32 lanes, in all of them: rotations within rows of 16
+// lanes, then a swap between rows.
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));      // row_ror:8
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    const uint32_t p0 = p[0], p1 = p[1];
+    return max(p0, p1);
 }
 
-// The power of two with which `top` stays within a type whose largest number
-// is 1.75 2^EXP, and its inverse.
+// The power of two with which `top` (its bits) stays within a type whose
+// largest number is 1.75 2^EXP, and its inverse.
 template <int EXP>
-__device__ __forceinline__ float block_scale(float top, float& inverse) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, top);
-    int e = (int)(b >> 23) - EXP + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-    e = e < 1 ? 1 : e;
-    if (top == 0.f) e = 127;
+__device__ __forceinline__ float block_scale(uint32_t top, float& inverse) {
+    int e = (int)(top >> 23) - EXP + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = max(e, 1);
+    if (top == 0) e = 127;
     inverse = __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
     return __builtin_bit_cast(float, (uint32_t)e << 23);
 }
 
-// v >= 0 times the block's inverse scale in e5m2, rounded up or down with the
-// 16 random bits: they are added below the kept fraction.  Subnormal numbers
-// are rounded in the binade above, whose step is theirs.
-__device__ __forceinline__ uint32_t chance_e5m2(float v, float inverse, uint32_t r) {
-    const float y = v * inverse;        // (may underflow)
-    const bool small = y < 0x1p-14f;
-    const uint32_t b = __builtin_bit_cast(uint32_t, small ? y + 0x1p-14f : y);
-    uint32_t code = ((b + (r << 5)) >> 21) - (small ? (113u << 2) : (112u << 2));
-    if (code == 0 && v > 0.f) code = 1;
-    return v < INFINITY ? code : 0x7fu;
-}
+__device__ __forceinline__ uint32_t bits_of(float v) { return __builtin_bit_cast(uint32_t, v); }
+
+constexpr uint32_t INF_BITS = 0x7f800000u;
 
 // AdamW of one chunk of a tensor: 8 elements per thread.
 template <int DT, int BITS, bool WHOLE>
@@ -213,29 +212,37 @@ __device__ __forceinline__ void adamw_chunk(const AdamTable& a, const AdamStep& 
     if (master) load(master, w);
     else load16(w16, w);
     const int64_t block = e / 256;
+    float b1 = a.beta1, b2 = a.beta2;
     if constexpr (BITS == 32) {
         load(static_cast<const float*>(a.m[i]) + e, m);
         load(static_cast<const float*>(a.v[i]) + e, v);
     } else {
         const u32x2 mc = load8(static_cast<const uint8_t*>(a.m[i]) + e), vc = load8(static_cast<const uint8_t*>(a.v[i]) + e);
-        const float ms = left ? a.m_scale[i][block] : 0.f, vs = left ? a.v_scale[i][block] : 0.f;
+        // (scales are powers of two: taken with beta, they round nothing)
+        b1 *= left ? a.m_scale[i][block] : 0.f;
+        b2 *= left ? a.v_scale[i][block] : 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const auto m0 = __builtin_amdgcn_cvt_pk_f32_fp8(mc[k], false), m1 = __builtin_amdgcn_cvt_pk_f32_fp8(mc[k], true);
             const auto v0 = __builtin_amdgcn_cvt_pk_f32_bf8(vc[k], false), v1 = __builtin_amdgcn_cvt_pk_f32_bf8(vc[k], true);
-            m[4 * k] = m0[0] * ms, m[4 * k + 1] = m0[1] * ms, m[4 * k + 2] = m1[0] * ms, m[4 * k + 3] = m1[1] * ms;
-            v[4 * k] = v0[0] * vs, v[4 * k + 1] = v0[1] * vs, v[4 * k + 2] = v1[0] * vs, v[4 * k + 3] = v1[1] * vs;
+            m[4 * k] = m0[0], m[4 * k + 1] = m0[1], m[4 * k + 2] = m1[0], m[4 * k + 3] = m1[1];
+            v[4 * k] = v0[0], v[4 * k + 1] = v0[1], v[4 * k + 2] = v1[0], v[4 * k + 3] = v1[1];
         }
     }
     const float keep = (float)(1.0 - q.lr * a.decay[i]);
+    auto update = [&](auto root) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float s = g[k] * q.scale;
-        m[k] = m[k] * a.beta1 + s * a.rest1;
-        v[k] = v[k] * a.beta2 + (s * s) * a.rest2;
-        // (a hardware reciprocal: an ulp of the step's change)
-        w[k] = w[k] * keep - q.size * (m[k] * __builtin_amdgcn_rcpf(root_of(v[k]) * q.root + a.eps));
-    }
+        for (int k = 0; k < 8; ++k) {
+            const float s = g[k] * q.scale;
+            m[k] = m[k] * b1 + s * a.rest1;
+            v[k] = v[k] * b2 + (s * s) * a.rest2;
+            // (hardware root and reciprocal: ulps of the step's change)
+            w[k] = w[k] * keep - q.size * (m[k] * __builtin_amdgcn_rcpf(root(v[k]) * q.root + a.eps));
+        }
+    };
+    // the hardware's root takes subnormal v as 0: beside an eps of 2^-39 and more that changes nothing
+    if (a.eps >= 0x1p-39f) update([](float x) { return __builtin_amdgcn_sqrtf(x); });
+    else update([](float x) { return root_of(x); });
     if (master) store(master, w);
     if (left == 8) *reinterpret_cast<u32x4_any*>(w16) = narrow8<DT>(w);
     else {
@@ -247,25 +254,45 @@ __device__ __forceinline__ void adamw_chunk(const AdamTable& a, const AdamStep& 
         store(static_cast<float*>(a.m[i]) + e, m);
         store(static_cast<float*>(a.v[i]) + e, v);
     } else {
-        float mt = 0.f, vt = 0.f, mi, vi;
+        // magnitudes compare like their bits; elements that are not there are 0
+        uint32_t mt = 0, vt = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            // (numbers only, of elements that are there)
-            mt = k < left && fabsf(m[k]) < INFINITY ? fmaxf(mt, fabsf(m[k])) : mt;
-            vt = k < left && v[k] < INFINITY ? fmaxf(vt, v[k]) : vt;
+        for (int k = 0; k < 8; ++k) mt = max(mt, bits_of(m[k]) & 0x7fffffffu), vt = max(vt, bits_of(v[k]) & 0x7fffffffu);
+        const bool numbers = !__any(max(mt, vt) >= INF_BITS);
+        if (!numbers) {
+            // what is no number leaves the scale alone and becomes NaN
+            mt = vt = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint32_t mb = bits_of(m[k]) & 0x7fffffffu, vb = bits_of(v[k]) & 0x7fffffffu;
+                pin(mb), pin(vb);       // (the branch is hardly ever taken: nothing of it before it)
+                if (mb < INF_BITS) mt = max(mt, mb);
+                else m[k] = NAN;
+                if (vb < INF_BITS) vt = max(vt, vb);
+            }
         }
-        mt = block_max(mt);
-        vt = block_max(vt);
-        const float ms = block_scale<8>(mt, mi), vs = block_scale<15>(vt, vi);
+        float mi, vi;
+        const float ms = block_scale<8>(block_max(mt), mi), vs = block_scale<15>(block_max(vt), vi);
         u32x2 mc = {0, 0}, vc = {0, 0};
-        const uint32_t key = mix(q.key + 0x9E3779B9u * (uint32_t)(a.number + i));
+        const uint32_t key = mix(q.key + 0x9E3779B9u * (uint32_t)(a.number + i)) + (uint32_t)(e >> 1);
+        // v in units of its scale (which may underflow), at least the smallest number unless it is 0
+        auto unit = [&](float x) {
+            return fmaxf(x * vi, x > 0.f ? 0x1p-16f : 0.f);
+        };
+        static_for<0, 4>([&](auto j) {
+            constexpr int K = decltype(j)::value * 2, W = K / 4, B = K % 4;
+            const uint32_t r = mix(key + K / 2);
+            vc[W] = __builtin_amdgcn_cvt_sr_bf8_f32(unit(v[K]), r << 16, vc[W], B);
+            vc[W] = __builtin_amdgcn_cvt_sr_bf8_f32(unit(v[K + 1]), r & 0xffff0000u, vc[W], B + 1);
+            mc[W] = __builtin_amdgcn_cvt_pk_fp8_f32(m[K] * mi, m[K + 1] * mi, mc[W], B != 0);
+        });
+        if (!numbers) {
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-            const uint32_t r = mix((uint32_t)((e + k) >> 1) + key);
-            vc[k / 4] |= (chance_e5m2(v[k], vi, r & 0xffffu) | chance_e5m2(v[k + 1], vi, r >> 16) << 8) << (8 * (k % 4));
-            const float lo = fabsf(m[k]) < INFINITY ? m[k] * mi : NAN, hi = fabsf(m[k + 1]) < INFINITY ? m[k + 1] * mi : NAN;
-            if (k % 4 == 0) mc[k / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, mc[k / 4], false);
-            else mc[k / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, mc[k / 4], true);
+            for (int k = 0; k < 8; ++k) {
+                uint32_t vb = bits_of(v[k]) & 0x7fffffffu;
+                pin(vb);
+                if (vb >= INF_BITS) vc[k / 4] |= 0x7fu << (8 * (k % 4));
+            }
         }
         store8(static_cast<uint8_t*>(a.m[i]) + e, mc);
         store8(static_cast<uint8_t*>(a.v[i]) + e, vc);

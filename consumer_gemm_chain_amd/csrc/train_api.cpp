@@ -174,7 +174,7 @@ mlpc::LossArgs loss_args(const mlp_loss* h, int64_t rows, const void* x, int64_t
 }
 
 void set_logits(mlpc::LossArgs& a, int cfg, int v0, int vn) {
-    const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
+    const mlpc::LinearCfgInfo c = mlpc_loss_config(cfg);
     a.v0 = v0;
     a.vn = vn;
     a.Mt = up_div(a.rows, c.BM);
@@ -183,7 +183,7 @@ void set_logits(mlpc::LossArgs& a, int cfg, int v0, int vn) {
 
 int logits_cfg(const mlp_loss* h, int64_t rows) {
     if (h->forced_cfg[0] >= 0) return h->forced_cfg[0];
-    return rows <= 16 ? 0 : rows <= 64 ? 1 : rows <= 128 ? 2 : 4;
+    return rows <= 16 ? 0 : rows <= 64 ? 1 : rows <= 128 ? 2 : 3;
 }
 
 }  // namespace
@@ -249,8 +249,8 @@ int mlp_loss_backward(mlp_loss_t h, int64_t rows, const void* x, int64_t ldx, co
     const int width = (int)(up_div(up_div(h->V, pieces), PIECE) * PIECE);
     a.lddz = width;
     const int cfg_z = logits_cfg(h, rows);
-    const int cfg = h->forced_cfg[1] >= 0 ? h->forced_cfg[1] : rows <= 64 ? 1 : rows <= 256 ? 2 : 4;
-    const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
+    const int cfg = h->forced_cfg[1] >= 0 ? h->forced_cfg[1] : rows <= 64 ? 1 : rows <= 256 ? 2 : 3;
+    const mlpc::LinearCfgInfo c = mlpc_loss_config(cfg);
     a.dxMt = up_div(rows, c.BM);
     a.dxNt = a.dwNt = up_div(h->H, c.BN);
     // dx's tiles have long reductions and may be few: parts no longer than an
@@ -288,7 +288,7 @@ int mlp_loss_destroy(mlp_loss_t h) {
 int mlp_loss_debug_set_plan(mlp_loss_t h, int product, int config_id, int split) {
     if (!h) return fail(MLP_EINVAL, "NULL handle");
     if (product < 0 || product > 1) return fail(MLP_EINVAL, "unknown product %d", product);
-    if (config_id < -1 || config_id >= mlpc_linear_num_configs())
+    if (config_id < -1 || config_id >= mlpc_loss_num_configs())
         return fail(MLP_EINVAL, "product %d has no tile configuration %d", product, config_id);
     if (split < 0 || split > 32) return fail(MLP_EINVAL, "the split must be in 0..32, got %d", split);
     h->forced_cfg[product] = config_id;
@@ -425,10 +425,11 @@ mlp_adamw_t mlp_adamw_create(int dtype, int bits, double beta1, double beta2, do
     return h;
 }
 
-int mlp_adamw_step(mlp_adamw_t h, int64_t count, const mlp_adamw_tensor* tensors, double lr, const float* lr_scale,
-                   const float* scale, int64_t* t, void* hip_stream) {
+int mlp_adamw_step(mlp_adamw_t h, int64_t count, const mlp_adamw_tensor* tensors, const void* const* grads, double lr,
+                   const float* lr_scale, const float* scale, int64_t* t, void* hip_stream) {
     if (!h) return fail(MLP_EINVAL, "NULL handle");
     int rc = check_count(count, tensors);
+    if (rc == MLP_OK) rc = check_count(count, grads);
     if (rc == MLP_OK) rc = check_vector("t", t, 8);
     if (rc != MLP_OK) return rc;
     if (misaligned(lr_scale, 4) || misaligned(scale, 4)) return fail(MLP_EINVAL, "lr_scale and scale must be 4-byte aligned");
@@ -439,7 +440,7 @@ int mlp_adamw_step(mlp_adamw_t h, int64_t count, const mlp_adamw_tensor* tensors
         if (rc == MLP_OK && !(fabs(q.decay) < INFINITY)) rc = fail(MLP_EINVAL, "the decay of tensor %lld must be finite", (long long)i);
         if (rc != MLP_OK || q.n == 0) continue;
         const unsigned align = h->bits == 32 ? 4 : 1;
-        rc = check_element_pointer("the gradient", i, q.grad, 2);
+        rc = check_element_pointer("the gradient", i, grads[i], 2);
         if (rc == MLP_OK) rc = check_element_pointer("w", i, q.w, 2);
         if (rc == MLP_OK && q.master) rc = check_element_pointer("master", i, q.master, 4);
         if (rc == MLP_OK) rc = check_element_pointer("m", i, q.m, align);
@@ -466,7 +467,7 @@ int mlp_adamw_step(mlp_adamw_t h, int64_t count, const mlp_adamw_tensor* tensors
         const int k = a.count;
         if (k == 0) a.number = (int)i;
         // (an empty tensor keeps its place: random bits go by the tensor's number)
-        a.grad[k] = static_cast<const uint16_t*>(q.grad);
+        a.grad[k] = static_cast<const uint16_t*>(grads[i]);
         a.w[k] = static_cast<uint16_t*>(q.w);
         a.master[k] = q.master;
         a.m[k] = q.m;

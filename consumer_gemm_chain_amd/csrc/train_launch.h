@@ -115,6 +115,9 @@ static_assert(sizeof(NormTable) <= 4096 && sizeof(AdamTable) <= 4096, "kernel ar
 
 }  // namespace mlpc
 
+// Tile configurations (loss_configs.h).
+int mlpc_loss_num_configs();
+mlpc::LinearCfgInfo mlpc_loss_config(int cfg);
 // Pack the rows that count, find dz's unit (backward) and gather x.
 hipError_t mlpc_loss_rows(const mlpc::LossArgs& a, bool backward, int dtype, hipStream_t s);
 // z's tiles of a piece: their maxima, sums and picked elements, or dz.

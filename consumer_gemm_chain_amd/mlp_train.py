@@ -6,6 +6,7 @@ supplies device memory and streams, and there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 
@@ -21,7 +22,7 @@ BLOCK = 256         # elements that share a scale in 8-bit states
 
 class AdamwTensor(ctypes.Structure):
     """mlp_adamw_tensor."""
-    _fields_ = [("n", ctypes.c_int64), ("grad", ctypes.c_void_p), ("w", ctypes.c_void_p), ("master", ctypes.c_void_p),
+    _fields_ = [("n", ctypes.c_int64), ("w", ctypes.c_void_p), ("master", ctypes.c_void_p),
                 ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("decay", ctypes.c_double)]
 
@@ -41,7 +42,7 @@ def _library():
         lib.mlp_grad_norm_create.argtypes = [ci]
         lib.mlp_grad_norm_forward.argtypes = [vp, i64, vp, vp, d, d, vp, vp, vp]
         lib.mlp_adamw_create.argtypes = [ci, ci, d, d, d, ctypes.c_uint32]
-        lib.mlp_adamw_step.argtypes = [vp, i64, vp, d, vp, vp, vp, vp]
+        lib.mlp_adamw_step.argtypes = [vp, i64, vp, vp, d, vp, vp, vp, vp]
         for name in ("mlp_loss_destroy", "mlp_grad_norm_destroy", "mlp_adamw_destroy"):
             getattr(lib, name).argtypes = [vp]
         for name in EXPORTS:
@@ -91,9 +92,9 @@ def mlp_adamw_create(dtype: int, bits: int, beta1: float, beta2: float, eps: flo
                                                 int(seed) & 0xFFFFFFFF))
 
 
-def mlp_adamw_step(h, count, tensors, lr, lr_scale, scale, t, hip_stream) -> int:
-    """`tensors`: a ctypes array of `count` AdamwTensor."""
-    return _check(_library().mlp_adamw_step(h, count, tensors, lr, lr_scale, scale, t, hip_stream))
+def mlp_adamw_step(h, count, tensors, grads, lr, lr_scale, scale, t, hip_stream) -> int:
+    """`tensors` and `grads`: ctypes arrays of `count` AdamwTensor and pointers."""
+    return _check(_library().mlp_adamw_step(h, count, tensors, grads, lr, lr_scale, scale, t, hip_stream))
 
 
 def mlp_adamw_destroy(h: int | None) -> int:
@@ -154,10 +155,8 @@ class MlpGradNorm(_Layer):
         """norm = |unscale| sqrt(sum g^2) over the contiguous tensors `grads`; scale = unscale min(1, max_norm / norm),
         NaN if the norm is not finite (both float32 [1])."""
         n = len(grads)
-        sizes, pointers = (ctypes.c_int64 * n)(), (ctypes.c_void_p * n)()
-        for i, g in enumerate(grads):
-            pointers[i] = _elements(self, "a gradient", g, self.torch_dtype)
-            sizes[i] = g.numel()
+        pointers = _pointers(self, "a gradient", grads, self.torch_dtype)
+        sizes = _array(ctypes.c_int64, "q", map(type(norm).numel, grads), n)
         mlp_grad_norm_forward(self.h, n, sizes, pointers, float(unscale), float(max_norm),
                               self._vector("norm", norm, 1, self._f32), self._vector("scale", scale, 1, self._f32),
                               self._stream(stream, norm))
@@ -174,6 +173,25 @@ def _elements(layer, name, t, dtype):
     return t.data_ptr()
 
 
+def _pointers(layer, name, tensors, dtype):
+    """A ctypes array of the pointers of contiguous tensors.  (A model has
+    hundreds, a kernel over them takes tens of microseconds: each look at a
+    tensor is one call of a C function for all, 0.04 us a tensor.)"""
+    from torch import Tensor
+    n = len(tensors)
+    if ([t.dtype for t in tensors].count(dtype) != n or not all(map(Tensor.is_contiguous, tensors))
+            or list(map(Tensor.get_device, tensors)).count(layer.device) != n):
+        for t in tensors:
+            _elements(layer, name, t, dtype)
+    return _array(ctypes.c_void_p, "Q", map(Tensor.data_ptr, tensors), n)
+
+
+def _array(kind, code, values, n):
+    """A ctypes array of `values`."""
+    values = array.array(code, values)
+    return (kind * n).from_buffer(values) if n else (kind * 1)()
+
+
 class MlpAdamW(_Layer):
     """AdamW over the contiguous tensors `params` of `dtype`, which it updates
     in place, with states of 32 or 8 bits, and with fp32 master weights if
@@ -182,7 +200,12 @@ class MlpAdamW(_Layer):
     `m` and `v` (one tensor per parameter, of its number of elements; float32,
     or of 8 bits float8_e4m3fn and float8_e5m2), `m_scale` and `v_scale`
     (float32, one per 256 elements) and `step` (int64 [1], counted on the
-    device).  `decay`: weight decay, of all or of each."""
+    device).  `decay`: weight decay, of all or of each.
+
+    A step works on the memory that these tensors had here; a parameter that
+    has got other memory since is refused.  The attributes `params`, `master`,
+    `m`, `v`, `m_scale`, `v_scale` (lists; None where there are none) and `t`
+    are what a checkpoint of the optimizer keeps."""
 
     def __init__(self, params, dtype: str = "f16", states: int = 32, beta1: float = 0.9, beta2: float = 0.999,
                  eps: float = 1e-8, decay=0.0, seed: int = 0, master=False, m=None, v=None, m_scale=None, v_scale=None,
@@ -194,57 +217,53 @@ class MlpAdamW(_Layer):
         self.params = list(params)
         n, f32 = len(self.params), torch.float32
         kinds = (f32, f32) if self.states == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
-        blocks = [-(-p.numel() // BLOCK) for p in self.params]
+        pointers = _pointers(self, "a parameter", self.params, self.torch_dtype)
+        sizes = [p.numel() for p in self.params]
+        blocks = [-(-k // BLOCK) for k in sizes]
 
         def given(name, tensors, dtype, sizes, make):
-            if tensors is None:
-                return [make(p, k) for p, k in zip(self.params, sizes)]
-            tensors = list(tensors)
-            if len(tensors) != n:
-                raise ValueError(f"{name} has {len(tensors)} tensors, expected {n}")
-            for t, k in zip(tensors, sizes):
-                if t.numel() != k:
-                    raise ValueError(f"{name} has a tensor of {t.numel()} elements, expected {k}")
-                _elements(self, name, t, dtype)
-            return tensors
+            tensors = list(tensors) if tensors is not None else [make(p, k) for p, k in zip(self.params, sizes)]
+            if [t.numel() for t in tensors] != sizes:
+                raise ValueError(f"{name} must have {n} tensors of {sizes} elements, got {[t.numel() for t in tensors]}")
+            return tensors, _pointers(self, name, tensors, dtype)
 
-        sizes = [p.numel() for p in self.params]
-        for p in self.params:
-            _elements(self, "a parameter", p, self.torch_dtype)
-        if master is None or master is False:
-            self.master = None
-        else:
-            self.master = given("master", None if master is True else master, f32, sizes, lambda p, k: p.float())
-        empty = lambda dtype: lambda p, k: torch.zeros(p.shape, device=p.device, dtype=torch.uint8 if dtype != f32 else f32).view(dtype)  # noqa: E731
-        self.m, self.v = (given(name, t, kind, sizes, empty(kind)) for name, t, kind in (("m", m, kinds[0]), ("v", v, kinds[1])))
-        ones = lambda p, k: torch.ones(k, device=p.device)  # noqa: E731
-        self.m_scale, self.v_scale = (None, None) if self.states == 32 else (
-            given(name, t, f32, blocks, ones) for name, t in (("m_scale", m_scale), ("v_scale", v_scale)))
-        self.t = torch.zeros(1, dtype=torch.int64, device=torch.device("cuda", self.device)) if step is None else step
-        self._vector("step", self.t, 1, torch.int64)
-        decays = list(decay) if hasattr(decay, "__len__") else [decay] * n
+        def zeros(kind):
+            return lambda p, k: torch.zeros(p.shape, device=p.device, dtype=f32 if kind is f32 else torch.uint8).view(kind)
+
+        self.master = self.m_scale = self.v_scale = masters = m_scales = v_scales = None
+        if master is not None and master is not False:
+            self.master, masters = given("master", None if master is True else master, f32, sizes, lambda p, k: p.float())
+        self.m, ms = given("m", m, kinds[0], sizes, zeros(kinds[0]))
+        self.v, vs = given("v", v, kinds[1], sizes, zeros(kinds[1]))
+        if self.states == 8:
+            ones = lambda p, k: torch.ones(k, device=p.device)  # noqa: E731
+            self.m_scale, m_scales = given("m_scale", m_scale, f32, blocks, ones)
+            self.v_scale, v_scales = given("v_scale", v_scale, f32, blocks, ones)
+        decays = [float(d) for d in decay] if hasattr(decay, "__len__") else [float(decay)] * n
         if len(decays) != n:
             raise ValueError(f"decay has {len(decays)} values, expected {n}")
-        self.decay = [float(d) for d in decays]
-        self._table = (AdamwTensor * n)()
+        at = lambda p, i: p[i] if p is not None else None  # noqa: E731
+        self._table = (AdamwTensor * n)(*[
+            AdamwTensor(sizes[i], pointers[i], at(masters, i), ms[i], vs[i], at(m_scales, i), at(v_scales, i), decays[i])
+            for i in range(n)])
+        self.t = torch.zeros(1, dtype=torch.int64, device=torch.device("cuda", self.device)) if step is None else step
+        self._t = self._vector("step", self.t, 1, torch.int64)
+        # (the memory behind the pointers stays while the optimizer does, whatever becomes of the tensors)
+        lists = (self.params, self.master, self.m, self.v, self.m_scale, self.v_scale, [self.t])
+        self._memory = [t.untyped_storage() for ts in lists if ts for t in ts]
+        self._params = list(pointers)[:n]
+        self._shapes = [p.shape for p in self.params]
 
     _destroy = staticmethod(mlp_adamw_destroy)
 
     def step(self, grads, lr: float, scale=None, lr_scale=None, stream=None):
         """One step with `grads`, one contiguous tensor per parameter, times `scale` (float32 [1] on the device); a scale
         that is not finite leaves the step out.  `lr_scale` (float32 [1] on the device) multiplies `lr`."""
-        if len(grads) != len(self.params):
-            raise ValueError(f"grads has {len(grads)} tensors, expected {len(self.params)}")
-        for i, (g, p, q) in enumerate(zip(grads, self.params, self._table)):
-            if g.shape != p.shape:
-                raise ValueError(f"a gradient has shape {tuple(g.shape)}, expected {tuple(p.shape)}")
-            q.grad = _elements(self, "a gradient", g, self.torch_dtype)
-            # (a parameter or state may have been moved since the last step)
-            q.n, q.w, q.m, q.v, q.decay = p.numel(), p.data_ptr(), self.m[i].data_ptr(), self.v[i].data_ptr(), self.decay[i]
-            if self.master is not None:
-                q.master = self.master[i].data_ptr()
-            if self.m_scale is not None:
-                q.m_scale, q.v_scale = self.m_scale[i].data_ptr(), self.v_scale[i].data_ptr()
-        mlp_adamw_step(self.h, len(self.params), self._table, float(lr), self._vector("lr_scale", lr_scale, 1, self._f32),
-                       self._vector("scale", scale, 1, self._f32), self._vector("t", self.t, 1, self.t.dtype),
-                       self._stream(stream, self.t))
+        shapes = [g.shape for g in grads]
+        if shapes != self._shapes:
+            raise ValueError(f"grads has shapes {[tuple(s) for s in shapes]}, expected {[tuple(s) for s in self._shapes]}")
+        if [p.data_ptr() or None for p in self.params] != self._params:
+            raise ValueError("a parameter has got other memory since the optimizer was made")
+        mlp_adamw_step(self.h, len(shapes), self._table, _pointers(self, "a gradient", grads, self.torch_dtype), float(lr),
+                       self._vector("lr_scale", lr_scale, 1, self._f32), self._vector("scale", scale, 1, self._f32),
+                       self._t, self._stream(stream, self.t))

@@ -136,7 +136,6 @@ int mlp_grad_norm_destroy(mlp_grad_norm_t h);
 /* One tensor of an AdamW step. */
 typedef struct {
     int64_t n;              /* elements, 0 <= n < 2^34 */
-    const void* grad;       /* storage type */
     void* w;                /* storage type */
     float* master;          /* fp32 weights: the step reads and writes these and w becomes their rounding; NULL: w itself */
     void* m;                /* fp32, or e4m3 bytes */
@@ -151,15 +150,15 @@ typedef struct {
  * >= 0. */
 mlp_adamw_t mlp_adamw_create(int dtype, int bits, double beta1, double beta2, double eps, uint32_t seed);
 
-/* One step of `count` tensors.  t (int64, one element, 8-byte aligned, on the
+/* One step of `count` tensors with grads[i] (storage type) of tensors[i].  t (int64, one element, 8-byte aligned, on the
  * device) counts the steps taken; the step's number is t + 1, in 1..2^31.
  * scale (fp32, one element on the device; NULL: 1) multiplies the gradients;
  * if it is NaN or infinite the step is left out: weights, states and t stay as
  * they are.  lr_scale (fp32, one element on the device; NULL: 1) multiplies lr
- * (finite), so that a captured step can follow a schedule.  The array of
- * tensors is read before the call returns. */
-int mlp_adamw_step(mlp_adamw_t h, int64_t count, const mlp_adamw_tensor* tensors, double lr, const float* lr_scale,
-                   const float* scale, int64_t* t, void* hip_stream);
+ * (finite), so that a captured step can follow a schedule.  The arrays are
+ * read before the call returns. */
+int mlp_adamw_step(mlp_adamw_t h, int64_t count, const mlp_adamw_tensor* tensors, const void* const* grads, double lr,
+                   const float* lr_scale, const float* scale, int64_t* t, void* hip_stream);
 
 int mlp_adamw_destroy(mlp_adamw_t h);
 

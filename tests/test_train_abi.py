@@ -67,6 +67,6 @@ def test_null_handles():
     assert lib.mlp_loss_backward(None, 1, None, 8, None, 8, *[None] * 5, 8, None, 8, None) == mc.MLP_EINVAL
     assert lib.mlp_loss_debug_set_plan(None, 0, 0, 0) == mc.MLP_EINVAL
     assert lib.mlp_grad_norm_forward(None, 0, None, None, 1.0, 1.0, None, None, None) == mc.MLP_EINVAL
-    assert lib.mlp_adamw_step(None, 0, None, 1.0, None, None, None, None) == mc.MLP_EINVAL
+    assert lib.mlp_adamw_step(None, 0, None, None, 1.0, None, None, None, None) == mc.MLP_EINVAL
     for destroy in (lib.mlp_loss_destroy, lib.mlp_grad_norm_destroy, lib.mlp_adamw_destroy):
         assert destroy(None) == mc.MLP_OK
