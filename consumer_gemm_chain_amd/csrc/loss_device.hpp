@@ -9,7 +9,9 @@
 //   dW    dz and x both across rows (the n packed rows); one output of V rows
 //
 // The number n of rows that count is known on the device alone: the grid is
-// for every row, and tiles past n end at once.
+// for every row, and tiles past n end at once.  Rows are packed by kernels of
+// their own (loss_rows.hip) before the products, but where all rows fit one
+// tile each workgroup finds out about them by itself.
 #pragma once
 
 #include "linear_device.hpp"
@@ -21,14 +23,26 @@ constexpr float LOG2E = 1.4426950408889634f;
 
 // Rows to reduce or multiply, as a scalar.
 __device__ __forceinline__ int packed_rows(const LossArgs& p) {
-    return p.info ? __builtin_amdgcn_readfirstlane(p.info->n) : (int)p.rows;
+    return p.packing ? __builtin_amdgcn_readfirstlane(p.info->n) : (int)p.rows;
 }
 
-// x's packed rows: x itself if every row counts.
-__device__ __forceinline__ const uint16_t* packed_x(const LossArgs& p, int n, int64_t& ld) {
-    const bool all = n == (int)p.rows;
-    ld = all ? p.ldx : p.H;
-    return all ? p.x : p.packed;
+__device__ __forceinline__ const uint16_t* packed_x(const LossArgs& p, bool copied, int64_t& ld) {
+    ld = copied ? p.H : p.ldx;
+    return copied ? p.packed : p.x;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+// dz's unit from its largest coefficient: dz is rounded to 16 bits, and where
+// all rows have the same dloss (a mean) the target's -dloss then is exact.
+// (fp16 has few small numbers: 2^14 makes room below)
+template <int DT>
+__device__ __forceinline__ float dz_unit(float top) {
+    return top > 0.f && top < INFINITY ? (DT == DT_F16 ? top * 0x1p-14f : top) : 1.f;
 }
 
 // The reduction of a tile: stages k0 .. k1 of `slabs` whole slabs and the one
@@ -66,7 +80,7 @@ __device__ __forceinline__ void softmax_epilogue(const f32x4 (&acc)[C::FM][C::FN
         const int r = m0 + row + f * 16;
         int target = -1;
         if (r < n) {
-            if (p.info) target = p.row[r].target;
+            if (p.packing) target = p.row[r].target;
             else {
                 const int64_t t = p.target[r];
                 target = t >= 0 && t < p.V ? (int)t : -1;
@@ -104,18 +118,70 @@ __device__ __forceinline__ void softmax_epilogue(const f32x4 (&acc)[C::FM][C::FN
     }
 }
 
+// What dz needs of the rows, where they fit one tile: a row per thread, loaded
+// before the reduction and brought to LDS after it.
+template <class C, int DT>
+struct RowsOfTile {
+    int64_t target;
+    float d, l, lse;
+
+    __device__ __forceinline__ void load(const LossArgs& p) {
+        const int r = threadIdx.x;
+        const bool in = r < (int)p.rows;
+        target = in ? p.target[r] : -1;
+        d = in && p.dloss ? p.dloss[r] : 1.f;
+        l = in && p.dlse ? p.dlse[r] : 0.f;
+        lse = in ? p.lse_in[r] : 0.f;
+    }
+
+    // Returns whether a row is left out.
+    __device__ __forceinline__ bool store(const LossArgs& p) {
+        static_assert(C::NT >= C::BM, "a row per thread");
+        LossRow* row = reinterpret_cast<LossRow*>(linear_ring<C>());            // [BM]
+        float* largest = reinterpret_cast<float*>(row + C::BM);                 // [NW]
+        const int r = threadIdx.x, lane = r & 63;
+        const bool counts = target >= 0 && target < p.V;
+        const float top = wave_max(counts ? fmaxf(fabsf(d), fabsf(d + l)) : 0.f);
+        if (lane == 0) largest[r >> 6] = top;
+        const bool out = __syncthreads_or(r < (int)p.rows && !counts);
+        float all = largest[0];
+#pragma unroll
+        for (int w = 1; w < C::NW; ++w) all = fmaxf(all, largest[w]);
+        const float unit = dz_unit<DT>(all);
+        if (r < C::BM) row[r] = counts ? LossRow{lse, (d + l) / unit, d / unit, (int)target} : LossRow{0.f, 0.f, 0.f, -1};
+        if (blockIdx.x == 0 && p.first) {
+            if (r < (int)p.rows) p.place[r] = counts ? r : -1;
+            if (r == 0) *p.info = LossInfo{(int)p.rows, unit, out};
+        }
+        __syncthreads();
+        return out;
+    }
+};
+
+// The products' x where a row is left out (its x may hold anything): the
+// workgroups share the copy.
+__device__ __forceinline__ void copy_rows(const LossArgs& p, int threads) {
+    const int per_row = p.H / 8, chunks = (int)p.rows * per_row;
+    for (int i = blockIdx.x * threads + threadIdx.x; i < chunks; i += gridDim.x * threads) {
+        const int r = i / per_row, c = i % per_row * 8;
+        const int64_t t = p.target[r];
+        st16(p.packed + (size_t)r * p.H + c, t >= 0 && t < p.V ? ld16(p.x + r * p.ldx + c) : u32x4{});
+    }
+}
+
 // dz of the tile, rounded to the storage type; columns between V and the next
 // multiple of 8 are zeros, which the products read.
 template <class C, int DT>
 __device__ __forceinline__ void dz_epilogue(const f32x4 (&acc)[C::FM][C::FN], const LossArgs& p, int n, int m0, int n0) {
     const int lane = threadIdx.x & 63, wave = uniform_wave(), g = lane >> 4;
-    const int row = m0 + wave / C::WN * C::WTM + (lane & 15);
+    const int row = wave / C::WN * C::WTM + (lane & 15);
     const int col = n0 + wave % C::WN * C::WTN + (g & 1) * 16 + (g >> 1) * 8;
 #pragma unroll
     for (int f = 0; f < C::FM; ++f) {
-        const int r = row + f * 16;
+        const int r = m0 + row + f * 16;
         LossRow q = {};
-        if (r < n) q = p.row[r];
+        if (!p.packing) q = reinterpret_cast<const LossRow*>(linear_ring<C>())[row + f * 16];
+        else if (r < n) q = p.row[r];
         const int target = q.target - p.v0;
         static_for<0, C::FN / 2>([&](auto i) {
             constexpr int I = decltype(i)::value;
@@ -127,19 +193,24 @@ __device__ __forceinline__ void dz_epilogue(const f32x4 (&acc)[C::FM][C::FN], co
             for (int k = 0; k < 8; ++k) {
                 v[k] = q.a * __builtin_amdgcn_exp2f((v[k] - q.lse) * LOG2E);
                 if (c + k == target) v[k] -= q.b;
-                if (c + k >= p.vn) v[k] = 0.f;
+                if (c + k >= p.vn || q.target < 0) v[k] = 0.f;
             }
             st16(p.dz + (size_t)r * p.lddz + c, narrow8<DT>(v));
         });
     }
 }
 
-// A tile of z = x W^T.
+// A tile of z = x W^T.  The tiles of different words begin at different places
+// of the reduction: rows of W whose length is a power of two would otherwise
+// have all workgroups read the same few memory channels at a time (48 x 8192 x
+// 32000 121 -> 97 us, 4.3 -> 5.5 TB/s of W).
 template <class C, int DT, bool GRAD>
 __global__ __launch_bounds__(C::NT, C::OCC) void loss_logits_kernel(LossArgs p) {
     const int n = packed_rows(p);
+    RowsOfTile<C, DT> rows;
+    if (GRAD && !p.packing) rows.load(p);
     GemmArgs g{};
-    g.a = packed_x(p, n, g.lda);
+    g.a = packed_x(p, p.packing && n < (int)p.rows, g.lda);
     g.b = p.w + (size_t)p.v0 * p.ldw;
     g.ldb = p.ldw;
     g.K = p.H;
@@ -154,9 +225,39 @@ __global__ __launch_bounds__(C::NT, C::OCC) void loss_logits_kernel(LossArgs p) 
     LinTile<C, PASS_DX> t;
     t.a.init(g.a, g.lda, m0, n, 0);
     t.b.init(g.b, g.ldb, n0, p.vn, 0);
-    loss_reduce<C, DT>(acc, t, g, 0, p.H / BK, true);
-    if constexpr (GRAD) dz_epilogue<C, DT>(acc, p, n, m0, n0);
-    else softmax_epilogue<C>(acc, p, n, nb, m0, n0);
+    const int slabs = p.H / BK, turn = (int)((uint64_t)nb * slabs / g.Nt);
+    loss_reduce<C, DT>(acc, t, g, turn, slabs, true);
+    if (turn > 0) loss_reduce<C, DT>(acc, t, g, 0, turn, false);
+    if constexpr (GRAD) {
+        const bool out = !p.packing && rows.store(p);
+        dz_epilogue<C, DT>(acc, p, n, m0, n0);
+        if (out && p.first) copy_rows(p, C::NT);
+    } else {
+        softmax_epilogue<C>(acc, p, n, nb, m0, n0);
+    }
+}
+
+// The tile's rows below `rows` and columns below `cols`, times `unit`, rounded;
+// rows whose place (unless nullptr) is -1 are zeros.
+template <class C, int DT>
+__device__ __forceinline__ void store_scaled(const f32x4 (&acc)[C::FM][C::FN], uint16_t* d, int64_t ld, int m0, int rows, int n0,
+                                             int cols, float unit, const int* place) {
+    const int lane = threadIdx.x & 63, wave = uniform_wave(), g = lane >> 4;
+    const int row = m0 + wave / C::WN * C::WTM + (lane & 15);
+    const int col = n0 + wave % C::WN * C::WTN + (g & 1) * 16 + (g >> 1) * 8;
+    static_for<0, C::FN / 2>([&](auto i) {
+        constexpr int I = decltype(i)::value;
+#pragma unroll
+        for (int f = 0; f < C::FM; ++f) {
+            float v[8];
+            pair8(acc[f][2 * I], acc[f][2 * I + 1], v);
+            const int r = row + f * 16, c = col + I * 32;
+            if (r >= rows || c >= cols) continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= unit;
+            st16(d + (size_t)r * ld + c, place && place[r] < 0 ? u32x4{} : narrow8<DT>(v));
+        }
+    });
 }
 
 // A part of a tile of dz W: added to the sums of the pieces before.
@@ -186,6 +287,10 @@ __device__ __forceinline__ void loss_dx_tile(const LossArgs& p, int n, uint32_t 
         loss_reduce<C, DT>(acc, t, g, k0, k1, part + 1 == p.S);
     }
     const int lane = threadIdx.x & 63, wave = uniform_wave();
+    if (p.direct) {
+        store_scaled<C, DT>(acc, p.dx, p.lddx, m0, n, n0, p.H, p.info->unit, p.place);
+        return;
+    }
     const int row = m0 + wave / C::WN * C::WTM + (lane & 15), col = n0 + wave % C::WN * C::WTN + (lane >> 4) * 4;
     float* sums = p.sums + (size_t)part * p.rows * p.H;
 #pragma unroll
@@ -207,7 +312,7 @@ __device__ __forceinline__ void loss_dw_tile(const LossArgs& p, int n, uint32_t 
     GemmArgs g{};
     g.a = p.dz;
     g.lda = p.lddz;
-    g.b = packed_x(p, n, g.ldb);
+    g.b = packed_x(p, __builtin_amdgcn_readfirstlane(p.info->copied), g.ldb);
     g.K = n;
     g.zero = p.zero;
     g.Mt = p.dwMt;
@@ -222,23 +327,7 @@ __device__ __forceinline__ void loss_dw_tile(const LossArgs& p, int n, uint32_t 
         t.b.init(g.b, g.ldb, n0, p.H, 0);
         loss_reduce<C, DT>(acc, t, g, 0, n / BK, true);
     }
-    const float unit = p.info->unit;
-    const int lane = threadIdx.x & 63, wave = uniform_wave(), l = lane >> 4;
-    const int row = m0 + wave / C::WN * C::WTM + (lane & 15);
-    const int col = n0 + wave % C::WN * C::WTN + (l & 1) * 16 + (l >> 1) * 8;
-    static_for<0, C::FN / 2>([&](auto i) {
-        constexpr int I = decltype(i)::value;
-#pragma unroll
-        for (int f = 0; f < C::FM; ++f) {
-            float v[8];
-            pair8(acc[f][2 * I], acc[f][2 * I + 1], v);
-            const int r = row + f * 16, c = col + I * 32;
-            if (r >= p.vn || c >= p.H) continue;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= unit;
-            st16(p.dw + (size_t)(p.v0 + r) * p.lddw + c, narrow8<DT>(v));
-        }
-    });
+    store_scaled<C, DT>(acc, p.dw + (size_t)p.v0 * p.lddw, p.lddw, m0, p.vn, n0, p.H, p.info->unit, nullptr);
 }
 
 // Both products of a piece: the first dx_blocks workgroups (a multiple of 8,

@@ -1,29 +1,39 @@
 // loss_kernels.hip -- the products of the cross entropy, one object per tile
-// configuration (-DMLPC_LOSS=<id>, loss_configs.h).
+// configuration (-DMLPC_LOSS=<id>, linear_configs.h).
 #include <hip/hip_runtime.h>
 
-#include "loss_configs.h"
+#include "linear_configs.h"
 #include "loss_device.hpp"
 
 namespace mlpc {
 
 #define MLPC_PICK(id, bm, bn, wm, wn, ns, ks, occ) \
     if constexpr (id == MLPC_LOSS) return LinCfg<bm, bn, wm, wn, ns, ks, occ>{};
-static constexpr auto this_cfg() { MLPC_LOSS_CONFIGS(MLPC_PICK) }
+static constexpr auto this_cfg() { MLPC_LINEAR_CONFIGS(MLPC_PICK) }
 #undef MLPC_PICK
 using Cfg = decltype(this_cfg());
 
+// The configurations that the linear layer has for dz W^T, whose layout z has,
+// and for both products in one launch.
+static constexpr bool HAS_LOGITS = MLPC_LOSS != 7, HAS_PRODUCTS = MLPC_LOSS != 0 && MLPC_LOSS != 7;
+
 template <int DT>
 static hipError_t logits(const LossArgs& a, bool backward, hipStream_t s) {
-    const dim3 grid(a.Mt * a.Nt);
-    return backward ? launch(loss_logits_kernel<Cfg, DT, true>, grid, Cfg::NT, s, a)
-                    : launch(loss_logits_kernel<Cfg, DT, false>, grid, Cfg::NT, s, a);
+    if constexpr (HAS_LOGITS) {
+        const dim3 grid(a.Mt * a.Nt);
+        return backward ? launch(loss_logits_kernel<Cfg, DT, true>, grid, Cfg::NT, s, a)
+                        : launch(loss_logits_kernel<Cfg, DT, false>, grid, Cfg::NT, s, a);
+    }
+    return hipErrorInvalidValue;
 }
 
 template <int DT>
 static hipError_t products(const LossArgs& a, hipStream_t s) {
-    const uint32_t dx = a.dx ? (a.dxMt * a.dxNt * a.S + 7) / 8 * 8 : 0, dw = a.dw ? a.dwMt * a.dwNt : 0;
-    return launch(loss_products_kernel<Cfg, DT>, dim3(dx + dw), Cfg::NT, s, a, dx);
+    if constexpr (HAS_PRODUCTS) {
+        const uint32_t dx = a.dx ? (a.dxMt * a.dxNt * a.S + 7) / 8 * 8 : 0, dw = a.dw ? a.dwMt * a.dwNt : 0;
+        return launch(loss_products_kernel<Cfg, DT>, dim3(dx + dw), Cfg::NT, s, a, dx);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace mlpc

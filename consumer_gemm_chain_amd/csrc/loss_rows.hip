@@ -8,16 +8,9 @@ namespace mlpc {
 
 constexpr int PNT = 1024;
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
-
 // Places of the rows that count, in order, by one workgroup: 1024 rows at a
 // time, places from the waves' ballots.  Backward also what dz needs of each
-// row, in units of the largest coefficient: dz is rounded to 16 bits, and where
-// all rows have the same dloss (a mean) the target's -dloss then is exact.
+// row.
 template <bool GRAD, int DT>
 __global__ __launch_bounds__(PNT) void loss_pack_kernel(LossArgs a) {
     __shared__ int count[PNT / 64];
@@ -40,8 +33,7 @@ __global__ __launch_bounds__(PNT) void loss_pack_kernel(LossArgs a) {
         __syncthreads();
         top = largest[lane & (PNT / 64 - 1)];
         top = wave_max(top);
-        // (fp16 has few small numbers: 2^14 makes room below)
-        if (top > 0.f && top < INFINITY) unit = DT == DT_F16 ? top * 0x1p-14f : top;
+        unit = dz_unit<DT>(top);
     }
     int n = 0;
     for (int64_t r0 = 0; r0 < a.rows; r0 += PNT) {
@@ -69,12 +61,12 @@ __global__ __launch_bounds__(PNT) void loss_pack_kernel(LossArgs a) {
         }
         a.row[at] = q;
     }
-    if (threadIdx.x == 0) *a.info = LossInfo{n, unit};
+    if (threadIdx.x == 0) *a.info = LossInfo{n, unit, n < (int)a.rows};
 }
 
 // The packed rows of x, unless every row counts.
 __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
-    if (a.info->n == (int)a.rows) return;
+    if (!a.info->copied) return;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int at = a.place[r];
         if (at < 0) continue;
@@ -98,7 +90,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a) {
         }
         return;
     }
-    const int64_t at = a.info ? a.place[r] : r;
+    const int64_t at = a.packing ? a.place[r] : r;
     float m = -INFINITY, s = 0.f;
     for (int i = lane; i < a.tiles; i += 64) {
         const float2 v = a.part[(size_t)at * a.tiles + i];

@@ -9,6 +9,7 @@
 
 #include "../../include/mlp_train.h"
 #include "api_checks.h"
+#include "linear_plan.h"
 #include "train_launch.h"
 
 struct mlp_loss {
@@ -53,6 +54,8 @@ constexpr size_t SPLIT_BYTES = (size_t)64 << 20;        // of dx's sums in parts
 constexpr int64_t MAX_PRODUCT = (int64_t)1 << 38;
 constexpr int PIECE = 256;                              // columns of a piece: a multiple of this
 constexpr int MIN_TILE = 128;                           // columns of the narrowest tile
+
+constexpr double PACK_US = 6.0;                         // packing a few rows, two launches
 
 uint32_t up_div(int64_t a, int64_t b) { return (uint32_t)((a + b - 1) / b); }
 
@@ -174,16 +177,53 @@ mlpc::LossArgs loss_args(const mlp_loss* h, int64_t rows, const void* x, int64_t
 }
 
 void set_logits(mlpc::LossArgs& a, int cfg, int v0, int vn) {
-    const mlpc::LinearCfgInfo c = mlpc_loss_config(cfg);
+    const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
     a.v0 = v0;
     a.vn = vn;
     a.Mt = up_div(a.rows, c.BM);
     a.Nt = up_div(vn, c.BN);
 }
 
-int logits_cfg(const mlp_loss* h, int64_t rows) {
+// The products run on tiles that the linear layer has for them, unsplit but for
+// dx, and its estimates choose among these.
+int logits_cfg(const mlp_loss* h, int64_t rows, int64_t vn) {
     if (h->forced_cfg[0] >= 0) return h->forced_cfg[0];
-    return rows <= 16 ? 0 : rows <= 64 ? 1 : rows <= 128 ? 2 : 3;
+    int best = 0;
+    double cost = 0.0;
+    for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
+        if (!mlpc_linear_has(cfg, mlpc::PASS_DX) || !config_fits(mlpc_linear_config(cfg), rows)) continue;
+        const Work w = {make_plan(cfg, rows, vn, h->H, 1, h->cus), rows, vn, h->H};
+        // (more than one row of tiles: the rows are packed first)
+        const double c = plan_cost(&w, 1, SINGLE, h->cus) + (w.p.Mt > 1 ? PACK_US : 0.0);
+        if (cfg == 0 || c < cost) best = cfg, cost = c;
+    }
+    return best;
+}
+
+// Tile configuration of both products of a piece, and the parts of dx's
+// reduction, at most `room`: dx's tiles have long reductions and may be few.
+int products_cfg(const mlp_loss* h, int64_t rows, int64_t vn, bool dx, bool dw, int64_t room, uint32_t* parts) {
+    int best = 1;
+    double cost = 0.0;
+    bool found = false;
+    for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
+        if (h->forced_cfg[1] >= 0 ? cfg != h->forced_cfg[1]
+                                  : !mlpc_linear_has(cfg, mlpc::PASS_BOTH_DX) || !config_fits(mlpc_linear_config(cfg), rows))
+            continue;
+        uint32_t last = 0;
+        for (int64_t S = 1; S <= 32 && S <= room; ++S) {
+            if (h->forced_split > 0 && S != h->forced_split && S < room) continue;
+            Work w[2] = {{make_plan(cfg, rows, h->H, vn, (uint32_t)S, h->cus), rows, h->H, vn},
+                         {make_plan(cfg, vn, h->H, rows, 1, h->cus), vn, h->H, rows}};
+            if (w[0].p.S == last) continue;
+            last = w[0].p.S;
+            w[0].p.direct = 0;
+            const double c = !dx ? plan_cost(w + 1, 1, BOTH, h->cus) : plan_cost(w, dw ? 2 : 1, BOTH, h->cus);
+            if (!found || c < cost) best = cfg, cost = c, *parts = (uint32_t)S, found = true;
+            if (!dx) break;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -206,12 +246,11 @@ int mlp_loss_forward(mlp_loss_t h, int64_t rows, const void* x, int64_t ldx, con
     mlpc::LossArgs a = loss_args(h, rows, x, ldx, w, ldw, target);
     a.loss = loss;
     a.lse = lse;
-    const int cfg = logits_cfg(h, rows);
+    const int cfg = logits_cfg(h, rows, h->V);
     set_logits(a, cfg, 0, h->V);
     a.tiles = (int)a.Nt;
-    hipError_t e = hipSuccess;
-    if (a.Mt > 1) e = mlpc_loss_rows(a, false, h->dtype, s);
-    else a.info = nullptr;          // one row of tiles: packing would save nothing
+    a.packing = a.Mt > 1;
+    hipError_t e = a.packing ? mlpc_loss_rows(a, false, h->dtype, s) : hipSuccess;
     if (e == hipSuccess) e = mlpc_loss_logits(a, cfg, false, h->dtype, s);
     if (e == hipSuccess) e = mlpc_loss_join(a, s);
     return launched(e);
@@ -248,33 +287,27 @@ int mlp_loss_backward(mlp_loss_t h, int64_t rows, const void* x, int64_t ldx, co
     const uint32_t pieces = up_div(h->V, most);
     const int width = (int)(up_div(up_div(h->V, pieces), PIECE) * PIECE);
     a.lddz = width;
-    const int cfg_z = logits_cfg(h, rows);
-    const int cfg = h->forced_cfg[1] >= 0 ? h->forced_cfg[1] : rows <= 64 ? 1 : rows <= 256 ? 2 : 3;
-    const mlpc::LinearCfgInfo c = mlpc_loss_config(cfg);
+    const int cfg_z = logits_cfg(h, rows > 0 ? rows : 1, width);
+    const int64_t room = rows > 0 ? (int64_t)(h->sum_elems / ((size_t)rows * h->H)) : 1;
+    a.S = 1;
+    const int cfg = products_cfg(h, rows > 0 ? rows : 1, width, a.dx != nullptr, a.dw != nullptr, room, &a.S);
+    const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
     a.dxMt = up_div(rows, c.BM);
     a.dxNt = a.dwNt = up_div(h->H, c.BN);
-    // dx's tiles have long reductions and may be few: parts no longer than an
-    // even share of all the slabs of both products per CU
-    const int64_t slabs = width / 64, tiles = (int64_t)a.dxMt * a.dxNt;
-    const int64_t all = slabs * tiles + (a.dw ? (int64_t)up_div(width, c.BM) * a.dwNt * up_div(rows, 64) : 0);
-    int64_t S = h->forced_split > 0 ? h->forced_split : all > 0 ? slabs * h->cus / all : 1;
-    const int64_t room = rows > 0 ? (int64_t)(h->sum_elems / ((size_t)rows * h->H)) : 1;
-    if (S > room) S = room;
-    if (S > 32) S = 32;
-    if (S > slabs / 4) S = slabs / 4;
-    if (S < 1) S = 1;
-    hipError_t e = mlpc_loss_rows(a, true, h->dtype, s);
+    set_logits(a, cfg_z, 0, width);
+    a.packing = a.Mt != 1;
+    a.direct = !a.packing && pieces == 1 && a.S == 1;
+    hipError_t e = a.packing ? mlpc_loss_rows(a, true, h->dtype, s) : hipSuccess;
     for (int64_t v0 = 0; v0 < h->V && e == hipSuccess; v0 += width) {
         const int vn = (int)(h->V - v0 < width ? h->V - v0 : width);
         set_logits(a, cfg_z, (int)v0, vn);
         a.first = v0 == 0;
-        a.S = (uint32_t)S;
-        a.ksp = up_div(slabs, S);
+        a.ksp = up_div(vn / 64, a.S);
         a.dwMt = up_div(vn, c.BM);
         if (rows > 0) e = mlpc_loss_logits(a, cfg_z, true, h->dtype, s);
         if (e == hipSuccess) e = mlpc_loss_products(a, cfg, h->dtype, s);
     }
-    if (e == hipSuccess && a.dx) e = mlpc_loss_dx(a, h->dtype, s);
+    if (e == hipSuccess && a.dx && !a.direct) e = mlpc_loss_dx(a, h->dtype, s);
     return launched(e);
 }
 
@@ -288,7 +321,8 @@ int mlp_loss_destroy(mlp_loss_t h) {
 int mlp_loss_debug_set_plan(mlp_loss_t h, int product, int config_id, int split) {
     if (!h) return fail(MLP_EINVAL, "NULL handle");
     if (product < 0 || product > 1) return fail(MLP_EINVAL, "unknown product %d", product);
-    if (config_id < -1 || config_id >= mlpc_loss_num_configs())
+    if (config_id < -1 || config_id >= mlpc_linear_num_configs() ||
+        (config_id >= 0 && !mlpc_linear_has(config_id, product ? mlpc::PASS_BOTH_DX : mlpc::PASS_DX)))
         return fail(MLP_EINVAL, "product %d has no tile configuration %d", product, config_id);
     if (split < 0 || split > 32) return fail(MLP_EINVAL, "the split must be in 0..32, got %d", split);
     h->forced_cfg[product] = config_id;

@@ -8,17 +8,19 @@
 
 namespace mlpc {
 
-// What the loss's kernels know of a call's rows, made on the device: the rows
+// What the loss's kernels know of a call's rows, made on the device.  The rows
 // that count are packed (row r is packed row place[r]), and the products run
-// over the `n` packed rows only.
+// over the n packed rows only.  Calls whose rows fit one tile would gain nothing
+// by that: theirs stay where they are, and dz is 0 in rows that are left out.
 struct LossInfo {
     int n;
     float unit;             // dz is held in units of this
+    int copied;             // the products' x is the workspace's: packed, or with zeros in the rows left out
 };
 
 struct LossRow {            // of a packed row, for dz
     float lse, a, b;        // dz = a exp(z - lse) - b [v = target], in units
-    int target;
+    int target;             // -1: left out
 };
 
 struct LossArgs {
@@ -34,10 +36,10 @@ struct LossArgs {
     uint16_t *dx, *dw;                      // nullptr: not computed
     int64_t lddx, lddw;
     // workspace
-    LossInfo* info;         // nullptr: every row is packed row r (forward)
-    int* place;             // [rows] (info)
+    LossInfo* info;
+    int* place;             // [rows]; -1: left out
     LossRow* row;           // [rows] packed (info); the forward pass uses its target alone
-    uint16_t* packed;       // [rows, H] packed rows of x, unless all count
+    uint16_t* packed;       // [rows, H] of x
     float2* part;           // [rows][Nt] maximum and sum of exp(z - maximum) of each tile's columns
     float* picked;          // [rows] z at the target
     uint16_t* dz;           // [rows, lddz] of a piece
@@ -47,6 +49,8 @@ struct LossArgs {
     // a piece of the vocabulary
     int v0, vn;
     bool first;             // sums start here
+    bool packing;           // the rows have been packed
+    bool direct;            // dx is written by the products, not its sums
     // plan: tiles of the launch's products; dx's reduction in S parts of ksp slabs
     uint32_t Mt, Nt;        // x W^T
     uint32_t dxMt, dxNt, S, ksp;
@@ -115,9 +119,6 @@ static_assert(sizeof(NormTable) <= 4096 && sizeof(AdamTable) <= 4096, "kernel ar
 
 }  // namespace mlpc
 
-// Tile configurations (loss_configs.h).
-int mlpc_loss_num_configs();
-mlpc::LinearCfgInfo mlpc_loss_config(int cfg);
 // Pack the rows that count, find dz's unit (backward) and gather x.
 hipError_t mlpc_loss_rows(const mlpc::LossArgs& a, bool backward, int dtype, hipStream_t s);
 // z's tiles of a piece: their maxima, sums and picked elements, or dz.
