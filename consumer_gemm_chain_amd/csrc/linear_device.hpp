@@ -52,10 +52,16 @@ struct LinCfg {
     static_assert(LPS * (NS - 1) <= 63, "vmcnt range");
 };
 
+template <int BYTES>
+__device__ __forceinline__ char* ring_bytes() {
+    __shared__ __attribute__((aligned(1024))) char buf[BYTES];
+    return buf;
+}
+
+// (one for all configurations of its size that a kernel takes)
 template <class C>
 __device__ __forceinline__ char* linear_ring() {
-    __shared__ __attribute__((aligned(1024))) char buf[C::RING];
-    return buf;
+    return ring_bytes<C::RING>();
 }
 
 // How a pass stores its operands.

@@ -45,6 +45,52 @@ __device__ __forceinline__ float dz_unit(float top) {
     return top > 0.f && top < INFINITY ? (DT == DT_F16 ? top * 0x1p-14f : top) : 1.f;
 }
 
+// A configuration whose waves multiply F fragments of 16 rows: tiles of 32 F
+// rows.  The DMA still brings BM rows.
+template <class C, int F>
+struct Shorter : C {
+    static constexpr int FM = F, NF = F * C::FN, WTM = 16 * F;
+};
+
+// Rows of a tile.
+template <class C>
+constexpr int tile_rows = C::WM * C::WTM;
+
+// The fragments per wave with which the row tiles of n rows take least, if each
+// row of tiles has `columns` tiles, dealt to `cus` CUs in rounds (0: among other
+// work): 670 rows are three tiles of 224.  A tile costs as much as 1.2 fragments
+// more than its products; half of what a last, partial round wastes comes back
+// as the others' higher clocks (1000 x 12288 x 50001 with a third of the rows
+// left out, z alone: 256 rows per tile 1030 us, 160 rows, which fill the rounds
+// best, 1225, 224 rows 955).
+__device__ __forceinline__ int fragments_for(int n, uint32_t columns, uint32_t cus) {
+    int best = 8;
+    float cost = 0.f;
+#pragma unroll
+    for (int f = 8; f >= 5; --f) {
+        const uint32_t tiles = (uint32_t)((n + 32 * f - 1) / (32 * f)) * columns;
+        const float rounds = cus ? 0.5f * ((float)((tiles + cus - 1) / cus) + (float)tiles / (float)cus) : (float)tiles;
+        const float c = rounds * (f + 1.2f);
+        if (f == 8 || c < cost) {
+            best = f;
+            cost = c;
+        }
+    }
+    return best;
+}
+
+// f(C with the fragments per wave that suit n rows), where tiles are tall.
+template <class C, class F>
+__device__ __forceinline__ void with_fragments(int n, uint32_t columns, uint32_t cus, F&& f) {
+    if constexpr (C::FM == 8) {
+        const int k = fragments_for(n, columns, cus);
+        if (k == 7) return f(Shorter<C, 7>{});
+        if (k == 6) return f(Shorter<C, 6>{});
+        if (k == 5) return f(Shorter<C, 5>{});
+    }
+    f(C{});
+}
+
 // The reduction of a tile: stages k0 .. k1 of `slabs` whole slabs and the one
 // that ends past K, for the last part.
 template <class C, int DT, int PASS>
@@ -109,7 +155,7 @@ __device__ __forceinline__ void softmax_epilogue(const f32x4 (&acc)[C::FM][C::FN
         if (g == 0) s[(row + f * 16) * C::WN + wave % C::WN] = make_float2(top, sum);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < C::BM; i += C::NT) {
+    for (int i = threadIdx.x; i < tile_rows<C>; i += C::NT) {
         if (m0 + i >= n) break;
         float2 t = s[i * C::WN];
 #pragma unroll
@@ -200,32 +246,30 @@ __device__ __forceinline__ void dz_epilogue(const f32x4 (&acc)[C::FM][C::FN], co
     }
 }
 
-// A tile of z = x W^T.  The tiles of different words begin at different places
-// of the reduction: rows of W whose length is a power of two would otherwise
-// have all workgroups read the same few memory channels at a time (48 x 8192 x
-// 32000 121 -> 97 us, 4.3 -> 5.5 TB/s of W).
+// A tile of z = x W^T.  With one or two rows of tiles, reading W bounds it, and
+// tiles of different words then begin at different places of a long reduction:
+// rows of W whose length is a power of two would otherwise have all workgroups
+// read the same few memory channels at a time (48 x 8192 x 32000 121 -> 97 us,
+// 4.3 -> 5.5 TB/s of W).
 template <class C, int DT, bool GRAD>
-__global__ __launch_bounds__(C::NT, C::OCC) void loss_logits_kernel(LossArgs p) {
-    const int n = packed_rows(p);
-    RowsOfTile<C, DT> rows;
-    if (GRAD && !p.packing) rows.load(p);
+__device__ __forceinline__ void loss_logits_tile(const LossArgs& p, int n, RowsOfTile<C, DT>& rows) {
     GemmArgs g{};
     g.a = packed_x(p, p.packing && n < (int)p.rows, g.lda);
     g.b = p.w + (size_t)p.v0 * p.ldw;
     g.ldb = p.ldw;
     g.K = p.H;
     g.zero = p.zero;
-    g.Mt = (n + C::BM - 1) / C::BM;
+    g.Mt = (n + tile_rows<C> - 1) / tile_rows<C>;
     g.Nt = p.Nt;
     if (blockIdx.x >= g.Mt * g.Nt) return;
     uint32_t mb, nb;
     tile_at(g, xcd_chunked(blockIdx.x, g.Mt * g.Nt), mb, nb);
-    const int m0 = mb * C::BM, n0 = nb * C::BN;
+    const int m0 = mb * tile_rows<C>, n0 = nb * C::BN;
     f32x4 acc[C::FM][C::FN] = {};
     LinTile<C, PASS_DX> t;
     t.a.init(g.a, g.lda, m0, n, 0);
     t.b.init(g.b, g.ldb, n0, p.vn, 0);
-    const int slabs = p.H / BK, turn = (int)((uint64_t)nb * slabs / g.Nt);
+    const int slabs = p.H / BK, turn = g.Mt <= 2 && slabs >= 32 ? (int)((uint64_t)nb * slabs / g.Nt) : 0;
     loss_reduce<C, DT>(acc, t, g, turn, slabs, true);
     if (turn > 0) loss_reduce<C, DT>(acc, t, g, 0, turn, false);
     if constexpr (GRAD) {
@@ -235,6 +279,21 @@ __global__ __launch_bounds__(C::NT, C::OCC) void loss_logits_kernel(LossArgs p) 
     } else {
         softmax_epilogue<C>(acc, p, n, nb, m0, n0);
     }
+}
+
+template <class C, int DT, bool GRAD>
+__global__ __launch_bounds__(C::NT, C::OCC) void loss_logits_kernel(LossArgs p) {
+    const int n = packed_rows(p);
+    if (p.packing) {
+        with_fragments<C>(n, p.Nt, p.cus, [&](auto c) {
+            RowsOfTile<decltype(c), DT> none;
+            loss_logits_tile<decltype(c), DT, GRAD>(p, n, none);
+        });
+        return;
+    }
+    RowsOfTile<C, DT> rows;
+    if (GRAD) rows.load(p);
+    loss_logits_tile<C, DT, GRAD>(p, n, rows);
 }
 
 // The tile's rows below `rows` and columns below `cols`, times `unit`, rounded;
@@ -270,14 +329,14 @@ __device__ __forceinline__ void loss_dx_tile(const LossArgs& p, int n, uint32_t 
     g.ldb = p.ldw;
     g.K = p.vn;
     g.zero = p.zero;
-    g.Mt = (n + C::BM - 1) / C::BM;
+    g.Mt = (n + tile_rows<C> - 1) / tile_rows<C>;
     g.Nt = p.dxNt;
     const uint32_t blocks = g.Mt * g.Nt * p.S;
     if (block >= blocks) return;
     const uint32_t q = xcd_chunked(block, blocks), part = q % p.S;
     uint32_t mb, nb;
     tile_at(g, q / p.S, mb, nb);
-    const int m0 = mb * C::BM, n0 = nb * C::BN, slabs = p.vn / BK;
+    const int m0 = mb * tile_rows<C>, n0 = nb * C::BN, slabs = p.vn / BK;
     f32x4 acc[C::FM][C::FN] = {};
     {
         LinTile<C, PASS_FWD> t;
@@ -335,7 +394,7 @@ __device__ __forceinline__ void loss_dw_tile(const LossArgs& p, int n, uint32_t 
 template <class C, int DT>
 __global__ __launch_bounds__(C::NT, C::OCC) void loss_products_kernel(LossArgs p, uint32_t dx_blocks) {
     const int n = packed_rows(p);
-    if (blockIdx.x < dx_blocks) loss_dx_tile<C, DT>(p, n, blockIdx.x);
+    if (blockIdx.x < dx_blocks) with_fragments<C>(n, 1, 0, [&](auto c) { loss_dx_tile<decltype(c), DT>(p, n, blockIdx.x); });
     else loss_dw_tile<C, DT>(p, n, blockIdx.x - dx_blocks);
 }
 

@@ -17,10 +17,17 @@ using Cfg = decltype(this_cfg());
 // and for both products in one launch.
 static constexpr bool HAS_LOGITS = MLPC_LOSS != 7, HAS_PRODUCTS = MLPC_LOSS != 0 && MLPC_LOSS != 7;
 
+// Rows of tiles for any number of rows up to `rows`: tall tiles may be of 160 to
+// 256 rows.
+static uint32_t row_tiles(int64_t rows) {
+    constexpr int least = Cfg::FM == 8 ? 160 : Cfg::BM;
+    return (uint32_t)((rows + least - 1) / least);
+}
+
 template <int DT>
 static hipError_t logits(const LossArgs& a, bool backward, hipStream_t s) {
     if constexpr (HAS_LOGITS) {
-        const dim3 grid(a.Mt * a.Nt);
+        const dim3 grid((a.packing ? row_tiles(a.rows) : a.Mt) * a.Nt);
         return backward ? launch(loss_logits_kernel<Cfg, DT, true>, grid, Cfg::NT, s, a)
                         : launch(loss_logits_kernel<Cfg, DT, false>, grid, Cfg::NT, s, a);
     }
@@ -30,7 +37,7 @@ static hipError_t logits(const LossArgs& a, bool backward, hipStream_t s) {
 template <int DT>
 static hipError_t products(const LossArgs& a, hipStream_t s) {
     if constexpr (HAS_PRODUCTS) {
-        const uint32_t dx = a.dx ? (a.dxMt * a.dxNt * a.S + 7) / 8 * 8 : 0, dw = a.dw ? a.dwMt * a.dwNt : 0;
+        const uint32_t dx = a.dx ? (row_tiles(a.rows) * a.dxNt * a.S + 7) / 8 * 8 : 0, dw = a.dw ? a.dwMt * a.dwNt : 0;
         return launch(loss_products_kernel<Cfg, DT>, dim3(dx + dw), Cfg::NT, s, a, dx);
     }
     return hipErrorInvalidValue;

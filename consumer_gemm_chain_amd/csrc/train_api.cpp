@@ -173,6 +173,7 @@ mlpc::LossArgs loss_args(const mlp_loss* h, int64_t rows, const void* x, int64_t
     a.dz = h->dz;
     a.sums = h->sums;
     a.zero = h->zero;
+    a.cus = (uint32_t)h->cus;
     return a;
 }
 
@@ -292,7 +293,6 @@ int mlp_loss_backward(mlp_loss_t h, int64_t rows, const void* x, int64_t ldx, co
     a.S = 1;
     const int cfg = products_cfg(h, rows > 0 ? rows : 1, width, a.dx != nullptr, a.dw != nullptr, room, &a.S);
     const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
-    a.dxMt = up_div(rows, c.BM);
     a.dxNt = a.dwNt = up_div(h->H, c.BN);
     set_logits(a, cfg_z, 0, width);
     a.packing = a.Mt != 1;

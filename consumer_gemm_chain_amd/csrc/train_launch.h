@@ -53,9 +53,10 @@ struct LossArgs {
     bool direct;            // dx is written by the products, not its sums
     // plan: tiles of the launch's products; dx's reduction in S parts of ksp slabs
     uint32_t Mt, Nt;        // x W^T
-    uint32_t dxMt, dxNt, S, ksp;
+    uint32_t dxNt, S, ksp;
     uint32_t dwMt, dwNt;
     int tiles;              // of the forward pass: Nt
+    uint32_t cus;
 };
 
 // Tables of tensors travel as kernel arguments (at most 4 KB), so a call needs
