@@ -33,7 +33,7 @@ BLOCK_SOURCES = ["block_api.cpp", "linear_dispatch.cpp", "linear_reduce.hip", "n
 LINEAR_KERNELS = "linear_kernels.hip"   # compiled once per configuration of linear_configs.h
 # loss and optimizer (include/mlp_train.h)
 TRAIN_SOURCES = ["train_api.cpp", "loss_dispatch.cpp", "loss_rows.hip", "optim_kernels.hip"]
-LOSS_KERNELS = "loss_kernels.hip"       # compiled once per configuration of linear_configs.h
+LOSS_KERNELS = "loss_kernels.hip"       # compiled once per configuration of loss_configs.h
 
 
 def num_configs(header: str = "chain_configs.h") -> int:
@@ -89,7 +89,7 @@ def build(verbose: bool = False) -> str:
     block = [(src, None, False) for src in BLOCK_SOURCES]
     block += [(LINEAR_KERNELS, c, False) for c in range(num_configs("linear_configs.h"))]
     block += [(src, None, False) for src in TRAIN_SOURCES]
-    block += [(LOSS_KERNELS, c, False) for c in range(num_configs("linear_configs.h"))]
+    block += [(LOSS_KERNELS, c, False) for c in range(num_configs("loss_configs.h"))]
     jobs = kern + chaos + api + block
     workers = min(len(jobs), max(1, min(8, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(max_workers=workers) as ex:

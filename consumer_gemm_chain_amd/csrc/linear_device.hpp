@@ -35,12 +35,13 @@
 
 namespace mlpc {
 
-template <int BM_, int BN_, int WM_, int WN_, int NS_, int KS_, int OCC_>
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int KS_, int OCC_, int EARLY_ = 0>
 struct LinCfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, KS = KS_, OCC = OCC_;
     static constexpr int NW = WM * WN, NT = 64 * NW;
     static constexpr int WTM = BM / WM, WTN = BN / WN;
     static constexpr int FM = WTM / 16, FN = WTN / 16, NF = FM * FN;
+    static constexpr int EARLY = EARLY_;                    // rows of A fragments with registers of their own for the next ones
     static constexpr int HP = KS / 32;                      // 32-deep half steps per stage
     static constexpr int SPS = BK / KS;                     // stages per slab
     static constexpr int A_BYTES = BM * KS * 2, STAGE = A_BYTES + BN * KS * 2, RING = NS * STAGE;
@@ -192,7 +193,9 @@ struct LinFrags {
 // A tile's operands and its reduction.  The next half step's LDS reads go among
 // this one's MFMAs (row-major over the fragments): an A fragment's reads after
 // the last MFMA of its row, when its registers are free, and one B read after
-// each other MFMA; B reads left over follow the block.
+// each other MFMA; B reads left over follow the block.  The last rows' reads
+// would then have no MFMAs left to wait behind: those of the last EARLY rows go
+// among an earlier row's, into registers of their own.
 template <class C, int PASS>
 struct LinTile {
     using A = Operand<C, true, Layout<PASS>::a_kr>;
@@ -204,6 +207,12 @@ struct LinTile {
     __device__ __forceinline__ void read_all(uint32_t so, LinFrags<C>& f) const {
         static_for<0, C::FM * A::READS>([&](auto r) { a.template read<H, decltype(r)::value>(so, f.a); });
         static_for<0, C::FN * B::READS>([&](auto r) { b.template read<H, decltype(r)::value>(so, f.b); });
+    }
+
+    // The reads of A fragment M.
+    template <int H, int M>
+    __device__ __forceinline__ void read_a(uint32_t so, LinFrags<C>& f) const {
+        static_for<0, A::READS>([&](auto r) { a.template read<H, M * A::READS + decltype(r)::value>(so, f.a); });
     }
 
     // DMA instruction Q of LPS of a stage, B's first.
@@ -220,15 +229,17 @@ struct LinTile {
     __device__ __forceinline__ void multiply(f32x4 (&acc)[C::FM][C::FN], const LinFrags<C>& cur, uint32_t so,
                                              LinFrags<C>& nxt, int h, int stage) const {
         constexpr int GAP = C::NF / C::LPS >= 2 ? 2 : 1;
-        constexpr int SLOTS = C::NF - C::FM, NB = C::FN * B::READS;
+        constexpr int SLOTS = C::NF - C::FM, NB = C::FN * B::READS, LATE = C::FM - C::EARLY;
+        static_assert(C::EARLY < C::FN && (C::EARLY == 0 || LATE >= 2), "slots of one row");
         static_for<0, C::NF>([&](auto i) {
             constexpr int I = decltype(i)::value, M = I / C::FN, N = I % C::FN;
             acc[M][N] = mfma16x16x32<DT>(cur.b[N], cur.a[M], acc[M][N]);
             if constexpr (N == C::FN - 1) {
-                static_for<0, A::READS>([&](auto r) { a.template read<H, M * A::READS + decltype(r)::value>(so, nxt.a); });
+                if constexpr (M < LATE) read_a<H, M>(so, nxt);
             } else {
                 constexpr int R = I - M;      // B slots before this one
                 if constexpr (R < NB) b.template read<H, R>(so, nxt.b);
+                if constexpr (M == LATE - 2 && N < C::EARLY) read_a<H, LATE + N>(so, nxt);
             }
             if constexpr (DMA && I % GAP == 0 && I / GAP < C::LPS) issue<I / GAP>(h, stage);
             __builtin_amdgcn_sched_barrier(0);

@@ -1,21 +1,20 @@
 // loss_kernels.hip -- the products of the cross entropy, one object per tile
-// configuration (-DMLPC_LOSS=<id>, linear_configs.h).
+// configuration (-DMLPC_LOSS=<id>, loss_configs.h).
 #include <hip/hip_runtime.h>
 
-#include "linear_configs.h"
+#include "loss_configs.h"
 #include "loss_device.hpp"
 
 namespace mlpc {
 
-#define MLPC_PICK(id, bm, bn, wm, wn, ns, ks, occ) \
-    if constexpr (id == MLPC_LOSS) return LinCfg<bm, bn, wm, wn, ns, ks, occ>{};
-static constexpr auto this_cfg() { MLPC_LINEAR_CONFIGS(MLPC_PICK) }
+#define MLPC_PICK(id, bm, bn, wm, wn, ns, ks, occ, early) \
+    if constexpr (id == MLPC_LOSS) return LinCfg<bm, bn, wm, wn, ns, ks, occ, early>{};
+static constexpr auto this_cfg() { MLPC_LOSS_CONFIGS(MLPC_PICK) }
 #undef MLPC_PICK
 using Cfg = decltype(this_cfg());
 
-// The configurations that the linear layer has for dz W^T, whose layout z has,
-// and for both products in one launch.
-static constexpr bool HAS_LOGITS = MLPC_LOSS != 7, HAS_PRODUCTS = MLPC_LOSS != 0 && MLPC_LOSS != 7;
+// The configurations that the linear layer has for both products in one launch.
+static constexpr bool HAS_PRODUCTS = MLPC_LOSS != 0;
 
 // Rows of tiles for any number of rows up to `rows`: tall tiles may be of 160 to
 // 256 rows.
@@ -26,12 +25,9 @@ static uint32_t row_tiles(int64_t rows) {
 
 template <int DT>
 static hipError_t logits(const LossArgs& a, bool backward, hipStream_t s) {
-    if constexpr (HAS_LOGITS) {
-        const dim3 grid((a.packing ? row_tiles(a.rows) : a.Mt) * a.Nt);
-        return backward ? launch(loss_logits_kernel<Cfg, DT, true>, grid, Cfg::NT, s, a)
-                        : launch(loss_logits_kernel<Cfg, DT, false>, grid, Cfg::NT, s, a);
-    }
-    return hipErrorInvalidValue;
+    const dim3 grid((a.packing ? row_tiles(a.rows) : a.Mt) * a.Nt);
+    return backward ? launch(loss_logits_kernel<Cfg, DT, true>, grid, Cfg::NT, s, a)
+                    : launch(loss_logits_kernel<Cfg, DT, false>, grid, Cfg::NT, s, a);
 }
 
 template <int DT>
