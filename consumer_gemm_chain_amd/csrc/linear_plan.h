@@ -130,8 +130,9 @@ const Rates BOTH = {{0, 0.44, 0.647, 0.799, 1.65, 1.53, 0.547, 0},
 
 // Estimated microseconds of the products `w` of one configuration in one
 // launch, and their partials' way out and back.  Small ones take no less than
-// the host's time for their launches.
-double plan_cost(const Work* w, int products, const Rates& t, int cus) {
+// the host's time for their launches.  A product's multiplications take `part`
+// of what its whole tiles would (the first one's, if its tiles are shorter).
+double plan_cost(const Work* w, int products, const Rates& t, int cus, double part = 1.0) {
     static const int per_cu[] = {2, 2, 1, 1, 1, 1, 3, 2};
     const int cfg = w[0].p.cfg;
     const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
@@ -147,8 +148,9 @@ double plan_cost(const Work* w, int products, const Rates& t, int cus) {
         const Plan& p = w[i].p;
         const double M = (double)w[i].M, N = (double)w[i].N, K = (double)w[i].K, tiles = (double)p.Mt * p.Nt, split = tiles - p.direct;
         const double bytes = 128.0 * ((double)c.BN / p.Mt + (double)c.BM / p.Nt);
-        const double per = fmax(slab, fmax(bytes * active / (t.all * 1e6), bytes / (t.cu * 1e3)));
-        power += tiles * c.BM * c.BN * K * 2e-6 / t.cap[cfg];
+        const double whole = i == 0 ? part : 1.0;
+        const double per = fmax(slab * whole, fmax(bytes * active / (t.all * 1e6), bytes / (t.cu * 1e3)));
+        power += whole * tiles * c.BM * c.BN * K * 2e-6 / t.cap[cfg];
         memory += 2.0 * (M * K + K * N) / (t.read * 1e6) + 2.0 * M * N / (t.write * 1e6);
         if (p.S == 1 || p.direct) {
             group[groups][0] = p.S == 1 ? tiles : p.direct;

@@ -56,34 +56,11 @@ struct Shorter : C {
 template <class C>
 constexpr int tile_rows = C::WM * C::WTM;
 
-// The fragments per wave with which the row tiles of n rows take least, if each
-// row of tiles has `columns` tiles, dealt to `cus` CUs in rounds (0: among other
-// work): 670 rows are three tiles of 224.  A tile costs as much as 1.2 fragments
-// more than its products; half of what a last, partial round wastes comes back
-// as the others' higher clocks (1000 x 12288 x 50001 with a third of the rows
-// left out, z alone: 256 rows per tile 1030 us, 160 rows, which fill the rounds
-// best, 1225, 224 rows 955).
-__device__ __forceinline__ int fragments_for(int n, uint32_t columns, uint32_t cus) {
-    int best = 8;
-    float cost = 0.f;
-#pragma unroll
-    for (int f = 8; f >= 5; --f) {
-        const uint32_t tiles = (uint32_t)((n + 32 * f - 1) / (32 * f)) * columns;
-        const float rounds = cus ? 0.5f * ((float)((tiles + cus - 1) / cus) + (float)tiles / (float)cus) : (float)tiles;
-        const float c = rounds * (f + 1.2f);
-        if (f == 8 || c < cost) {
-            best = f;
-            cost = c;
-        }
-    }
-    return best;
-}
-
 // f(C with the fragments per wave that suit n rows), where tiles are tall.
 template <class C, class F>
 __device__ __forceinline__ void with_fragments(int n, uint32_t columns, uint32_t cus, F&& f) {
     if constexpr (C::FM == 8) {
-        const int k = fragments_for(n, columns, cus);
+        const int k = fragments_for(n, columns, cus).count;
         if (k == 7) return f(Shorter<C, 7>{});
         if (k == 6) return f(Shorter<C, 6>{});
         if (k == 5) return f(Shorter<C, 5>{});

@@ -18,6 +18,12 @@ struct mlp_loss {
     int dtype, device, cus;
     bool grad;
     int forced_cfg[2], forced_split;    // logits, products; -1 / 0: the planner's
+    struct {
+        int64_t rows;                   // that the plan is for (-1: none)
+        int outputs;                    // 1: dx, 2: dw
+        int cfg_z, cfg;
+        uint32_t parts;
+    } forward_plan, plan;
     // workspace (one allocation)
     void* ws;
     void* zero;
@@ -55,7 +61,6 @@ constexpr int64_t MAX_PRODUCT = (int64_t)1 << 38;
 constexpr int PIECE = 256;                              // columns of a piece: a multiple of this
 constexpr int MIN_TILE = 128;                           // columns of the narrowest tile
 
-constexpr double PACK_US = 6.0;                         // packing a few rows, two launches
 
 uint32_t up_div(int64_t a, int64_t b) { return (uint32_t)((a + b - 1) / b); }
 
@@ -91,6 +96,7 @@ mlp_loss_t mlp_loss_create(int64_t max_rows, int64_t H, int64_t V, int dtype, in
     h->device = dev;
     h->grad = grad != 0;
     h->forced_cfg[0] = h->forced_cfg[1] = -1;
+    h->forward_plan.rows = h->plan.rows = -1;
     hipError_t e = hipDeviceGetAttribute(&h->cus, hipDeviceAttributeMultiprocessorCount, dev);
     if (e != hipSuccess) {
         fail(MLP_EHIP, "hipDeviceGetAttribute failed: %s", hipGetErrorString(e));
@@ -186,7 +192,30 @@ void set_logits(mlpc::LossArgs& a, int cfg, int v0, int vn) {
 }
 
 // The products run on tiles that the linear layer has for them, unsplit but for
-// dx, and its estimates choose among these.
+// dx, and its estimates choose among these, with rates fitted to every
+// configuration (and split) of 348 sizes of 1 to 4096 rows.  On 120 sizes drawn
+// afterwards the chosen tiles took 1.2% (z) and 5.5% (the gradient's products)
+// longer than the fastest on average; with the linear layer's own rates 2.7% and
+// 7.0%.
+const Rates LOGITS = {{0.586, 0.787, 0.732, 1.09, 2.2, 0.966, 0.658, 0},
+                      {0.921, 0.845, 1.25, 1.16, 0.904, 1.47, 2.69, 0},
+                      {1.66, 3.06, 5.84, 14.9, 23.8, 12.1, 3.19, 0},
+                      {1140, 1150, 904, 1120, 1230, 1070, 1150, 1},
+                      0.27, 5.49, 4.55, 3.02, 7.23, 2.43, 6.8, 35.8};
+const Rates PRODUCTS = {{0, 0.408, 0.745, 0.799, 1.9, 1.24, 0.605, 0},
+                        {0, 0.902, 0.951, 1.21, 0.799, 0.5, 1.82, 0},
+                        {0, 1.39, 2.78, 7.66, 6.31, 12, 1.6, 0},
+                        {1, 1080, 769, 595, 1210, 1500, 648, 1},
+                        0.383, 2.32, 2.32, 0.428, 8.65, 3.3, 6.45, 107};
+constexpr double PACK_US = 15.5;        // more than one row of tiles: rows are packed first
+
+// What the products of `rows` rows take of whole tiles' time.
+double tall_part(int cfg, int64_t rows, uint32_t columns, int cus) {
+    if (mlpc_linear_config(cfg).BM < 256 || mlpc_linear_config(cfg).BN < 256 || rows <= 256) return 1.0;
+    const mlpc::Fragments f = mlpc::fragments_for((int)rows, columns, (uint32_t)cus);
+    return f.cost / f.whole;
+}
+
 int logits_cfg(const mlp_loss* h, int64_t rows, int64_t vn) {
     if (h->forced_cfg[0] >= 0) return h->forced_cfg[0];
     int best = 0;
@@ -194,8 +223,7 @@ int logits_cfg(const mlp_loss* h, int64_t rows, int64_t vn) {
     for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
         if (!mlpc_linear_has(cfg, mlpc::PASS_DX) || !config_fits(mlpc_linear_config(cfg), rows)) continue;
         const Work w = {make_plan(cfg, rows, vn, h->H, 1, h->cus), rows, vn, h->H};
-        // (more than one row of tiles: the rows are packed first)
-        const double c = plan_cost(&w, 1, SINGLE, h->cus) + (w.p.Mt > 1 ? PACK_US : 0.0);
+        const double c = plan_cost(&w, 1, LOGITS, h->cus, tall_part(cfg, rows, w.p.Nt, h->cus)) + (w.p.Mt > 1 ? PACK_US : 0.0);
         if (cfg == 0 || c < cost) best = cfg, cost = c;
     }
     return best;
@@ -207,9 +235,10 @@ int products_cfg(const mlp_loss* h, int64_t rows, int64_t vn, bool dx, bool dw, 
     int best = 1;
     double cost = 0.0;
     bool found = false;
+    *parts = 1;
     for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
         if (h->forced_cfg[1] >= 0 ? cfg != h->forced_cfg[1]
-                                  : !mlpc_linear_has(cfg, mlpc::PASS_BOTH_DX) || !config_fits(mlpc_linear_config(cfg), rows))
+                                  : !mlpc_linear_has(cfg, mlpc::PASS_BOTH_DX))
             continue;
         uint32_t last = 0;
         for (int64_t S = 1; S <= 32 && S <= room; ++S) {
@@ -219,7 +248,8 @@ int products_cfg(const mlp_loss* h, int64_t rows, int64_t vn, bool dx, bool dw, 
             if (w[0].p.S == last) continue;
             last = w[0].p.S;
             w[0].p.direct = 0;
-            const double c = !dx ? plan_cost(w + 1, 1, BOTH, h->cus) : plan_cost(w, dw ? 2 : 1, BOTH, h->cus);
+            const double c = !dx ? plan_cost(w + 1, 1, PRODUCTS, h->cus)
+                                 : plan_cost(w, dw ? 2 : 1, PRODUCTS, h->cus, tall_part(cfg, rows, 1, 0));
             if (!found || c < cost) best = cfg, cost = c, *parts = (uint32_t)S, found = true;
             if (!dx) break;
         }
@@ -247,7 +277,11 @@ int mlp_loss_forward(mlp_loss_t h, int64_t rows, const void* x, int64_t ldx, con
     mlpc::LossArgs a = loss_args(h, rows, x, ldx, w, ldw, target);
     a.loss = loss;
     a.lse = lse;
-    const int cfg = logits_cfg(h, rows, h->V);
+    if (h->forward_plan.rows != rows) {
+        h->forward_plan.cfg_z = logits_cfg(h, rows, h->V);
+        h->forward_plan.rows = rows;
+    }
+    const int cfg = h->forward_plan.cfg_z;
     set_logits(a, cfg, 0, h->V);
     a.tiles = (int)a.Nt;
     a.packing = a.Mt > 1;
@@ -288,10 +322,16 @@ int mlp_loss_backward(mlp_loss_t h, int64_t rows, const void* x, int64_t ldx, co
     const uint32_t pieces = up_div(h->V, most);
     const int width = (int)(up_div(up_div(h->V, pieces), PIECE) * PIECE);
     a.lddz = width;
-    const int cfg_z = logits_cfg(h, rows > 0 ? rows : 1, width);
-    const int64_t room = rows > 0 ? (int64_t)(h->sum_elems / ((size_t)rows * h->H)) : 1;
-    a.S = 1;
-    const int cfg = products_cfg(h, rows > 0 ? rows : 1, width, a.dx != nullptr, a.dw != nullptr, room, &a.S);
+    const int outputs = (a.dx ? 1 : 0) | (a.dw ? 2 : 0);
+    if (h->plan.rows != rows || h->plan.outputs != outputs) {
+        const int64_t some = rows > 0 ? rows : 1, room = (int64_t)(h->sum_elems / ((size_t)some * h->H));
+        h->plan.cfg_z = logits_cfg(h, some, width);
+        h->plan.cfg = products_cfg(h, some, width, a.dx != nullptr, a.dw != nullptr, room, &h->plan.parts);
+        h->plan.rows = rows;
+        h->plan.outputs = outputs;
+    }
+    const int cfg_z = h->plan.cfg_z, cfg = h->plan.cfg;
+    a.S = h->plan.parts;
     const mlpc::LinearCfgInfo c = mlpc_linear_config(cfg);
     a.dxNt = a.dwNt = up_div(h->H, c.BN);
     set_logits(a, cfg_z, 0, width);
@@ -326,6 +366,7 @@ int mlp_loss_debug_set_plan(mlp_loss_t h, int product, int config_id, int split)
         return fail(MLP_EINVAL, "product %d has no tile configuration %d", product, config_id);
     if (split < 0 || split > 32) return fail(MLP_EINVAL, "the split must be in 0..32, got %d", split);
     h->forced_cfg[product] = config_id;
+    h->forward_plan.rows = h->plan.rows = -1;
     if (product == 1) h->forced_split = split;
     return MLP_OK;
 }

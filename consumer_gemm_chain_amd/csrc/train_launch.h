@@ -18,6 +18,31 @@ struct LossInfo {
     int copied;             // the products' x is the workspace's: packed, or with zeros in the rows left out
 };
 
+// The fragments of 16 rows per wave with which tiles of 32 fragments' rows take
+// n rows in least time, if each row of tiles has `columns` tiles, dealt to `cus`
+// CUs in rounds (0: among other work), and that time in units of a fragment: 670
+// rows are three tiles of 224.  A tile costs as much as 1.2 fragments more than
+// its products; half of what a last, partial round wastes comes back as the
+// others' higher clocks (1000 x 12288 x 50001 with a third of the rows left out,
+// z alone: 256 rows per tile 1030 us, 160 rows, which fill the rounds best, 1225,
+// 224 rows 955).
+struct Fragments {
+    int count;
+    float cost, whole;          // of these, and of 8
+};
+
+__host__ __device__ inline Fragments fragments_for(int n, uint32_t columns, uint32_t cus) {
+    Fragments best{};
+    for (int f = 8; f >= 5; --f) {
+        const uint32_t tiles = (uint32_t)((n + 32 * f - 1) / (32 * f)) * columns;
+        const float rounds = cus ? 0.5f * ((float)((tiles + cus - 1) / cus) + (float)tiles / (float)cus) : (float)tiles;
+        const float c = rounds * (f + 1.2f);
+        if (f == 8) best = Fragments{8, c, c};
+        else if (c < best.cost) best = Fragments{f, c, best.whole};
+    }
+    return best;
+}
+
 struct LossRow {            // of a packed row, for dz
     float lse, a, b;        // dz = a exp(z - lse) - b [v = target], in units
     int target;             // -1: left out
