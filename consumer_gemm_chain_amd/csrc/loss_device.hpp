@@ -42,7 +42,7 @@ __device__ __forceinline__ float wave_max(float v) {
 // (fp16 has few small numbers: 2^14 makes room below)
 template <int DT>
 __device__ __forceinline__ float dz_unit(float top) {
-    return top > 0.f && top < INFINITY ? (DT == DT_F16 ? top * 0x1p-14f : top) : 1.f;
+    return top > 0.f && top < INFINITY ? fmaxf(DT == DT_F16 ? top * 0x1p-14f : top, 0x1p-126f) : 1.f;
 }
 
 // A configuration whose waves multiply F fragments of 16 rows: tiles of 32 F

@@ -75,7 +75,7 @@ mlp_loss_t mlp_loss_create(int64_t max_rows, int64_t H, int64_t V, int dtype, in
              (long long)V);
         return nullptr;
     }
-    // (the largest tiles are 256 x 256 by 512 threads, and a launch has fewer than 2^32 threads)
+    // (with the largest tiles, 256 x 256 by 512 threads, a launch has at most 2^31 threads)
     if (max_rows > MAX_PRODUCT / V || max_rows > MAX_PRODUCT / H || H > MAX_PRODUCT / V) {
         fail(MLP_EINVAL, "max_rows V, max_rows H and H V must be at most 2^38 (got max_rows=%lld H=%lld V=%lld)", (long long)max_rows,
              (long long)H, (long long)V);
@@ -209,6 +209,9 @@ const Rates PRODUCTS = {{0, 0.408, 0.745, 0.799, 1.9, 1.24, 0.605, 0},
                         0.383, 2.32, 2.32, 0.428, 8.65, 3.3, 6.45, 107};
 constexpr double PACK_US = 15.5;        // more than one row of tiles: rows are packed first
 
+// A launch has fewer than 2^32 threads.
+bool launchable(int cfg, int64_t blocks) { return blocks * mlpc_linear_config(cfg).NT < ((int64_t)1 << 32); }
+
 // What the products of `rows` rows take of whole tiles' time.
 double tall_part(int cfg, int64_t rows, uint32_t columns, int cus) {
     if (mlpc_linear_config(cfg).BM < 256 || mlpc_linear_config(cfg).BN < 256 || rows <= 256) return 1.0;
@@ -218,13 +221,15 @@ double tall_part(int cfg, int64_t rows, uint32_t columns, int cus) {
 
 int logits_cfg(const mlp_loss* h, int64_t rows, int64_t vn) {
     if (h->forced_cfg[0] >= 0) return h->forced_cfg[0];
-    int best = 0;
+    int best = 4;
     double cost = 0.0;
+    bool found = false;
     for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
         if (!mlpc_linear_has(cfg, mlpc::PASS_DX) || !config_fits(mlpc_linear_config(cfg), rows)) continue;
         const Work w = {make_plan(cfg, rows, vn, h->H, 1, h->cus), rows, vn, h->H};
+        if (!launchable(cfg, (int64_t)w.p.Mt * w.p.Nt * 2)) continue;
         const double c = plan_cost(&w, 1, LOGITS, h->cus, tall_part(cfg, rows, w.p.Nt, h->cus)) + (w.p.Mt > 1 ? PACK_US : 0.0);
-        if (cfg == 0 || c < cost) best = cfg, cost = c;
+        if (!found || c < cost) best = cfg, cost = c, found = true;
     }
     return best;
 }
@@ -232,14 +237,12 @@ int logits_cfg(const mlp_loss* h, int64_t rows, int64_t vn) {
 // Tile configuration of both products of a piece, and the parts of dx's
 // reduction, at most `room`: dx's tiles have long reductions and may be few.
 int products_cfg(const mlp_loss* h, int64_t rows, int64_t vn, bool dx, bool dw, int64_t room, uint32_t* parts) {
-    int best = 1;
+    int best = 4;
     double cost = 0.0;
     bool found = false;
     *parts = 1;
     for (int cfg = 0; cfg < mlpc_linear_num_configs(); ++cfg) {
-        if (h->forced_cfg[1] >= 0 ? cfg != h->forced_cfg[1]
-                                  : !mlpc_linear_has(cfg, mlpc::PASS_BOTH_DX))
-            continue;
+        if (h->forced_cfg[1] >= 0 ? cfg != h->forced_cfg[1] : !mlpc_linear_has(cfg, mlpc::PASS_BOTH_DX)) continue;
         uint32_t last = 0;
         for (int64_t S = 1; S <= 32 && S <= room; ++S) {
             if (h->forced_split > 0 && S != h->forced_split && S < room) continue;
@@ -247,6 +250,7 @@ int products_cfg(const mlp_loss* h, int64_t rows, int64_t vn, bool dx, bool dw, 
                          {make_plan(cfg, vn, h->H, rows, 1, h->cus), vn, h->H, rows}};
             if (w[0].p.S == last) continue;
             last = w[0].p.S;
+            if (!launchable(cfg, ((int64_t)w[0].p.Mt * w[0].p.Nt * w[0].p.S + (int64_t)w[1].p.Mt * w[1].p.Nt) * 2)) continue;
             w[0].p.direct = 0;
             const double c = !dx ? plan_cost(w + 1, 1, PRODUCTS, h->cus)
                                  : plan_cost(w, dw ? 2 : 1, PRODUCTS, h->cus, tall_part(cfg, rows, 1, 0));

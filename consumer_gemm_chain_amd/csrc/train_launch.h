@@ -84,13 +84,14 @@ struct LossArgs {
     uint32_t cus;
 };
 
-// Tables of tensors travel as kernel arguments (at most 4 KB), so a call needs
+// Tables of tensors travel as kernel arguments (at most 4 KB with the implicit
+// ones), so a call needs
 // no copy and no memory of its own; entry i's chunks begin at first[i].
 constexpr int NORM_CHUNK = 8192;        // elements
 constexpr int NORM_PARTS = 2048;        // workgroups, and partial sums
 
 struct NormTable {
-    static constexpr int MAX = 192;
+    static constexpr int MAX = 184;
     const uint16_t* grad[MAX];
     int64_t n[MAX];
     uint32_t first[MAX];
@@ -141,7 +142,7 @@ struct AdamTable {
     const AdamStep* step;
 };
 
-static_assert(sizeof(NormTable) <= 4096 && sizeof(AdamTable) <= 4096, "kernel arguments");
+static_assert(sizeof(NormTable) <= 3840 && sizeof(AdamTable) <= 3840, "kernel arguments");
 
 }  // namespace mlpc
 

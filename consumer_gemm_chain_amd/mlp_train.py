@@ -219,6 +219,9 @@ class MlpAdamW(_Layer):
         kinds = (f32, f32) if self.states == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
         pointers = _pointers(self, "a parameter", self.params, self.torch_dtype)
         sizes = [p.numel() for p in self.params]
+        some = [p for p in list(pointers)[:n] if p]
+        if len(set(some)) != len(some):
+            raise ValueError("params has the same memory twice (a tied weight is one parameter)")
         blocks = [-(-k // BLOCK) for k in sizes]
 
         def given(name, tensors, dtype, sizes, make):
@@ -242,6 +245,7 @@ class MlpAdamW(_Layer):
         decays = [float(d) for d in decay] if hasattr(decay, "__len__") else [float(decay)] * n
         if len(decays) != n:
             raise ValueError(f"decay has {len(decays)} values, expected {n}")
+        self.decay = decays
         at = lambda p, i: p[i] if p is not None else None  # noqa: E731
         self._table = (AdamwTensor * n)(*[
             AdamwTensor(sizes[i], pointers[i], at(masters, i), ms[i], vs[i], at(m_scales, i), at(v_scales, i), decays[i])

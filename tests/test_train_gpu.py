@@ -200,3 +200,288 @@ def test_loss_backward_single_outputs(rows, H, V, outputs):
 def test_loss_backward_upstream_gradients(rows, H, V, dloss, dlse):
     check_loss_backward(rows, H, V, "f16", dloss=dloss, dlse=dlse)
     check_loss_backward(rows, H, V, "bf16", dloss=dloss, dlse=dlse)
+
+
+# ------------------------------------------------- forced plans, pieces, far apart
+
+@pytest.mark.parametrize("plan", [0, 1, 2, 3, 4, 5, 6])
+@pytest.mark.parametrize("rows,H,V", [(33, 136, 300), (300, 200, 700), (777, 72, 513)])
+def test_loss_forward_with_every_tile(rows, H, V, plan):
+    check_loss_forward(rows, H, V, "bf16", plan=plan)
+
+
+@pytest.mark.parametrize("split", [1, 3, 8])
+@pytest.mark.parametrize("plan", [1, 2, 3, 4, 5, 6])
+def test_loss_backward_with_every_tile(plan, split):
+    for rows, H, V in ((33, 136, 1300), (300, 200, 2100), (777, 72, 513)):
+        check_loss_backward(rows, H, V, "f16", plan=plan, split=split)
+
+
+@pytest.mark.parametrize("rows", [257, 320, 321, 352, 448, 480, 481, 512, 670, 700])
+def test_loss_with_tall_tiles(rows):
+    """Row counts around what tiles of 160 to 256 rows take, all rows counted and some."""
+    for left_out in ("none", "some"):
+        check_loss_forward(rows, 136, 1500, "bf16", left_out, plan=4)
+        check_loss_backward(rows, 136, 1500, "bf16", left_out, plan=4)
+
+
+@pytest.mark.parametrize("rows,H", [(1, 2048), (40, 4096), (200, 2104), (257, 4096)])
+def test_loss_of_long_rows(rows, H):
+    """Reductions that begin at another place for each tile."""
+    for dtype in ("f16", "bf16"):
+        check_loss_forward(rows, H, 1000, dtype)
+        check_loss_backward(rows, H, 1000, dtype)
+
+
+def test_loss_backward_in_pieces():
+    """A vocabulary whose dz does not fit the workspace at once, the last piece ragged."""
+    check_loss_backward(3000, 64, 50001, "bf16")
+
+
+def test_loss_backward_in_many_pieces():
+    """A handle for far more rows than the call has, and one whose pieces are 256 words wide."""
+    check_loss_backward(700, 64, 50001, "f16", most=1 << 16)
+    check_loss_backward(600, 64, 1001, "f16", most=1 << 20)
+
+
+def test_loss_of_a_head_past_2_gb():
+    """Offsets of W and dW past 2^31 bytes."""
+    rows, H, V = 20, 8192, 140000
+    g, n = gen(5)
+    x = n(rows, H).bfloat16()
+    w = torch.empty(V, H, dtype=torch.bfloat16, device="cuda")
+    for v in range(0, V, 20000):
+        w[v:v + 20000].copy_(n(20000, H) * (3 / math.sqrt(H)))
+    target = torch.randint(V - 1000, V, (rows,), generator=g, device="cuda")
+    loss, lse = (torch.empty(rows, device="cuda") for _ in range(2))
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    with MlpLoss(rows, H, V, "bf16") as layer:
+        layer.forward(x, w, target, loss, lse)
+        layer.backward(x, w, target, lse, dx=dx, dw=dw)
+        torch.cuda.synchronize()
+    z = torch.cat([x.double() @ w[v:v + 20000].double().t().contiguous() for v in range(0, V, 20000)], 1)
+    ez = (H / 32 + 64) * E32 * H * float(x.abs().amax()) * float(w.abs().amax()) / 4
+    ref = torch.logsumexp(z, 1)
+    close(lse, ref, ez + 2.0 ** -18 + 2 * E32 * ref.abs(), "lse")
+    dz = torch.exp(z - lse.double()[:, None])
+    dz[torch.arange(rows, device="cuda"), target] -= 1.0
+    for v in range(0, V, 20000):
+        part = dz[:, v:v + 20000]
+        want = part.t().contiguous() @ x.double()
+        size = part.abs().t().contiguous() @ x.double().abs()
+        close(dw[v:v + 20000], want, U["bf16"] * want.abs() + (U["bf16"] + 2.0 ** -16) * size, "dw")
+
+
+# ------------------------------------------------------------- values and rows
+
+def run_loss(x, w, target, dtype, dloss=None, dlse=None, layer=None):
+    rows, V = x.shape[0], w.shape[0]
+    loss, lse = (torch.full((rows,), 7.0, device="cuda") for _ in range(2))
+    dx, dw = torch.full_like(x, 7.0), torch.full_like(w, 7.0)
+    own = layer is None
+    layer = layer or MlpLoss(rows, x.shape[1], V, dtype)
+    layer.forward(x, w, target, loss, lse)
+    layer.backward(x, w, target, lse, dloss, dlse, dx=dx, dw=dw)
+    torch.cuda.synchronize()
+    if own:
+        layer.close()
+    return loss, lse, dx, dw
+
+
+@pytest.mark.parametrize("rows", [5, 300, 700])
+def test_rows_left_out_may_hold_anything(rows):
+    """NaN and infinities in rows that are left out, and a NaN in their dloss, reach nothing."""
+    x, w, target = loss_case(rows, 72, 500, "bf16", 3)
+    target[1] = -5
+    out = target < 0
+    clean = x.clone()
+    clean[out] = 0
+    d = torch.rand(rows, device="cuda")
+    x[out] = math.nan
+    x[out.nonzero()[0]] = math.inf
+    got = run_loss(x, w, target, "bf16", torch.where(out, math.nan, d))
+    want = run_loss(clean, w, target, "bf16", torch.where(out, 0.0, d))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+def test_a_row_that_is_not_finite(rows):
+    """It has a loss and a dx that are not finite, and so has dW; the other rows' are what they would be."""
+    x, w, target = loss_case(rows, 72, 500, "bf16", 4, "none")
+    want = run_loss(x, w, target, "bf16")
+    x[2, 5] = math.nan
+    loss, lse, dx, dw = run_loss(x, w, target, "bf16")
+    others = torch.arange(rows, device="cuda") != 2
+    assert loss[2].isnan() and lse[2].isnan() and dx[2].isnan().all() and dw.isnan().any()
+    assert torch.equal(loss[others], want[0][others]) and torch.equal(lse[others], want[1][others])
+    assert torch.equal(dx[others], want[2][others])
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+def test_targets_outside_the_vocabulary(rows):
+    """Shown as NaN; in the gradient their rows are left out."""
+    x, w, target = loss_case(rows, 72, 500, "f16", 5, "none")
+    wrong = target.clone()
+    wrong[1], wrong[3], wrong[4] = 500, 2 ** 40, 2 ** 31
+    left = torch.where(wrong >= 500, -1, wrong)
+    got, want = run_loss(x, w, wrong, "f16"), run_loss(x, w, left, "f16")
+    outside = wrong >= 500
+    for k in range(2):
+        assert got[k][outside].isnan().all() and torch.equal(got[k][~outside], want[k][~outside])
+    assert torch.equal(got[2], want[2]) and torch.equal(got[3], want[3])
+    low = torch.where(wrong >= 500, -2 ** 62, wrong)
+    for a, b in zip(run_loss(x, w, low, "f16"), want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [6, 300])
+def test_upstream_gradients_of_zero_and_almost_zero(rows, dtype):
+    x, w, target = loss_case(rows, 72, 500, dtype, 6, "none")
+    for value in (0.0, 1e-42, 1e-38, 2.0 ** -126):
+        _, _, dx, dw = run_loss(x, w, target, dtype, torch.full((rows,), value, device="cuda"))
+        assert dx.isfinite().all() and dw.isfinite().all()
+        assert float(dx.abs().max()) <= 2.0 ** -100
+
+
+@pytest.mark.parametrize("rows", [6, 300])
+def test_upstream_gradients_of_very_different_sizes(rows):
+    """bf16 holds each row's dz whatever the others' size."""
+    d = torch.logspace(-30, 0, rows, device="cuda")
+    x, w, target = loss_case(rows, 72, 500, "bf16", 7, "none")
+    _, lse, dx, _ = run_loss(x, w, target, "bf16", d)
+    z, _, _, _ = loss_ref(x, w, target)
+    dz = torch.exp(z - lse.double()[:, None])
+    dz[torch.arange(rows, device="cuda"), target] -= 1.0
+    ref = (dz @ w.double()) * d.double()[:, None]
+    size = (dz.abs() @ w.double().abs()) * d.double()[:, None]
+    close(dx, ref, U["bf16"] * ref.abs() + (U["bf16"] + 2.0 ** -14) * size, "dx")
+
+
+@pytest.mark.parametrize("which", ["dx", "dw"])
+@pytest.mark.parametrize("rows,H,V", [(7, 40, 33), (300, 64, 129)])
+def test_loss_gradient_against_differences(rows, H, V, which):
+    """The directional derivative of sum(a loss + b lse) by central differences in 64 bits."""
+    x, w, target = loss_case(rows, H, V, "f16", 8)
+    _, n = gen(1)
+    a, b = n(rows), n(rows)
+    _, _, dx, dw = run_loss(x, w, target, "f16", a, b)
+    got = {"dx": dx, "dw": dw}[which].double()
+    d = torch.randn(got.shape, generator=torch.Generator("cuda").manual_seed(1), device="cuda", dtype=torch.float64)
+
+    def value(t):
+        _, lse, loss, _ = loss_ref(x.double() + (t * d if which == "dx" else 0), w.double() + (t * d if which == "dw" else 0), target)
+        return (a.double() * loss + b.double() * lse).sum()
+    h = 1e-5
+    diff = float((value(h) - value(-h)) / (2 * h))
+    # roundings of outputs and of dz, each of at most u |g d|, independent: eight times their 2-norm
+    assert abs(float((got * d).sum()) - diff) <= 8 * 2 * U["f16"] * float((got * d).norm()) + 1e-4
+
+
+def test_loss_of_no_rows():
+    w = torch.randn(300, 64, device="cuda").half()
+    dw = torch.full_like(w, 7.0)
+    with MlpLoss(8, 64, 300, "f16") as layer:
+        e = torch.empty(0, 64, dtype=torch.float16, device="cuda")
+        f, t = torch.empty(0, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
+        layer.forward(e, w, t, f, f)
+        layer.backward(e, w, t, f, dx=e, dw=dw)
+        torch.cuda.synchronize()
+    assert (dw == 0).all()
+
+
+# --------------------------------------------------- streams, graphs, repetition
+
+@pytest.mark.parametrize("rows", [20, 300, 700])
+def test_loss_twice_the_same_and_with_fewer_rows(rows):
+    """A handle's calls depend on nothing from earlier ones: other rows, other targets, then the first again."""
+    x, w, target = loss_case(rows, 136, 1003, "bf16", 9)
+    with MlpLoss(rows, 136, 1003, "bf16") as layer:
+        first = run_loss(x, w, target, "bf16", layer=layer)
+        run_loss(x[:rows // 2], w, torch.zeros_like(target[:rows // 2]), "bf16", layer=layer)
+        run_loss(x[:3], w, torch.full_like(target[:3], -1), "bf16", layer=layer)
+        again = run_loss(x, w, target, "bf16", layer=layer)
+    for a, b in zip(first, again):
+        assert torch.equal(a, b)
+
+
+def test_loss_on_two_streams_at_once():
+    """Separate handles on streams of their own."""
+    cases = [loss_case(r, 136, 1003, "bf16", 10 + r) for r in (40, 500)]
+    want = [run_loss(*c, "bf16") for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    layers = [MlpLoss(c[0].shape[0], 136, 1003, "bf16") for c in cases]
+    outs = [[torch.empty(c[0].shape[0], device="cuda") for _ in range(2)] + [torch.empty_like(c[0]), torch.empty_like(c[1])] for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (x, w, t), s, layer, (loss, lse, dx, dw) in zip(cases, streams, layers, outs):
+            with torch.cuda.stream(s):
+                layer.forward(x, w, t, loss, lse)
+                layer.backward(x, w, t, lse, dx=dx, dw=dw)
+    torch.cuda.synchronize()
+    for got, ref in zip(outs, want):
+        for a, b in zip(got, ref):
+            assert torch.equal(a, b)
+    for layer in layers:
+        layer.close()
+
+
+@pytest.mark.parametrize("rows", [20, 700])
+def test_loss_graph_replays(rows):
+    """Captured once, replayed with other inputs and targets, eager work between the replays."""
+    x, w, target = loss_case(rows, 136, 1003, "bf16", 12)
+    loss, lse = (torch.empty(rows, device="cuda") for _ in range(2))
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    with MlpLoss(rows, 136, 1003, "bf16") as layer:
+        def step():
+            layer.forward(x, w, target, loss, lse)
+            layer.backward(x, w, target, lse, dx=dx, dw=dw)
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for k in range(3):
+            x2, w2, t2 = loss_case(rows, 136, 1003, "bf16", 20 + k, ("some", "none", "all")[k])
+            x.copy_(x2), w.copy_(w2), target.copy_(t2)
+            for t in (loss, lse, dx, dw):
+                t.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip((loss, lse, dx, dw), run_loss(x2, w2, t2, "bf16")):
+                assert torch.equal(a, b)
+
+
+def test_loss_refusals_of_tensors():
+    x, w, target = loss_case(6, 64, 100, "f16", 1)
+    loss, lse = (torch.empty(6, device="cuda") for _ in range(2))
+    with MlpLoss(6, 64, 100, "f16", grad=False) as layer:
+        with pytest.raises(ValueError, match="shape"):
+            layer.forward(x[:, :56], w, target, loss, lse)
+        with pytest.raises(ValueError, match="w has shape"):
+            layer.forward(x, w[:50], target, loss, lse)
+        with pytest.raises(ValueError, match="w has shape"):
+            layer.forward(x, w.t(), target, loss, lse)
+        with pytest.raises(ValueError, match="f16"):
+            layer.forward(x.bfloat16(), w, target, loss, lse)
+        with pytest.raises(ValueError, match="int64"):
+            layer.forward(x, w, target.int(), loss, lse)
+        with pytest.raises(ValueError, match="float32"):
+            layer.forward(x, w, target, loss.half(), lse)
+        with pytest.raises(ValueError, match="target must be"):
+            layer.forward(x, w, target[:5], loss, lse)
+        with pytest.raises(ValueError, match="device"):
+            layer.forward(x, w, target.cpu(), loss, lse)
+        with pytest.raises(MlpChainError, match="lse"):
+            layer.forward(x, w, target, loss, None)
+        with pytest.raises(MlpChainError, match="gradient"):
+            layer.backward(x, w, target, lse, dx=torch.empty_like(x))
+        with pytest.raises(MlpChainError, match="aligned"):
+            off = torch.empty(6 * 64 + 8, dtype=torch.float16, device="cuda")[4:6 * 64 + 4].view(6, 64)
+            layer.forward(off, w, target, loss, lse)
+        with pytest.raises(MlpChainError, match="rows"):
+            big = torch.cat([x, x])
+            layer.forward(big, w, torch.cat([target, target]), torch.cat([loss, loss]), torch.cat([lse, lse]))
