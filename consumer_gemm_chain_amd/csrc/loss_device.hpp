@@ -37,12 +37,24 @@ __device__ __forceinline__ float wave_max(float v) {
     return v;
 }
 
-// dz's unit from its largest coefficient: dz is rounded to 16 bits, and where
-// all rows have the same dloss (a mean) the target's -dloss then is exact.
-// (fp16 has few small numbers: 2^14 makes room below)
+// The largest coefficient in a row of dz, for its unit; 0 if it is not finite
+// (whatever the unit, that row's gradients are not, and the other rows' are not
+// to suffer).
+__device__ __forceinline__ float largest_coefficient(float dloss, float dlse) {
+    const float top = fmaxf(fabsf(dloss), fabsf(dloss + dlse));
+    return top < INFINITY ? top : 0.f;
+}
+
+// dz's unit from the call's largest coefficient.  The matrix cores take dz in
+// 16 bits.  Where all rows have the same dloss (a mean), a target of probability
+// p has dz = p - 1 units: exact to within p / 2, so dx of a wide vocabulary is as
+// good as from an unrounded dz.  With few rows and a narrow one that rounding
+// shows beside the outputs' own (one row, 711 words, bf16: relative error 3.0e-3,
+// 1.7e-3 from an unrounded dz).  A second 16-bit term would cure that at twice
+// the products' work.  (fp16 has few small numbers: 2^14 makes room below)
 template <int DT>
 __device__ __forceinline__ float dz_unit(float top) {
-    return top > 0.f && top < INFINITY ? fmaxf(DT == DT_F16 ? top * 0x1p-14f : top, 0x1p-126f) : 1.f;
+    return top > 0.f ? fmaxf(DT == DT_F16 ? top * 0x1p-14f : top, 0x1p-126f) : 1.f;
 }
 
 // A configuration whose waves multiply F fragments of 16 rows: tiles of 32 F
@@ -164,7 +176,7 @@ struct RowsOfTile {
         float* largest = reinterpret_cast<float*>(row + C::BM);                 // [NW]
         const int r = threadIdx.x, lane = r & 63;
         const bool counts = target >= 0 && target < p.V;
-        const float top = wave_max(counts ? fmaxf(fabsf(d), fabsf(d + l)) : 0.f);
+        const float top = wave_max(counts ? largest_coefficient(d, l) : 0.f);
         if (lane == 0) largest[r >> 6] = top;
         const bool out = __syncthreads_or(r < (int)p.rows && !counts);
         float all = largest[0];
@@ -226,7 +238,7 @@ __device__ __forceinline__ void dz_epilogue(const f32x4 (&acc)[C::FM][C::FN], co
 // A tile of z = x W^T.  With one or two rows of tiles, reading W bounds it, and
 // tiles of different words then begin at different places of a long reduction:
 // rows of W whose length is a power of two would otherwise have all workgroups
-// read the same few memory channels at a time (48 x 8192 x 32000 121 -> 97 us,
+// read the same few memory channels at a time (48 x 8192 x 32000 121 -> 95 us,
 // 4.3 -> 5.5 TB/s of W).
 template <class C, int DT, bool GRAD>
 __device__ __forceinline__ void loss_logits_tile(const LossArgs& p, int n, RowsOfTile<C, DT>& rows) {

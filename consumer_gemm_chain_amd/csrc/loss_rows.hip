@@ -25,8 +25,7 @@ __global__ __launch_bounds__(PNT) void loss_pack_kernel(LossArgs a) {
         float top = 0.f;
         for (int64_t r = threadIdx.x; r < a.rows; r += PNT) {
             if (!counts(r)) continue;
-            const float d = a.dloss ? a.dloss[r] : 1.f, l = a.dlse ? a.dlse[r] : 0.f;
-            top = fmaxf(top, fmaxf(fabsf(d), fabsf(d + l)));
+            top = fmaxf(top, largest_coefficient(a.dloss ? a.dloss[r] : 1.f, a.dlse ? a.dlse[r] : 0.f));
         }
         top = wave_max(top);
         if (lane == 0) largest[wave] = top;

@@ -35,8 +35,8 @@
  * per handle; loss, lse and their gradients are fp32.  Sums and softmax are
  * fp32; every output is rounded once (to nearest even).  dz is rounded to the
  * storage type before its two products, whose operands the matrix cores take
- * in 16 bits, in units of the largest |dloss_r| or |dloss_r + dlse_r| of the
- * call (and in fp16 of 2^-14 of it, so that the rest of the vocabulary is not
+ * in 16 bits, in units of the largest finite |dloss_r| or |dloss_r + dlse_r| of
+ * the call (and in fp16 of 2^-14 of it, so that the rest of the vocabulary is not
  * lost: in fp16 dz below 2^-38 of that unit is).  Reductions have a fixed
  * order: the same call gives the same bits.  The gradient norm sums in 64
  * bits.  Outputs that the formulas make depend on a NaN or an infinity are not
@@ -91,7 +91,7 @@ typedef struct mlp_adamw* mlp_adamw_t;
  * positive multiple of 8 and V >= 1, each below 2^22, and no two of the three
  * with a product above 2^38.  The workspace is
  * allocated here: a copy of max_rows rows of x (calls that leave rows out
- * gather the others), 8 bytes per row and 128 words, and if `grad` != 0 the
+ * gather the others), 8 bytes per row and 128 words, 24 bytes per row, and if `grad` != 0 the
  * piece of dz (at most 256 MB, or 256 columns of max_rows rows where that is
  * more) and fp32 sums of dx; a handle without it only runs forward.  Returns
  * NULL on error with mlp_chain_last_error() set. */

@@ -345,6 +345,24 @@ def test_upstream_gradients_of_zero_and_almost_zero(rows, dtype):
         assert float(dx.abs().max()) <= 2.0 ** -100
 
 
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("dtype,value", [("f16", 1e5), ("f16", 2.0 ** -10), ("bf16", 1e5)])
+@pytest.mark.parametrize("rows", [6, 300])
+def test_an_upstream_gradient_that_is_not_finite(rows, dtype, value, bad):
+    """Its row's dx is not finite, nor is dW; the other rows' dx is what it would be: dz's unit is theirs."""
+    x, w, target = loss_case(rows, 72, 500, dtype, 8, "none", spread=0.1)
+    d = torch.full((rows,), value, device="cuda")
+    d[2] = 0.0
+    want = run_loss(x, w, target, dtype, d)[2]
+    others = torch.arange(rows, device="cuda") != 2
+    assert want.isfinite().all() and want[others].any(1).all()
+    zeros = torch.zeros_like(d)
+    for dloss, dlse in ((torch.where(others, d, bad), None), (d, torch.where(others, zeros, bad))):
+        _, _, dx, dw = run_loss(x, w, target, dtype, dloss, dlse)
+        assert not dx[2].isfinite().any() and not dw.isfinite().any()
+        assert torch.equal(dx[others], want[others])
+
+
 @pytest.mark.parametrize("rows", [6, 300])
 def test_upstream_gradients_of_very_different_sizes(rows):
     """bf16 holds each row's dz whatever the others' size."""
