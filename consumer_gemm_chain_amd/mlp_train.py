@@ -154,9 +154,10 @@ class MlpGradNorm(_Layer):
     def forward(self, grads, norm, scale=None, max_norm: float = math.inf, unscale: float = 1.0, stream=None):
         """norm = |unscale| sqrt(sum g^2) over the contiguous tensors `grads`; scale = unscale min(1, max_norm / norm),
         NaN if the norm is not finite (both float32 [1])."""
+        from torch import Tensor
         n = len(grads)
         pointers = _pointers(self, "a gradient", grads, self.torch_dtype)
-        sizes = _array(ctypes.c_int64, "q", map(type(norm).numel, grads), n)
+        sizes = _array(ctypes.c_int64, "q", map(Tensor.numel, grads), n)
         mlp_grad_norm_forward(self.h, n, sizes, pointers, float(unscale), float(max_norm),
                               self._vector("norm", norm, 1, self._f32), self._vector("scale", scale, 1, self._f32),
                               self._stream(stream, norm))
@@ -235,7 +236,7 @@ class MlpAdamW(_Layer):
 
         self.master = self.m_scale = self.v_scale = masters = m_scales = v_scales = None
         if master is not None and master is not False:
-            self.master, masters = given("master", None if master is True else master, f32, sizes, lambda p, k: p.float())
+            self.master, masters = given("master", None if master is True else master, f32, sizes, lambda p, k: p.detach().float())
         self.m, ms = given("m", m, kinds[0], sizes, zeros(kinds[0]))
         self.v, vs = given("v", v, kinds[1], sizes, zeros(kinds[1]))
         if self.states == 8:
@@ -257,6 +258,8 @@ class MlpAdamW(_Layer):
         self._memory = [t.untyped_storage() for ts in lists if ts for t in ts]
         self._params = list(pointers)[:n]
         self._shapes = [p.shape for p in self.params]
+        # (what was made here is there for steps on any stream)
+        torch.cuda.current_stream(self.device).synchronize()
 
     _destroy = staticmethod(mlp_adamw_destroy)
 

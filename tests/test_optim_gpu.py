@@ -445,6 +445,42 @@ def test_optimizers_on_two_streams_at_once():
         opt.close()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_step_on_another_stream_than_the_optimizer_was_made_on(bits):
+    """States and master weights are there when the constructor returns."""
+    n = gen(3)
+    w = [(0.02 * n(k)).half() for k in (1 << 20, 300)]
+    g = [(1e-3 * n(k)).half() for k in (1 << 20, 300)]
+
+    def step(make, run):
+        params = [t.clone() for t in w]
+        slow = n(4096, 4096)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(make):
+            for _ in range(10):
+                slow = slow @ slow
+            opt = MlpAdamW(params, "f16", bits, master=True)
+        with torch.cuda.stream(run):
+            opt.step(g, 1e-3)
+        torch.cuda.synchronize()
+        state = opt.params + opt.master + opt.m + opt.v + (opt.m_scale or []) + (opt.v_scale or []) + [opt.t]
+        opt.close()
+        return [t.view(torch.uint8) for t in state]
+    here, there = torch.cuda.Stream(), torch.cuda.Stream()
+    for a, b in zip(step(here, there), step(here, here)):
+        assert torch.equal(a, b)
+
+
+def test_parameters_that_require_gradients():
+    """Master weights are plain tensors, not part of a graph."""
+    w = torch.nn.Parameter(torch.randn(300, device="cuda").half())
+    with MlpAdamW([w], "f16", master=True) as opt:
+        assert not opt.master[0].requires_grad
+        opt.step([torch.ones_like(w)], 1e-2)
+        torch.cuda.synchronize()
+        assert torch.equal(opt.master[0].half(), w.detach())
+
+
 def test_tensors_of_any_shape():
     n = gen(6)
     w = n(30, 17).half()
