@@ -58,10 +58,16 @@ __device__ __forceinline__ float dz_unit(float top) {
 }
 
 // A configuration whose waves multiply F fragments of 16 rows: tiles of 32 F
-// rows.  The DMA still brings BM rows.
+// rows.  Each wave requests as many rows as the others, so the DMA brings 192
+// rows for 5 and 6 fragments and 256 for 7 (8192 -> 32000 bf16 on 160- and
+// 192-row tiles, with 256 rows for all of them against this: 320 rows z 223 ->
+// 214 us, gradient 715 -> 692; 384 rows 234 -> 225, 735 -> 713; 1100 rows 584 ->
+// 559, 1627 -> 1602.  With one line requested for all of the last 32 rows of 7
+// fragments: no difference).
 template <class C, int F>
 struct Shorter : C {
     static constexpr int FM = F, NF = F * C::FN, WTM = 16 * F;
+    static constexpr int A_PER_WAVE = (32 * F * C::KS / 512 + C::NW - 1) / C::NW, LPS = A_PER_WAVE + C::B_PER_WAVE;
 };
 
 // Rows of a tile.

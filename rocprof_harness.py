@@ -5,6 +5,7 @@ text summaries.
     python rocprof_harness.py [--workload 1] [--M 2048] [--policy tile_sync]
                               [--raw-dir gpurun_out/prof] [--summary-dir profiles]
     python rocprof_harness.py --block      # the block operators instead: the cases of perf/operators.py
+    python rocprof_harness.py --train      # the training step's operators: the cases of perf/more_operators.py
 
 Each measurement is its own profiler run of `bench.py --kernels-only` (the
 headline policy's persistent kernel and the planned stream-ordered pair,
@@ -22,9 +23,10 @@ Matrix-core utilisation and HBM bytes per second follow from the counters and
 the profiled durations; at small M (weight streaming) the GB/s figure is the
 one that matters, at large M the matrix-core one.
 
-With --block the profiled program is this file with --block-cases, which runs
-every listed case of perf/operators.py through the package; one table of all
-of these measurements goes to <summary-dir>/block_kernels.md.
+With --block (or --train) the profiled program is this file with --block-cases
+(--train-cases), which runs every listed case of perf/operators.py
+(perf/more_operators.py) through the package; one table of all of these
+measurements goes to <summary-dir>/block_kernels.md (train_kernels.md).
 
 The harness itself never touches the GPU: it only starts the profiler runs
 as child processes and parses their CSV output.
@@ -99,22 +101,34 @@ def _chain_rows(disp):
 
 
 BLOCK_PASSES = 21     # per case, over three sets of inputs in turn
+CASES = {"block": "operators.py", "train": "more_operators.py"}
+TITLES = {"block": "Block operators", "train": "The training step's operators"}
+NOTES = {
+    "block": """`linear<BM, BN, waves M, waves N, stages, stage depth, waves per SIMD, type (0 fp16, 1 bf16), pass (0 x W, 1 dz W^T,
+2 x^T dz)>`; `linear_both<...>`: dz W^T and x^T dz in one launch; `norm_forward<type, threads per row, chunks, ragged>`,
+`norm_backward<type, threads, chunks, ragged, single workgroup>`; `dz<type, activation, columns>`.
+""",
+    "train": """`loss_logits<BM, BN, waves M, waves N, stages, stage depth, waves per SIMD, fragments read early, type (0 fp16, 1 bf16),
+gradient>`: z = x W^T with a softmax's maxima and sums, or as dz; `loss_products<...>`: dz W and dz^T x in one launch;
+`loss_pack<gradient, type>`, `loss_gather`: the rows that count; `loss_join`: loss and lse; `loss_dx<type>`: dx from its sums;
+`adamw<type, bits>` per table of up to 48 tensors, `norm_sum<type>` per table of up to 184.
+"""}
 
 
-def block_operators():
+def block_operators(kind="block"):
     import importlib.util
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", CASES[kind]))
     ops = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(ops)
     ops.own = True
     return ops
 
 
-def run_block_cases():
+def run_block_cases(kind="block"):
     """The profiled program: the passes of each case one after another; inputs
     are made between the cases, by kernels that are not the package's."""
     import torch
-    ops = block_operators()
+    ops = block_operators(kind)
     for case in ops.listed():
         states = [ops.prepare(case, seed) for seed in range(3)]
         torch.cuda.synchronize()
@@ -145,13 +159,13 @@ def _by_case(dispatches):
     return groups
 
 
-def profile_block(args):
-    raw = os.path.join(args.raw_dir, "block")
+def profile_block(args, kind="block"):
+    raw = os.path.join(args.raw_dir, kind)
     os.makedirs(raw, exist_ok=True)
     os.makedirs(args.summary_dir, exist_ok=True)
     py = sys.executable or "python3"
     copy = [py, "bench.py", "--copy-mib", str(COPY_MIB)]
-    cases = [py, "rocprof_harness.py", "--block-cases"]
+    cases = [py, "rocprof_harness.py", f"--{kind}-cases"]
     mfma = ["SQ_VALU_MFMA_BUSY_CYCLES", "SQ_BUSY_CU_CYCLES", "GRBM_GUI_ACTIVE", "SQ_LDS_BANK_CONFLICT"]
     runs = {"kt": (["--kernel-trace"], cases), "mfma": (["--pmc", *mfma], cases), "fetch": (["--pmc", "FETCH_SIZE"], cases),
             "write": (["--pmc", "WRITE_SIZE"], cases), "cfetch": (["--pmc", "FETCH_SIZE"], copy),
@@ -172,7 +186,7 @@ def profile_block(args):
     for n, counter in (("cfetch", "FETCH_SIZE"), ("cwrite", "WRITE_SIZE")):
         factor[counter] = COPY_MIB * 1024 / statistics.mean(d[3][counter] for d in count[n] if "copyBuffer" in d[0])
     mf, fetch, write = (_by_case(count[n]) for n in ("mfma", "fetch", "write"))
-    names = [c["name"] for c in block_operators().listed()]
+    names = [c["name"] for c in block_operators(kind).listed()]
     rows = []
     for key, ts in times.items():
         us = statistics.median(t for t, in ts)
@@ -185,35 +199,34 @@ def profile_block(args):
         rows.append(f"| {names[key[0]]} | {key[1]} | {key[2]} | {us:.1f} | {f'{busy:.2f}' if busy >= 0.005 else '-'} | {cu:.2f} | "
                     f"{f'{ghz:.2f}' if us > 100 else '-'} | {of('SQ_LDS_BANK_CONFLICT') / of('SQ_BUSY_CU_CYCLES'):.3f} | "
                     f"{mb[0]:.1f} | {mb[1]:.1f} | {sum(mb) / us:.2f} |")
-    with open(os.path.join(args.summary_dir, "block_kernels.md"), "w") as fh:
-        fh.write(f"""# Block operators: kernels of the listed cases, one MI355X
+    with open(os.path.join(args.summary_dir, f"{kind}_kernels.md"), "w") as fh:
+        fh.write(f"""# {TITLES[kind]}: kernels of the listed cases, one MI355X
 
-    python rocprof_harness.py --block
-      -> rocprofv3 --kernel-trace -- rocprof_harness.py --block-cases
-      -> rocprofv3 --pmc {' '.join(mfma)} -- rocprof_harness.py --block-cases
-      -> rocprofv3 --pmc FETCH_SIZE (then WRITE_SIZE) -- rocprof_harness.py --block-cases
+    python rocprof_harness.py --{kind}
+      -> rocprofv3 --kernel-trace -- rocprof_harness.py --{kind}-cases
+      -> rocprofv3 --pmc {' '.join(mfma)} -- rocprof_harness.py --{kind}-cases
+      -> rocprofv3 --pmc FETCH_SIZE (then WRITE_SIZE) -- rocprof_harness.py --{kind}-cases
       -> rocprofv3 --pmc FETCH_SIZE (then WRITE_SIZE) -- bench.py --copy-mib {COPY_MIB}
 
-Every listed case of perf/operators.py, {BLOCK_PASSES} passes over three sets of inputs in turn; medians per (case, kernel,
+Every listed case of perf/{CASES[kind]}, {BLOCK_PASSES} passes over three sets of inputs in turn; medians per (case, kernel,
 workgroups). The profiled runs of the large products are up to 15% slower than unprofiled ones (the clock).
 
 cycles = GRBM_GUI_ACTIVE / {XCDS}, GHz = cycles / duration (kernels of more than 100 us), MFMA busy =
 SQ_VALU_MFMA_BUSY_CYCLES / ({SIMDS} SIMDs x cycles), CU busy = SQ_BUSY_CU_CYCLES / ({CUS} x cycles). MB read and written =
 FETCH_SIZE x {factor['FETCH_SIZE']:.3f} and WRITE_SIZE x {factor['WRITE_SIZE']:.3f} (calibrated on the copy), across the L2 boundary, the Infinity Cache included.
-`linear<BM, BN, waves M, waves N, stages, stage depth, waves per SIMD, type (0 fp16, 1 bf16), pass (0 x W, 1 dz W^T,
-2 x^T dz)>`; `linear_both<...>`: dz W^T and x^T dz in one launch; `norm_forward<type, threads per row, chunks, ragged>`,
-`norm_backward<type, threads, chunks, ragged, single workgroup>`; `dz<type, activation, columns>`.
-
+{NOTES[kind]}
 | case | kernel | workgroups | us | MFMA busy | CU busy | GHz | LDS conflict cycles / CU busy | MB read | MB written | TB/s |
 |---|---|---|---|---|---|---|---|---|---|---|
 """ + "\n".join(rows) + "\n")
-    print(f"summary written to {args.summary_dir}/block_kernels.md", flush=True)
+    print(f"summary written to {args.summary_dir}/{kind}_kernels.md", flush=True)
 
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--block", action="store_true")
     ap.add_argument("--block-cases", action="store_true", help="the program that --block profiles")
+    ap.add_argument("--train", action="store_true")
+    ap.add_argument("--train-cases", action="store_true", help="the program that --train profiles")
     ap.add_argument("--workload", type=int, default=1)
     ap.add_argument("--M", type=int, default=2048)
     ap.add_argument("--policy", default="tile_sync")
@@ -224,6 +237,10 @@ def main():
         return run_block_cases()
     if args.block:
         return profile_block(args)
+    if args.train_cases:
+        return run_block_cases("train")
+    if args.train:
+        return profile_block(args, "train")
 
     from consumer_gemm_chain_amd import gen
     import bench
