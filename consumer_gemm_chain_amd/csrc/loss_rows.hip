@@ -109,9 +109,10 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a) {
         }
     }
     if (lane != 0) return;
-    const float lse = m + logf(s);
-    a.lse[r] = lse;
-    if (a.loss) a.loss[r] = lse - a.picked[at];
+    // (the loss is not taken from the rounded lse: a confident row's is far smaller)
+    const float rest = logf(s);
+    a.lse[r] = m + rest;
+    if (a.loss) a.loss[r] = rest + (m - a.picked[at]);
 }
 
 // dx = unit (sum of the parts), rows that are left out 0.

@@ -120,6 +120,23 @@ def test_loss_forward_of_flat_and_peaked_rows(spread):
     check_loss_forward(300, 128, 1003, "bf16", spread=spread)
 
 
+@pytest.mark.parametrize("rows", [5, 300])
+def test_the_loss_of_a_confident_row_does_not_suffer_from_the_size_of_its_logits(rows):
+    """Logits are exact here: 1000 at the target, 992 elsewhere, so loss = log(1 + 199 e^-8), of which fp32 sums near one
+    (at most 32 roundings of 2^-24) and 2^x (2^-20 of the other terms' sum) leave 2e-6; half a step of lse is 3e-5."""
+    at = torch.arange(rows, device="cuda") % 8
+    x = torch.nn.functional.one_hot(at, 8).bfloat16()
+    w = torch.full((200, 8), 992.0, device="cuda").bfloat16()
+    w[torch.arange(8) * 3, torch.arange(8)] = 1000.0
+    loss, lse = (torch.empty(rows, device="cuda") for _ in range(2))
+    with MlpLoss(rows, 8, 200, "bf16", grad=False) as layer:
+        layer.forward(x, w, at * 3, loss, lse)
+        torch.cuda.synchronize()
+    want = math.log1p(199 * math.exp(-8.0))
+    assert float((loss.double() - want).abs().max()) <= 2e-6
+    assert float((lse.double() - 1000 - want).abs().max()) <= 2.0 ** -14
+
+
 def check_loss_backward(rows, H, V, dtype, left_out="some", pad=0, seed=2, dloss="mean", dlse=False, outputs="xw", plan=None,
                         split=0, most=None):
     x, w, target = loss_case(rows, H, V, dtype, seed, left_out)
