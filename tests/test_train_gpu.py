@@ -221,6 +221,20 @@ def test_loss_backward_upstream_gradients(rows, H, V, dloss, dlse):
 
 # ------------------------------------------------- forced plans, pieces, far apart
 
+@pytest.mark.parametrize("rows,H,V", [(9, 64, 100), (300, 72, 777)])
+def test_loss_backward_of_the_lse_alone_and_ones(rows, H, V):
+    check_loss_backward(rows, H, V, "bf16", dloss=None, dlse=True)
+    check_loss_backward(rows, H, V, "f16", dloss=None, dlse=True)
+
+
+@pytest.mark.parametrize("left_out", ["some", "none", "all"])
+@pytest.mark.parametrize("rows", [4095, 4096, 4097, 9001])
+def test_loss_of_many_rows(rows, left_out):
+    """Rows are packed a thousand at a time."""
+    check_loss_forward(rows, 16, 100, "bf16", left_out)
+    check_loss_backward(rows, 16, 100, "bf16", left_out, dloss="any", dlse=True)
+
+
 @pytest.mark.parametrize("plan", [0, 1, 2, 3, 4, 5, 6])
 @pytest.mark.parametrize("rows,H,V", [(33, 136, 300), (300, 200, 700), (777, 72, 513)])
 def test_loss_forward_with_every_tile(rows, H, V, plan):
