@@ -325,7 +325,7 @@ __device__ __forceinline__ void store_scaled(const f32x4 (&acc)[C::FM][C::FN], u
 
 // A part of a tile of dz W: added to the sums of the pieces before.
 template <class C, int DT>
-__device__ __forceinline__ void loss_dx_tile(const LossArgs& p, int n, uint32_t block) {
+__device__ __forceinline__ void loss_dx_tile(const LossArgs& p, const LossInfo& info, int n, uint32_t block) {
     GemmArgs g{};
     g.a = p.dz;
     g.lda = p.lddz;
@@ -351,7 +351,7 @@ __device__ __forceinline__ void loss_dx_tile(const LossArgs& p, int n, uint32_t 
     }
     const int lane = threadIdx.x & 63, wave = uniform_wave();
     if (p.direct) {
-        store_scaled<C, DT>(acc, p.dx, p.lddx, m0, n, n0, p.H, p.info->unit, p.place);
+        store_scaled<C, DT>(acc, p.dx, p.lddx, m0, n, n0, p.H, info.unit, p.place);
         return;
     }
     const int row = m0 + wave / C::WN * C::WTM + (lane & 15), col = n0 + wave % C::WN * C::WTN + (lane >> 4) * 4;
@@ -371,11 +371,11 @@ __device__ __forceinline__ void loss_dx_tile(const LossArgs& p, int n, uint32_t 
 
 // A tile of dz^T x.
 template <class C, int DT>
-__device__ __forceinline__ void loss_dw_tile(const LossArgs& p, int n, uint32_t block) {
+__device__ __forceinline__ void loss_dw_tile(const LossArgs& p, const LossInfo& info, int n, uint32_t block) {
     GemmArgs g{};
     g.a = p.dz;
     g.lda = p.lddz;
-    g.b = packed_x(p, __builtin_amdgcn_readfirstlane(p.info->copied), g.ldb);
+    g.b = packed_x(p, info.copied, g.ldb);
     g.K = n;
     g.zero = p.zero;
     g.Mt = p.dwMt;
@@ -390,7 +390,7 @@ __device__ __forceinline__ void loss_dw_tile(const LossArgs& p, int n, uint32_t 
         t.b.init(g.b, g.ldb, n0, p.H, 0);
         loss_reduce<C, DT>(acc, t, g, 0, n / BK, true);
     }
-    store_scaled<C, DT>(acc, p.dw + (size_t)p.v0 * p.lddw, p.lddw, m0, p.vn, n0, p.H, p.info->unit, nullptr);
+    store_scaled<C, DT>(acc, p.dw + (size_t)p.v0 * p.lddw, p.lddw, m0, p.vn, n0, p.H, info.unit, nullptr);
 }
 
 // Both products of a piece: the first dx_blocks workgroups (a multiple of 8,
@@ -401,14 +401,21 @@ __device__ __forceinline__ void loss_dw_tile(const LossArgs& p, int n, uint32_t 
 // busy at 1.81 GHz); 667 x 12288 x 50001 reaches 0.96 PFLOP/s: dW's tiles
 // have ten slabs each between filling the ring and storing 128 KB.
 // With a few rows W's second reading and dW's writing bound it (48 x 8192 x 32000:
-// 290 us for 1.05 GB; a kernel of its own for dW of up to 128 rows, x in registers
+// 262 us for 1.05 GB; a kernel of its own for dW of up to 128 rows, x in registers
 // and dz turned around in LDS, took 251 instead of 327 us for a call without dx,
-// but 392 instead of 387 with it, and small ones a launch more: dropped).
+// but 392 with it, and small ones a launch more: dropped).
 template <class C, int DT>
 __global__ __launch_bounds__(C::NT, C::OCC) void loss_products_kernel(LossArgs p, uint32_t dx_blocks) {
-    const int n = packed_rows(p);
-    if (blockIdx.x < dx_blocks) with_fragments<C>(n, 1, 0, [&](auto c) { loss_dx_tile<decltype(c), DT>(p, n, blockIdx.x); });
-    else loss_dw_tile<C, DT>(p, n, blockIdx.x - dx_blocks);
+    // Loaded once, ahead: a tile that asks for the unit before its stores waits for
+    // it (48 x 8192 x 32000 389 -> 357 us, 1 row 367 -> 318, 667 x 12288 x 50001
+    // 2647 -> 2602; dW alone of 48 x 8192 x 32000 324 -> 332, of other sizes 2 to 6%
+    // less).
+    const LossInfo info = {__builtin_amdgcn_readfirstlane(p.info->n),
+                           __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, p.info->unit))),
+                           __builtin_amdgcn_readfirstlane(p.info->copied)};
+    const int n = p.packing ? info.n : (int)p.rows;
+    if (blockIdx.x < dx_blocks) with_fragments<C>(n, 1, 0, [&](auto c) { loss_dx_tile<decltype(c), DT>(p, info, n, blockIdx.x); });
+    else loss_dw_tile<C, DT>(p, info, n, blockIdx.x - dx_blocks);
 }
 
 }  // namespace mlpc
