@@ -193,10 +193,11 @@ void set_logits(mlpc::LossArgs& a, int cfg, int v0, int vn) {
 
 // The products run on tiles that the linear layer has for them, unsplit but for
 // dx, and its estimates choose among these, with rates fitted to every
-// configuration (and split) of 348 sizes of 1 to 4096 rows.  On 120 sizes drawn
-// afterwards the chosen tiles took 1.2% (z) and 5.5% (the gradient's products)
-// longer than the fastest on average; with the linear layer's own rates 2.7% and
-// 7.0%.
+// configuration (and split) of 348 sizes (470 for dW alone) of 1 to 4096 rows.  On
+// 120 sizes drawn afterwards (dW, dx alone: 580) the chosen tiles took 1.2% (z),
+// 5.5% (both products), 4.1% (dx alone) and 1.7% (dW alone; 4.5% with both
+// products' rates, 48 x 8192 x 32000 330 -> 245 us) longer than the fastest on
+// average; with the linear layer's own rates z 2.7% and both products 7.0%.
 const Rates LOGITS = {{0.586, 0.787, 0.732, 1.09, 2.2, 0.966, 0.658, 0},
                       {0.921, 0.845, 1.25, 1.16, 0.904, 1.47, 2.69, 0},
                       {1.66, 3.06, 5.84, 14.9, 23.8, 12.1, 3.19, 0},
@@ -207,6 +208,11 @@ const Rates PRODUCTS = {{0, 0.408, 0.745, 0.799, 1.9, 1.24, 0.605, 0},
                         {0, 1.39, 2.78, 7.66, 6.31, 12, 1.6, 0},
                         {1, 1080, 769, 595, 1210, 1500, 648, 1},
                         0.383, 2.32, 2.32, 0.428, 8.65, 3.3, 6.45, 107};
+const Rates DW_ALONE = {{0, 0.624, 0.71, 0.596, 1.74, 1.08, 0.627, 0},
+                        {0, 0.588, 0.608, 1.93, 1.14, 1, 1.85, 0},
+                        {0, 1.04, 10.3, 11.8, 10.8, 11.1, 1.33, 0},
+                        {1, 1080, 769, 687, 1210, 1500, 527, 1},
+                        0.293, 4.33, 3.2, 1.45, 3.37, 4.52, 5.35, 106};
 constexpr double PACK_US = 15.5;        // more than one row of tiles: rows are packed first
 
 // A launch has fewer than 2^32 threads.
@@ -252,7 +258,7 @@ int products_cfg(const mlp_loss* h, int64_t rows, int64_t vn, bool dx, bool dw, 
             last = w[0].p.S;
             if (!launchable(cfg, ((int64_t)w[0].p.Mt * w[0].p.Nt * w[0].p.S + (int64_t)w[1].p.Mt * w[1].p.Nt) * 2)) continue;
             w[0].p.direct = 0;
-            const double c = !dx ? plan_cost(w + 1, 1, PRODUCTS, h->cus)
+            const double c = !dx ? plan_cost(w + 1, 1, DW_ALONE, h->cus)
                                  : plan_cost(w, dw ? 2 : 1, PRODUCTS, h->cus, tall_part(cfg, rows, 1, 0));
             if (!found || c < cost) best = cfg, cost = c, *parts = (uint32_t)S, found = true;
             if (!dx) break;
