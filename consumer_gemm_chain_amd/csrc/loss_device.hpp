@@ -74,17 +74,33 @@ struct Shorter : C {
 template <class C>
 constexpr int tile_rows = C::WM * C::WTM;
 
-// f(C with the fragments per wave that suit n rows), where tiles are tall.
-template <class C, class F>
-__device__ __forceinline__ void with_fragments(int n, uint32_t columns, uint32_t cus, F&& f) {
-    if constexpr (C::FM == 8) {
-        const int k = fragments_for(n, columns, cus).count;
-        if (k == 7) return f(Shorter<C, 7>{});
-        if (k == 6) return f(Shorter<C, 6>{});
-        if (k == 5) return f(Shorter<C, 5>{});
+// Rows of tiles of n rows.
+template <class C>
+struct RowTiles {
+    static constexpr bool TALL = C::FM == 8;
+    Fragments fragments;
+    uint32_t Mt;
+
+    __device__ __forceinline__ RowTiles(int n, uint32_t columns, uint32_t cus) {
+        if constexpr (TALL) fragments = fragments_for(n, columns, cus);
+        Mt = TALL ? fragments.tiles : (n + C::BM - 1) / C::BM;
     }
-    f(C{});
-}
+
+    // f(C with the fragments of row mb, its first row).
+    template <class F>
+    __device__ __forceinline__ void take(uint32_t mb, F&& f) const {
+        if constexpr (TALL) {
+            const int extra = min((int)mb, fragments.extra), k = fragments.base + ((int)mb < fragments.extra ? 1 : 0);
+            const int m0 = 32 * ((int)mb * fragments.base + extra);
+            if (k == 7) return f(Shorter<C, 7>{}, m0);
+            if (k == 6) return f(Shorter<C, 6>{}, m0);
+            if (k == 5) return f(Shorter<C, 5>{}, m0);
+            f(C{}, m0);
+        } else {
+            f(C{}, (int)mb * C::BM);
+        }
+    }
+};
 
 // The reduction of a tile: stages k0 .. k1 of `slabs` whole slabs and the one
 // that ends past K, for the last part.
@@ -247,19 +263,9 @@ __device__ __forceinline__ void dz_epilogue(const f32x4 (&acc)[C::FM][C::FN], co
 // read the same few memory channels at a time (48 x 8192 x 32000 121 -> 95 us,
 // 4.3 -> 5.5 TB/s of W).
 template <class C, int DT, bool GRAD>
-__device__ __forceinline__ void loss_logits_tile(const LossArgs& p, int n, RowsOfTile<C, DT>& rows) {
-    GemmArgs g{};
-    g.a = packed_x(p, p.packing && n < (int)p.rows, g.lda);
-    g.b = p.w + (size_t)p.v0 * p.ldw;
-    g.ldb = p.ldw;
-    g.K = p.H;
-    g.zero = p.zero;
-    g.Mt = (n + tile_rows<C> - 1) / tile_rows<C>;
-    g.Nt = p.Nt;
-    if (blockIdx.x >= g.Mt * g.Nt) return;
-    uint32_t mb, nb;
-    tile_at(g, xcd_chunked(blockIdx.x, g.Mt * g.Nt), mb, nb);
-    const int m0 = mb * tile_rows<C>, n0 = nb * C::BN;
+__device__ __forceinline__ void loss_logits_tile(const LossArgs& p, const GemmArgs& g, int n, int m0, uint32_t nb,
+                                                 RowsOfTile<C, DT>& rows) {
+    const int n0 = nb * C::BN;
     f32x4 acc[C::FM][C::FN] = {};
     LinTile<C, PASS_DX> t;
     t.a.init(g.a, g.lda, m0, n, 0);
@@ -288,16 +294,29 @@ __device__ __forceinline__ void loss_logits_tile(const LossArgs& p, int n, RowsO
 template <class C, int DT, bool GRAD>
 __global__ __launch_bounds__(C::NT, C::OCC) void loss_logits_kernel(LossArgs p) {
     const int n = packed_rows(p);
+    GemmArgs g{};
+    g.a = packed_x(p, p.packing && n < (int)p.rows, g.lda);
+    g.b = p.w + (size_t)p.v0 * p.ldw;
+    g.ldb = p.ldw;
+    g.K = p.H;
+    g.zero = p.zero;
+    g.Nt = p.Nt;
     if (p.packing) {
-        with_fragments<C>(n, p.Nt, p.cus, [&](auto c) {
+        const RowTiles<C> rows(n, p.Nt, p.cus);
+        g.Mt = rows.Mt;
+        if (blockIdx.x >= g.Mt * g.Nt) return;
+        uint32_t mb, nb;
+        tile_at(g, xcd_chunked(blockIdx.x, g.Mt * g.Nt), mb, nb);
+        rows.take(mb, [&](auto c, int m0) {
             RowsOfTile<decltype(c), DT> none;
-            loss_logits_tile<decltype(c), DT, GRAD>(p, n, none);
+            loss_logits_tile<decltype(c), DT, GRAD>(p, g, n, m0, nb, none);
         });
         return;
     }
+    g.Mt = 1;
     RowsOfTile<C, DT> rows;
     if (GRAD) rows.load(p);
-    loss_logits_tile<C, DT, GRAD>(p, n, rows);
+    loss_logits_tile<C, DT, GRAD>(p, g, n, 0, xcd_chunked(blockIdx.x, g.Nt), rows);
 }
 
 // The tile's rows below `rows` and columns below `cols`, times `unit`, rounded;
@@ -325,22 +344,9 @@ __device__ __forceinline__ void store_scaled(const f32x4 (&acc)[C::FM][C::FN], u
 
 // A part of a tile of dz W: added to the sums of the pieces before.
 template <class C, int DT>
-__device__ __forceinline__ void loss_dx_tile(const LossArgs& p, const LossInfo& info, int n, uint32_t block) {
-    GemmArgs g{};
-    g.a = p.dz;
-    g.lda = p.lddz;
-    g.b = p.w + (size_t)p.v0 * p.ldw;
-    g.ldb = p.ldw;
-    g.K = p.vn;
-    g.zero = p.zero;
-    g.Mt = (n + tile_rows<C> - 1) / tile_rows<C>;
-    g.Nt = p.dxNt;
-    const uint32_t blocks = g.Mt * g.Nt * p.S;
-    if (block >= blocks) return;
-    const uint32_t q = xcd_chunked(block, blocks), part = q % p.S;
-    uint32_t mb, nb;
-    tile_at(g, q / p.S, mb, nb);
-    const int m0 = mb * tile_rows<C>, n0 = nb * C::BN, slabs = p.vn / BK;
+__device__ __forceinline__ void loss_dx_tile(const LossArgs& p, const LossInfo& info, const GemmArgs& g, int n, int m0, uint32_t nb,
+                                             uint32_t part) {
+    const int n0 = nb * C::BN, slabs = p.vn / BK;
     f32x4 acc[C::FM][C::FN] = {};
     {
         LinTile<C, PASS_FWD> t;
@@ -414,8 +420,23 @@ __global__ __launch_bounds__(C::NT, C::OCC) void loss_products_kernel(LossArgs p
                            __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, p.info->unit))),
                            __builtin_amdgcn_readfirstlane(p.info->copied)};
     const int n = p.packing ? info.n : (int)p.rows;
-    if (blockIdx.x < dx_blocks) with_fragments<C>(n, 1, 0, [&](auto c) { loss_dx_tile<decltype(c), DT>(p, info, n, blockIdx.x); });
-    else loss_dw_tile<C, DT>(p, info, n, blockIdx.x - dx_blocks);
+    if (blockIdx.x >= dx_blocks) return loss_dw_tile<C, DT>(p, info, n, blockIdx.x - dx_blocks);
+    const RowTiles<C> rows(n, 1, 0);
+    GemmArgs g{};
+    g.a = p.dz;
+    g.lda = p.lddz;
+    g.b = p.w + (size_t)p.v0 * p.ldw;
+    g.ldb = p.ldw;
+    g.K = p.vn;
+    g.zero = p.zero;
+    g.Mt = rows.Mt;
+    g.Nt = p.dxNt;
+    const uint32_t blocks = g.Mt * g.Nt * p.S;
+    if (blockIdx.x >= blocks) return;
+    const uint32_t q = xcd_chunked(blockIdx.x, blocks), part = q % p.S;
+    uint32_t mb, nb;
+    tile_at(g, q / p.S, mb, nb);
+    rows.take(mb, [&](auto c, int m0) { loss_dx_tile<decltype(c), DT>(p, info, g, n, m0, nb, part); });
 }
 
 }  // namespace mlpc

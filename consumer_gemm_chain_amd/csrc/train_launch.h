@@ -18,27 +18,34 @@ struct LossInfo {
     int copied;             // the products' x is the workspace's: packed, or with zeros in the rows left out
 };
 
-// The fragments of 16 rows per wave with which tiles of 32 fragments' rows take
-// n rows in least time, if each row of tiles has `columns` tiles, dealt to `cus`
-// CUs in rounds (0: among other work), and that time in units of a fragment: 670
-// rows are three tiles of 224.  A tile costs as much as 1.2 fragments more than
-// its products; half of what a last, partial round wastes comes back as the
-// others' higher clocks (1000 x 12288 x 50001 with a third of the rows left out,
-// z alone: 256 rows per tile 1030 us, 160 rows, which fill the rounds best, 1225,
-// 224 rows 955).
+// How tall tiles, of 5 to 8 fragments of 32 rows, take n rows in least time, if
+// each row of tiles has `columns` tiles, dealt to `cus` CUs in rounds (0: among
+// other work): 670 rows are three tiles of seven fragments, 700 one of eight and
+// two of seven.  A tile costs as much as 1.2 fragments more than its products; half
+// of what a last, partial round wastes comes back as the others' higher clocks
+// (1000 x 12288 x 50001 with a third of the rows left out, z alone: 256 rows per
+// tile 1030 us, 160 rows, which fill the rounds best, 1225, 224 rows 955).  With
+// one height for all of a call's tiles 8192 -> 32000 bf16 took, z and gradient, 2300
+// rows 1090 and 3065 us, with these 985 and 2975; 3686 rows 1562 and 4584, 1495 and
+// 4488; 330 rows 224 and 693, 220 and 690.
 struct Fragments {
-    int count;
-    float cost, whole;          // of these, and of 8
+    int tiles, base, extra;     // the first `extra` tiles have base + 1 fragments
+    float cost, whole;          // in units of a fragment, and that of tiles of 8
 };
 
 __host__ __device__ inline Fragments fragments_for(int n, uint32_t columns, uint32_t cus) {
+    const int all = (n + 31) / 32, least = (all + 7) / 8, most = (all + 4) / 5;
     Fragments best{};
-    for (int f = 8; f >= 5; --f) {
-        const uint32_t tiles = (uint32_t)((n + 32 * f - 1) / (32 * f)) * columns;
+    for (int k = least; k <= most && k < least + 4; ++k) {
+        const uint32_t tiles = (uint32_t)k * columns;
         const float rounds = cus ? 0.5f * ((float)((tiles + cus - 1) / cus) + (float)tiles / (float)cus) : (float)tiles;
-        const float c = rounds * (f + 1.2f);
-        if (f == 8) best = Fragments{8, c, c};
-        else if (c < best.cost) best = Fragments{f, c, best.whole};
+        const float height = (float)all / (float)k, c = rounds * ((height < 5.f ? 5.f : height) + 1.2f);
+        if (k == least) best.whole = rounds * 9.2f;
+        if (k > least && c >= best.cost) continue;
+        best.cost = c;
+        best.tiles = k;
+        best.base = all / k < 5 ? 5 : all / k;
+        best.extra = all - k * best.base < 0 ? 0 : all - k * best.base;
     }
     return best;
 }
