@@ -285,8 +285,8 @@ __device__ __forceinline__ void loss_logits_tile(const LossArgs& p, const GemmAr
 // z = x W^T, and from the accumulators either a maximum and a sum per row and tile
 // (softmax_epilogue; 8 bytes for BN logits) or dz in 16 bits (dz_epilogue): the
 // logits themselves never leave the registers.  48 x 8192 x 32000 takes 89 us, 6.0
-// TB/s of W.  3700 x 8192 x 128000 takes 6.1 to 6.4 ms (1.2 to 1.27 PFLOP/s, matrix
-// cores 70% busy at 1.75 GHz), most of it the tiles' way from L2 to LDS: 64 KB per
+// TB/s of W.  3700 x 8192 x 128000 takes 6.14 ms (1.26 PFLOP/s, matrix cores
+// 67% busy at 1.77 GHz), most of it the tiles' way from L2 to LDS: 64 KB per
 // stage take 0.84 us where 112 CUs ask for them, 1.29 for 224, 1.56 for 256 (11
 // TB/s over all), and 1.42 with an x and a W of zeros, whose products cost no power.
 // Rows further apart, requests spread over both halves of a stage and lines brought
@@ -403,8 +403,8 @@ __device__ __forceinline__ void loss_dw_tile(const LossArgs& p, const LossInfo& 
 // the XCDs that the others are dealt to) dz W, the others dz^T x.  dx has few
 // tiles with a long reduction, dW many with a short one, which fill the round
 // that dx's leave open (667 x 12288 x 50001: one launch 1655 us, dx alone 1038, dW
-// alone 925).  3700 x 8192 x 32000 takes 2.95 ms (1.31 PFLOP/s, matrix cores 70%
-// busy at 1.81 GHz); 667 x 12288 x 50001 reaches 0.96 PFLOP/s: dW's tiles
+// alone 925).  3700 x 8192 x 32000 takes 2.95 ms (1.31 PFLOP/s, matrix cores 68%
+// busy at 1.84 GHz); 667 x 12288 x 50001 reaches 0.98 PFLOP/s: dW's tiles
 // have ten slabs each between filling the ring and storing 128 KB.
 // With a few rows W's second reading and dW's writing bound it (48 x 8192 x 32000:
 // 262 us for 1.05 GB; a kernel of its own for dW of up to 128 rows, x in registers
