@@ -36,6 +36,7 @@ struct Fragments {
 __host__ __device__ inline Fragments fragments_for(int n, uint32_t columns, uint32_t cus) {
     const int all = (n + 31) / 32, least = (all + 7) / 8, most = (all + 4) / 5;
     Fragments best{};
+    if (all == 0) return best;      // every row is left out: no tile, and no number of them to divide by
     for (int k = least; k <= most && k < least + 4; ++k) {
         const uint32_t tiles = (uint32_t)k * columns;
         const float rounds = cus ? 0.5f * ((float)((tiles + cus - 1) / cus) + (float)tiles / (float)cus) : (float)tiles;
