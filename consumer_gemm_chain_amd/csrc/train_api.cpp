@@ -496,8 +496,9 @@ mlp_adamw_t mlp_adamw_create(int dtype, int bits, double beta1, double beta2, do
         fail(MLP_EINVAL, "beta1 and beta2 must be in [0, 1), got %g and %g", beta1, beta2);
         return nullptr;
     }
-    if (!(eps >= 0.0 && eps < INFINITY)) {
-        fail(MLP_EINVAL, "eps must be finite and not negative, got %g", eps);
+    // (a smaller one has no reciprocal in fp32: elements whose v is 0 would become NaN)
+    if (!(eps == 0.0 || (eps >= 0x1p-126 && eps < INFINITY))) {
+        fail(MLP_EINVAL, "eps must be finite and either 0 or at least 2^-126, got %g", eps);
         return nullptr;
     }
     mlp_adamw* h = new (std::nothrow) mlp_adamw();

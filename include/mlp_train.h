@@ -146,8 +146,9 @@ typedef struct {
 } mlp_adamw_tensor;
 
 /* Create an AdamW optimizer of weights of `dtype` with states of `bits` (32
- * or 8) bits on the current HIP device.  0 <= beta1, beta2 < 1, eps finite and
- * >= 0. */
+ * or 8) bits on the current HIP device.  0 <= beta1, beta2 < 1, eps 0 or at
+ * least 2^-126 (a normal fp32 number) and finite.  With an eps of 0 an element
+ * whose m and v are 0 becomes NaN, as the formula's 0 / 0. */
 mlp_adamw_t mlp_adamw_create(int dtype, int bits, double beta1, double beta2, double eps, uint32_t seed);
 
 /* One step of `count` tensors with grads[i] (storage type) of tensors[i].  t (int64, one element, 8-byte aligned, on the
