@@ -2,6 +2,7 @@
 // workspace ownership and launches.
 #include <hip/hip_runtime.h>
 
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -450,7 +451,9 @@ int mlp_grad_norm_forward(mlp_grad_norm_t h, int64_t count, const int64_t* sizes
     if (rc == MLP_OK) rc = check_vector("norm", norm, 4);
     if (rc != MLP_OK) return rc;
     if (misaligned(scale, 4)) return fail(MLP_EINVAL, "scale must be 4-byte aligned");
-    if (!(fabs(unscale) < INFINITY) || unscale == 0.0) return fail(MLP_EINVAL, "unscale must be finite and not zero, got %g", unscale);
+    // (beyond fp32's normal numbers the scale would be infinite or 0 beside a finite norm)
+    if (!(fabs(unscale) >= FLT_MIN && fabs(unscale) <= FLT_MAX))
+        return fail(MLP_EINVAL, "the magnitude of unscale must be a normal fp32 number, got %g", unscale);
     if (!(max_norm > 0.0)) return fail(MLP_EINVAL, "max_norm must be positive, got %g", max_norm);
     if (chunks > INT32_MAX) return fail(MLP_EINVAL, "the tensors have more than 2^44 elements");
     DeviceGuard g(h->device);

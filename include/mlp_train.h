@@ -126,8 +126,9 @@ mlp_grad_norm_t mlp_grad_norm_create(int dtype);
 /* The norm of `count` tensors together, grads[i] of 0 <= sizes[i] < 2^34
  * elements (NULL if none): norm (fp32, one element) and, unless NULL, scale (fp32, one
  * element), the factor that takes the gradients' loss scale out (`unscale`,
- * finite and not zero; 1: none) and clips their norm to max_norm (> 0,
- * infinity: no clipping).  The arrays are read before the call returns. */
+ * its magnitude within fp32's normal numbers; 1: none) and clips their norm to
+ * max_norm (> 0, infinity: no clipping).  The arrays are read before the call
+ * returns. */
 int mlp_grad_norm_forward(mlp_grad_norm_t h, int64_t count, const int64_t* sizes, const void* const* grads,
                           double unscale, double max_norm, float* norm, float* scale, void* hip_stream);
 
