@@ -239,15 +239,16 @@ __device__ __forceinline__ void adamw_chunk(const AdamTable& a, const AdamStep& 
             v[4 * k] = v0[0], v[4 * k + 1] = v0[1], v[4 * k + 2] = v1[0], v[4 * k + 3] = v1[1];
         }
     }
-    const float keep = (float)(1.0 - q.lr * a.decay[i]);
+    const float decay = (float)(q.lr * a.decay[i]);
     auto update = [&](auto root) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const float s = g[k] * q.scale;
             m[k] = m[k] * b1 + s * a.rest1;
             v[k] = v[k] * b2 + (s * s) * a.rest2;
-            // (hardware root and reciprocal: ulps of the step's change)
-            w[k] = w[k] * keep - q.size * (m[k] * __builtin_amdgcn_rcpf(root(v[k]) * q.root + a.eps));
+            // (hardware root and reciprocal: ulps of the step's change; the decay is part of the change, because a factor of
+            // 1 - 1e-6 rounded to fp32 decays by 1.3% more than that at every step)
+            w[k] -= __builtin_fmaf(decay, w[k], q.size * (m[k] * __builtin_amdgcn_rcpf(root(v[k]) * q.root + a.eps)));
         }
     };
     // the hardware's root takes subnormal v as 0: beside an eps of 2^-39 and more that changes nothing
