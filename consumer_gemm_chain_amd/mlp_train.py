@@ -193,6 +193,15 @@ def _array(kind, code, values, n):
     return (kind * n).from_buffer(values) if n else (kind * 1)()
 
 
+def _check_apart(lists):
+    """Refuse contiguous tensors, given as (name, list) pairs, that share memory: a step writes all of them at once."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name, i)
+                   for name, ts in lists for i, t in enumerate(ts) if t.numel())
+    for (_, end, a, i), (begin, _, b, k) in zip(spans, spans[1:]):
+        if begin < end:
+            raise ValueError(f"{a}[{i}] and {b}[{k}] share memory")
+
+
 class MlpAdamW(_Layer):
     """AdamW over the contiguous tensors `params` of `dtype`, which it updates
     in place, with states of 32 or 8 bits, and with fp32 master weights if
@@ -201,7 +210,8 @@ class MlpAdamW(_Layer):
     `m` and `v` (one tensor per parameter, of its number of elements; float32,
     or of 8 bits float8_e4m3fn and float8_e5m2), `m_scale` and `v_scale`
     (float32, one per 256 elements) and `step` (int64 [1], counted on the
-    device).  `decay`: weight decay, of all or of each.
+    device); none of these may share memory.  `decay`: weight decay, of all or
+    of each.
 
     A step works on the memory that these tensors had here; a parameter that
     has got other memory since is refused.  The attributes `params`, `master`,
@@ -254,8 +264,10 @@ class MlpAdamW(_Layer):
         self.t = torch.zeros(1, dtype=torch.int64, device=torch.device("cuda", self.device)) if step is None else step
         self._t = self._vector("step", self.t, 1, torch.int64)
         # (the memory behind the pointers stays while the optimizer does, whatever becomes of the tensors)
-        lists = (self.params, self.master, self.m, self.v, self.m_scale, self.v_scale, [self.t])
-        self._memory = [t.untyped_storage() for ts in lists if ts for t in ts]
+        lists = [(name, getattr(self, name)) for name in ("params", "master", "m", "v", "m_scale", "v_scale")] + [("step", [self.t])]
+        lists = [(name, ts) for name, ts in lists if ts]
+        _check_apart(lists)
+        self._memory = [t.untyped_storage() for _, ts in lists for t in ts]
         self._params = list(pointers)[:n]
         self._shapes = [p.shape for p in self.params]
         # (what was made here is there for steps on any stream)
