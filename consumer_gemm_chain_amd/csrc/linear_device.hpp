@@ -259,12 +259,6 @@ struct LinTile {
     // not read, so the number of requests in flight at a barrier is fixed.
     template <int DT>
     __device__ __forceinline__ void kloop(f32x4 (&acc)[C::FM][C::FN], int h0, int h1, int tail, const GemmArgs& p) const {
-        fill(h0, h1, tail, p);
-        run<DT>(acc, h0, h1, tail);
-    }
-
-    // Its first requests, and all that follows them.
-    __device__ __forceinline__ void fill(int h0, int h1, int tail, const GemmArgs& p) const {
         static_assert(C::NS > C::SPS, "the tail's stages are requested by the first fill");
 #pragma unroll
         for (int i = 0; i < C::NS; ++i) {
@@ -274,10 +268,6 @@ struct LinTile {
                 static_for<0, C::LPS>([&](auto q) { issue<decltype(q)::value>(h, i); });
             }
         }
-    }
-
-    template <int DT>
-    __device__ __forceinline__ void run(f32x4 (&acc)[C::FM][C::FN], int h0, int h1, int tail) const {
         if (tail >= 0) h0 -= C::SPS;
         LinFrags<C> f, g;
         ring_barrier<C::LPS * (C::NS - 1)>();
@@ -319,17 +309,8 @@ struct LinTile {
     // The slab that ends past K alone (a reduction of fewer than 64).
     template <int DT>
     __device__ __forceinline__ void only_tail(f32x4 (&acc)[C::FM][C::FN], int slab, const GemmArgs& p) const {
-        fill_tail(slab, p);
-        run_tail<DT>(acc);
-    }
-
-    __device__ __forceinline__ void fill_tail(int slab, const GemmArgs& p) const {
 #pragma unroll
         for (int i = 0; i < C::SPS; ++i) issue_tail(slab * C::SPS + i, i, p);
-    }
-
-    template <int DT>
-    __device__ __forceinline__ void run_tail(f32x4 (&acc)[C::FM][C::FN]) const {
         ring_barrier<0>();
         static_for<0, 2>([&](auto s) {
             constexpr int S = decltype(s)::value;
