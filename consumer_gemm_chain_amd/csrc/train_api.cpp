@@ -41,7 +41,7 @@ struct mlp_loss {
 };
 
 struct mlp_grad_norm {
-    int dtype, device, cus;
+    int dtype, device;
     double* part;               // [NORM_PARTS]
     hipStream_t last_stream;
 };
@@ -61,7 +61,6 @@ constexpr size_t SPLIT_BYTES = (size_t)64 << 20;        // of dx's sums in parts
 constexpr int64_t MAX_PRODUCT = (int64_t)1 << 38;
 constexpr int PIECE = 256;                              // columns of a piece: a multiple of this
 constexpr int MIN_TILE = 128;                           // columns of the narrowest tile
-
 
 uint32_t up_div(int64_t a, int64_t b) { return (uint32_t)((a + b - 1) / b); }
 
