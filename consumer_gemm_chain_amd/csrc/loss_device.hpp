@@ -215,8 +215,8 @@ struct RowsOfTile {
     }
 };
 
-// The products' x where a row is left out (its x may hold anything): the
-// workgroups share the copy.
+// dW's x where a row is left out (its x may hold anything): the workgroups
+// share the copy.
 __device__ __forceinline__ void copy_rows(const LossArgs& p, int threads) {
     const int per_row = p.H / 8, chunks = (int)p.rows * per_row;
     for (int i = blockIdx.x * threads + threadIdx.x; i < chunks; i += gridDim.x * threads) {
@@ -276,7 +276,7 @@ __device__ __forceinline__ void loss_logits_tile(const LossArgs& p, const GemmAr
     if constexpr (GRAD) {
         const bool out = !p.packing && rows.store(p);
         dz_epilogue<C, DT>(acc, p, n, m0, n0);
-        if (out && p.first) copy_rows(p, C::NT);
+        if (out && p.first && p.dw) copy_rows(p, C::NT);
     } else {
         softmax_epilogue<C>(acc, p, n, nb, m0, n0);
     }
