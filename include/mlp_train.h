@@ -24,7 +24,8 @@
  *             v = beta2 v + (1 - beta2) g^2
  *             w = w (1 - lr decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
  *
- * Loss.  A row whose target is negative is left out: its x is not read, its
+ * Loss.  A row whose target is negative is left out: its x may hold anything
+ * (in memory that can be read: where a call's rows fit one tile it is), its
  * loss, lse and dx are 0 and it adds nothing to dW.  A target of V or more
  * gives a loss and an lse of NaN; in the gradient its row is left out.  The
  * logits are never kept: the forward pass holds a maximum and a sum per row
