@@ -295,7 +295,13 @@ __device__ __forceinline__ void adamw_chunk(const AdamTable& a, const AdamStep& 
             const uint32_t r = mix(key + K / 2);
             vc[W] = __builtin_amdgcn_cvt_sr_bf8_f32(unit(v[K]), r << 16, vc[W], B);
             vc[W] = __builtin_amdgcn_cvt_sr_bf8_f32(unit(v[K + 1]), r & 0xffff0000u, vc[W], B + 1);
-            mc[W] = __builtin_amdgcn_cvt_pk_fp8_f32(m[K] * mi, m[K + 1] * mi, mc[W], B != 0);
+            // (m's bits are the ones that its neighbour's v is rounded with: m and v of an element are independent)
+            if (a.chance) {
+                mc[W] = __builtin_amdgcn_cvt_sr_fp8_f32(m[K] * mi, r & 0xffff0000u, mc[W], B);
+                mc[W] = __builtin_amdgcn_cvt_sr_fp8_f32(m[K + 1] * mi, r << 16, mc[W], B + 1);
+            } else {
+                mc[W] = __builtin_amdgcn_cvt_pk_fp8_f32(m[K] * mi, m[K + 1] * mi, mc[W], B != 0);
+            }
         });
         if (!numbers) {
 #pragma unroll

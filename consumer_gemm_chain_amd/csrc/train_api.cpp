@@ -389,6 +389,11 @@ constexpr int64_t MAX_TENSORS = (int64_t)1 << 20;
 // Of a tensor: one workgroup per chunk, and a launch has fewer than 2^32 threads.
 constexpr int64_t MAX_ELEMENTS = (int64_t)1 << 34;
 constexpr uint32_t MAX_CHUNKS = ((uint32_t)1 << 24) - 1;
+// The largest beta1 with which an m of 8 bits is rounded to nearest.  A step
+// without a gradient takes (1 - beta1) m away, and e4m3's half step is up to m / 18:
+// from 17/18 on such an m would stay for good while v falls (0.95: 0.84 of m's norm
+// is left after 400 steps, of which 1e-9 should be; 0.94: 1e-15).
+constexpr double M_NEAREST = 15.0 / 16.0;
 
 int check_count(int64_t count, const void* array) {
     if (count < 0 || count > MAX_TENSORS || (count > 0 && !array))
@@ -549,6 +554,7 @@ int mlp_adamw_step(mlp_adamw_t h, int64_t count, const mlp_adamw_tensor* tensors
     a.beta2 = (float)h->beta2;
     a.rest2 = (float)(1.0 - h->beta2);
     a.eps = (float)h->eps;
+    a.chance = h->beta1 > M_NEAREST;
     a.step = h->step;
     for (int64_t i = 0; i < count && e == hipSuccess; ++i) {
         const mlp_adamw_tensor& q = tensors[i];

@@ -147,6 +147,7 @@ struct AdamTable {
     int count, number;      // number: of the first entry in the call
     uint32_t chunks;
     float beta1, rest1, beta2, rest2, eps;
+    bool chance;            // m in 8 bits is rounded by chance, as v is
     const AdamStep* step;
 };
 

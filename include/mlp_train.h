@@ -48,11 +48,12 @@
  * of 256 elements of a tensor (the last one may be short), each with an fp32
  * scale, a power of two: the smallest one, but at least 2^-126, with which the
  * block's largest magnitude stays within the type (1 for a block of zeros).
- * The step itself takes m and v before they are rounded.  m is rounded to
- * nearest even.  One step moves v by less than half a step of 8 bits, so v is
- * rounded up or down by chance, with a mean of v, and to no less than the
- * smallest number unless it is zero; its random bits are a hash of `seed`, t,
- * the tensor's number in the call and the element's place.  Elements that are
+ * The step itself takes m and v before they are rounded.  One step moves v by
+ * less than half a step of 8 bits, so v is rounded up or down by chance, with a
+ * mean of v, and to no less than the smallest number unless it is zero; its
+ * random bits are a hash of `seed`, t, the tensor's number in the call and the
+ * element's place.  m is rounded to nearest even, but by chance as well with a
+ * beta1 above 15/16, which moves m by as little.  Elements that are
  * not finite are NaN in 8 bits and leave the scale alone.
  *
  * Row counts: any R >= 0 per call up to the handle's max_rows.  With R = 0
