@@ -52,8 +52,9 @@
  * less than half a step of 8 bits, so v is rounded up or down by chance, with a
  * mean of v, and to no less than the smallest number unless it is zero; its
  * random bits are a hash of `seed`, t, the tensor's number in the call and the
- * element's place.  m is rounded to nearest even, but by chance as well with a
- * beta1 above 15/16, which moves m by as little.  Elements that are
+ * element's place.  m is rounded to nearest even, but by chance as well where
+ * a step moves it by as little: with a beta1 above 15/16, and below 2^-6 of its
+ * scale where the nearest is what it was.  Elements that are
  * not finite are NaN in 8 bits and leave the scale alone.
  *
  * Row counts: any R >= 0 per call up to the handle's max_rows.  With R = 0
