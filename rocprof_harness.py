@@ -104,8 +104,8 @@ BLOCK_PASSES = 21     # per case, over three sets of inputs in turn
 CASES = {"block": "operators.py", "train": "more_operators.py"}
 TITLES = {"block": "Block operators", "train": "The training step's operators"}
 NOTES = {
-    "block": """`linear<BM, BN, waves M, waves N, stages, stage depth, waves per SIMD, type (0 fp16, 1 bf16), pass (0 x W, 1 dz W^T,
-2 x^T dz)>`; `linear_both<...>`: dz W^T and x^T dz in one launch; `norm_forward<type, threads per row, chunks, ragged>`,
+    "block": """`linear<BM, BN, waves M, waves N, stages, stage depth, waves per SIMD, fragments read early, type (0 fp16, 1 bf16),
+pass (0 x W, 1 dz W^T, 2 x^T dz)>`; `linear_both<...>`: dz W^T and x^T dz in one launch; `norm_forward<type, threads per row, chunks, ragged>`,
 `norm_backward<type, threads, chunks, ragged, single workgroup>`; `dz<type, activation, columns>`.
 """,
     "train": """`loss_logits<BM, BN, waves M, waves N, stages, stage depth, waves per SIMD, fragments read early, type (0 fp16, 1 bf16),
