@@ -409,7 +409,7 @@ __device__ __forceinline__ void loss_dw_tile(const LossArgs& p, const LossInfo& 
 // With a few rows W's second reading and dW's writing bound it (48 x 8192 x 32000:
 // 262 us for 1.05 GB; a kernel of its own for dW of up to 128 rows, x in registers
 // and dz turned around in LDS, took 251 us for a call without dx, which 128 x 128
-// tiles reach as well (245), and 392 with it: dropped).
+// tiles reach as well (245 to 251), and 392 with it: dropped).
 template <class C, int DT>
 __global__ __launch_bounds__(C::NT, C::OCC) void loss_products_kernel(LossArgs p, uint32_t dx_blocks) {
     // Loaded once, ahead: a tile that asks for the unit before its stores waits for
