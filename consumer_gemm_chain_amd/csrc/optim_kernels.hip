@@ -35,9 +35,10 @@ __device__ __forceinline__ double wave_sum64(double v) {
 
 // A workgroup's share of the launch's chunks, neighbours, to its partial sum.
 // Reading the gradients bounds it: 302 MB of bf16 in 54 us (5.6 TB/s; 50 us where
-// part of them is still in the Infinity Cache), 101 MB of fp16 in 144 tensors in 27.  A square of 16 bits is exact in 64, and gradients
-// of 1e-25 or 1e30 neither vanish nor overflow, so no scaling pass is needed; the
-// products in 64 bits stay hidden behind the loads.
+// part of them is still in the Infinity Cache), 101 MB of fp16 in 144 tensors in 27.
+// A square of 16 bits is exact in 64, and gradients of 1e-25 or 1e30 neither vanish
+// nor overflow, so no scaling pass is needed; the products in 64 bits stay hidden
+// behind the loads.
 template <int DT>
 __global__ __launch_bounds__(ONT) void norm_sum_kernel(NormTable a) {
     __shared__ double s[ONT / 64];
@@ -303,7 +304,8 @@ __device__ __forceinline__ void adamw_chunk(const AdamTable& a, const AdamStep& 
         // Where a step moves m by less than half a code, rounding to nearest would leave it
         // as it was for good: with a large beta1 (chance) anywhere, with any below the
         // normal numbers (of codes up to 4 a beta1 of 0.9 takes less than half of one).
-        // There m is rounded by chance, with the random bits of its neighbour's v.
+        // There m is rounded by chance, with the random bits of its neighbour's v.  (An m
+        // that was 0 stays 0 below half a code, to nearest: that moves no weight.)
         // (Off the common path, and with m's codes read again: kept, they cost a wave of
         // seven per SIMD, and 50 million elements in 144 tensors took 112 us, not 107.)
         if (a.chance || __any(low < bits_of(0x1p-6f * ms) - 1u)) {

@@ -54,8 +54,8 @@
  * random bits are a hash of `seed`, t, the tensor's number in the call and the
  * element's place.  m is rounded to nearest even, but by chance as well where
  * a step moves it by as little: with a beta1 above 15/16, and below 2^-6 of its
- * scale where the nearest is what it was.  Elements that are
- * not finite are NaN in 8 bits and leave the scale alone.
+ * scale where the nearest is what it was, but for 0.  Elements that are not
+ * finite are NaN in 8 bits and leave the scale alone.
  *
  * Row counts: any R >= 0 per call up to the handle's max_rows.  With R = 0
  * nothing is read, operands of R rows may be NULL and dW is zero.
